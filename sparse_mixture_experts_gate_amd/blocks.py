@@ -1,0 +1,207 @@
+"""Objects over the operators of ``include/dsmoe_ops.h``: layer norm, linear
+maps grouped by expert, and the orthogonalized update. They check shapes,
+allocate outputs and keep the workspace; all arithmetic is the library's."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _lib as L
+from . import _ops as O
+
+_DT = {torch.float32: L.MOE_DT_F32, torch.bfloat16: L.MOE_DT_BF16}
+
+
+def _on(stream):
+    """Allocate on the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, d: int) -> int:
+    """Row stride of a row matrix [n, d], checked."""
+    if t.dtype != dtype or t.shape != (n, d):
+        raise ValueError(f"{name}: expected {dtype} [{n}, {d}], got {t.dtype} {list(t.shape)}")
+    if d > 1 and n and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    if n <= 1:
+        return d
+    if t.stride(0) < d:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {d})")
+    return t.stride(0)
+
+
+def _vector(t, name: str, dtype: torch.dtype, n: int) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected contiguous {dtype} [{n}], got {t.dtype} "
+                         f"{list(t.shape)}")
+
+
+class _Workspace:
+    """One buffer per stream, grown as calls need it."""
+
+    def __init__(self):
+        self._bufs = {}
+
+    def get(self, need: int, device, stream) -> torch.Tensor:
+        key = (device, O._stream(stream))
+        buf = self._bufs.get(key)
+        if buf is None or buf.numel() < need:
+            buf = self._bufs[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        return buf
+
+
+class LayerNorm:
+    """Layer norm over the last dimension with fp32 weight and bias (either
+    may be None), for bf16 or fp32 rows (moe_layernorm_forward)."""
+
+    def __init__(self, weight: torch.Tensor | None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-5):
+        self.weight, self.bias, self.eps = weight, bias, eps
+        self._ws = _Workspace()
+
+    def _desc(self, x: torch.Tensor) -> O.MoeNormDesc:
+        if x.dim() != 2 or x.dtype not in _DT:
+            raise ValueError(f"x: expected bf16 or fp32 [n, d], got {x.dtype} {list(x.shape)}")
+        n, d = x.shape
+        _vector(self.weight, "weight", torch.float32, d)
+        _vector(self.bias, "bias", torch.float32, d)
+        return O.MoeNormDesc(n=n, d=d, dtype=_DT[x.dtype], eps=self.eps,
+                             ld_x=_rows(x, "x", x.dtype, n, d))
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
+                stream=None) -> dict:
+        """y = norm(x + residual) with the row statistics, and the sum itself
+        when there is a residual: {"y", "mean", "rstd", "sum"}; "sum" is what
+        the backward takes as x (x itself without a residual)."""
+        desc = self._desc(x)
+        n, d = x.shape
+        if residual is not None:
+            desc.ld_r = _rows(residual, "residual", x.dtype, n, d)
+        with _on(stream):
+            y = torch.empty(n, d, dtype=x.dtype, device=x.device)
+            total = torch.empty_like(y) if residual is not None else None
+            mean = torch.empty(n, dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        O.moe_layernorm_forward(desc, x, residual, self.weight, self.bias, y, total, mean, rstd,
+                                stream)
+        return {"y": y, "mean": mean, "rstd": rstd, "sum": x if residual is None else total}
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                 dresidual: torch.Tensor | None = None, stream=None) -> dict:
+        """{"dx", "dweight", "dbias"} for the forward's normalized rows x
+        (its "sum"); dresidual is added to dx."""
+        desc = self._desc(x)
+        n, d = x.shape
+        desc.ld_y = _rows(dy, "dy", x.dtype, n, d)
+        if dresidual is not None:
+            desc.ld_r = _rows(dresidual, "dresidual", x.dtype, n, d)
+        _vector(mean, "mean", torch.float32, n)
+        _vector(rstd, "rstd", torch.float32, n)
+        with _on(stream):
+            dx = torch.empty(n, d, dtype=x.dtype, device=x.device)
+            dw = torch.empty(d, dtype=torch.float32, device=x.device)
+            db = torch.empty_like(dw)
+            ws = self._ws.get(O.moe_layernorm_backward_workspace_size(desc), x.device, stream)
+        O.moe_layernorm_backward(desc, dy, x, self.weight, mean, rstd, dresidual, dx, dw, db, ws,
+                                 stream)
+        return {"dx": dx, "dweight": dw, "dbias": db}
+
+
+class GroupedLinear:
+    """One linear map per expert, weight [groups, n, k] bf16, over rows sorted
+    by expert (``moe_permute``'s order) with ``offsets`` [groups + 1] int32 on
+    the device: group g owns rows offsets[g] .. offsets[g + 1] - 1. Rows
+    outside the groups are not written."""
+
+    def __init__(self, weight: torch.Tensor):
+        if weight.dim() != 3 or weight.dtype != torch.bfloat16 or not weight.is_contiguous():
+            raise ValueError(f"weight: expected contiguous bf16 [groups, n, k], got "
+                             f"{weight.dtype} {list(weight.shape)}")
+        self.weight = weight
+
+    @staticmethod
+    def _desc(rows, groups, n, k, offsets, out_dtype=torch.float32) -> O.MoeGroupedDesc:
+        _vector(offsets, "offsets", torch.int32, groups + 1)
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype: bf16 or fp32, got {out_dtype}")
+        return O.MoeGroupedDesc(rows=rows, n_groups=groups, n=n, k=k, out_dtype=_DT[out_dtype])
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor, out_dtype=torch.bfloat16,
+                stream=None) -> torch.Tensor:
+        """y [rows, n] = x W_g^T (moe_grouped_gemm)."""
+        G, n, k = self.weight.shape
+        desc = self._desc(x.shape[0], G, n, k, offsets, out_dtype)
+        desc.ld_k = _rows(x, "x", torch.bfloat16, x.shape[0], k)
+        with _on(stream):
+            y = torch.empty(x.shape[0], n, dtype=out_dtype, device=x.device)
+        O.moe_grouped_gemm(desc, x, self.weight, offsets, y, stream)
+        return y
+
+    def input_grad(self, dy: torch.Tensor, offsets: torch.Tensor, out_dtype=torch.bfloat16,
+                   stream=None) -> torch.Tensor:
+        """dx [rows, k] = dy W_g (moe_grouped_gemm_dgrad)."""
+        G, n, k = self.weight.shape
+        desc = self._desc(dy.shape[0], G, n, k, offsets, out_dtype)
+        desc.ld_n = _rows(dy, "dy", torch.bfloat16, dy.shape[0], n)
+        with _on(stream):
+            dx = torch.empty(dy.shape[0], k, dtype=out_dtype, device=dy.device)
+        O.moe_grouped_gemm_dgrad(desc, dy, self.weight, offsets, dx, stream)
+        return dx
+
+    @staticmethod
+    def weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                    into: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """dw [groups, n, k] fp32 = dy_g^T x_g (moe_grouped_gemm_wgrad), added
+        to ``into`` when given (gradient accumulation)."""
+        G = offsets.shape[0] - 1
+        rows, n, k = dy.shape[0], dy.shape[1], x.shape[1]
+        desc = GroupedLinear._desc(rows, G, n, k, offsets)
+        desc.ld_n = _rows(dy, "dy", torch.bfloat16, rows, n)
+        desc.ld_k = _rows(x, "x", torch.bfloat16, rows, k)
+        desc.accumulate = into is not None
+        if into is None:
+            with _on(stream):
+                into = torch.empty(G, n, k, dtype=torch.float32, device=dy.device)
+        elif into.dtype != torch.float32 or into.shape != (G, n, k) or not into.is_contiguous():
+            raise ValueError(f"into: expected contiguous fp32 [{G}, {n}, {k}], got {into.dtype} "
+                             f"{list(into.shape)}")
+        O.moe_grouped_gemm_wgrad(desc, dy, x, offsets, into, stream)
+        return into
+
+
+class Muon:
+    """Momentum and Newton-Schulz orthogonalization of weight updates
+    (moe_orthogonalize) for matrices [..., rows, cols], all at once."""
+
+    def __init__(self, momentum: float = 0.95, nesterov: bool = True, steps: int = 5):
+        self.momentum, self.nesterov, self.steps = momentum, nesterov, steps
+        self._ws = _Workspace()
+
+    def direction(self, grad: torch.Tensor, momentum: torch.Tensor | None = None,
+                  out_momentum: torch.Tensor | None = None, stream=None) -> tuple:
+        """(out, momentum'): the orthogonalized direction in bf16 and the new
+        fp32 momentum, written to ``out_momentum`` (which may be
+        ``momentum``). Without momentum: (out, None)."""
+        if grad.dim() < 2 or grad.dtype not in _DT or not grad.is_contiguous():
+            raise ValueError(f"grad: expected contiguous bf16 or fp32 [..., rows, cols], got "
+                             f"{grad.dtype} {list(grad.shape)}")
+        rows, cols = grad.shape[-2:]
+        for t, name in ((momentum, "momentum"), (out_momentum, "out_momentum")):
+            if t is not None and (t.dtype != torch.float32 or t.shape != grad.shape
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous fp32 {list(grad.shape)}, got "
+                                 f"{t.dtype} {list(t.shape)}")
+        if momentum is None and out_momentum is not None:
+            raise ValueError("out_momentum without momentum")
+        desc = O.MoeOrthDesc(n_mats=grad.numel() // (rows * cols) if rows * cols else 0, rows=rows,
+                             cols=cols, grad_dtype=_DT[grad.dtype], steps=self.steps,
+                             momentum=self.momentum, nesterov=int(self.nesterov))
+        need = O.moe_orthogonalize_workspace_size(desc)
+        with _on(stream):
+            out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
+            if momentum is not None and out_momentum is None:
+                out_momentum = torch.empty_like(momentum)
+            ws = self._ws.get(need, grad.device, stream)
+        O.moe_orthogonalize(desc, grad, momentum, out_momentum, out, ws, stream)
+        return out, out_momentum

@@ -32,7 +32,8 @@ NO_CONTRACT = {"router.hip", "elementwise.hip", "balance.hip", "backward_fp8.hip
 # which serialized the MFMAs of the decode tiles behind the copies out
 MFMA_VGPR = {"gemm_fp8.hip", "backward_fp8.hip"}
 SOURCES = ["dsmoe_api.cpp", "router.hip", "permute.hip", "gemm_bf16.hip", "gemm_f32.hip",
-           "gemm_fp8.hip", "elementwise.hip", "backward.hip", "balance.hip", "backward_fp8.hip"]
+           "gemm_fp8.hip", "elementwise.hip", "backward.hip", "balance.hip", "backward_fp8.hip",
+           "ops_api.cpp", "norm.hip", "grouped.hip", "orth.hip"]
 
 
 def _compile(src: str) -> str:

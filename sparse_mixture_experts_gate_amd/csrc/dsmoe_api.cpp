@@ -12,19 +12,14 @@
 #include <hip/hip_runtime.h>
 
 #include "dsmoe.h"
+#include "api_common.h"
 #include "internal.h"
 
 using namespace dsmoe;
 
-namespace {
+namespace dsmoe {
 
 thread_local std::string g_last_error;
-thread_local hipEvent_t g_prof[6] = {};
-thread_local bool g_prof_on = false;
-
-hipError_t prof_record(int i, hipStream_t s) {
-  return g_prof_on ? hipEventRecord(g_prof[i], s) : hipSuccess;
-}
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[512];
@@ -36,17 +31,16 @@ moe_status fail(moe_status st, const char* fmt, ...) {
   return st;
 }
 
-moe_status hip_fail(hipError_t e, const char* what) {
-  return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}  // namespace dsmoe
+
+namespace {
+
+thread_local hipEvent_t g_prof[6] = {};
+thread_local bool g_prof_on = false;
+
+hipError_t prof_record(int i, hipStream_t s) {
+  return g_prof_on ? hipEventRecord(g_prof[i], s) : hipSuccess;
 }
-
-#define HIP_TRY(expr, what)                     \
-  do {                                          \
-    hipError_t _e = (expr);                     \
-    if (_e != hipSuccess) return hip_fail(_e, what); \
-  } while (0)
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 moe_status validate_desc(const moe_layer_desc* d) {
   if (!d) return fail(MOE_ERR_INVALID_ARGUMENT, "desc is NULL");
@@ -110,17 +104,6 @@ moe_status validate_desc(const moe_layer_desc* d) {
     return fail(MOE_ERR_UNSUPPORTED, "E*3*d*2 must be < 2^31 bytes");
   return MOE_OK;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-struct Carver {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    const size_t o = off;
-    off = align256(off + bytes);
-    return o;
-  }
-};
 
 int io_bytes(const moe_layer_desc* d) { return d->act_dtype == MOE_DT_F32 ? 4 : 2; }
 int h_bytes(const moe_layer_desc* d) {
@@ -191,11 +174,6 @@ FwdLayout fwd_layout(const moe_layer_desc* d) {
   L.yshared = c.take(d->shared_inter > 0 ? size_t(T) * d->d * io_bytes(d) : 0);
   L.bytes = c.off;
   return L;
-}
-
-template <class T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
 moe_status check_ptrs(std::initializer_list<std::pair<const void*, const char*>> req) {

@@ -1,0 +1,316 @@
+// Core of the 16-bit matrix products of the expert operators (bf16 or fp16
+// operands, fp32 accumulation): tile shapes, one tile's operand streams and
+// the two k-loops that run a workgroup's tiles.
+//
+// An operand is k-contiguous ([M, K] rows, the contraction along a row) or
+// k-major ([K, M] rows, a k-step is 64 consecutive rows). Both go from memory
+// straight into LDS (16-byte LDS-DMA loads) in the layouts of
+// gemm_bf16_core.h: 128-byte rows with XOR-swizzled chunks, or 64 k rows read
+// back by transpose reads.
+#pragma once
+
+#include <type_traits>
+
+#include "gemm_bf16_core.h"
+
+namespace dsmoe {
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// Operand types of the matrix cores; fragments travel as bf16x8_t (16 bytes).
+struct TypeBf16 {
+  __device__ static f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+struct TypeF16 {
+  __device__ static f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  }
+};
+
+// One tile's operands. `tail` masks (0, or the sign bit that sends an offset
+// out of range) apply in the last k-step to chunks past the contraction of a
+// k-contiguous operand. A k-major operand's resource is moved forward by
+// `step` bytes every k-step (64-bit base: a group's rows may exceed 2^31
+// bytes), with `left` bytes from it to the operand's end; rows past the end
+// read as zeros in hardware.
+template <class C>
+struct Ops16 {
+  i32x4_t ra, rb;
+  uint32_t ao[C::A_LOADS], bo[C::B_LOADS];
+  uint32_t tail_a, tail_b;
+  uint64_t base_a, base_b;  // k-major only
+  int64_t left_a, left_b;
+  uint32_t step_a, step_b;
+  int nk;
+};
+
+__device__ __forceinline__ uint32_t clamp_bytes(int64_t n) {
+  return static_cast<uint32_t>(n < 0 ? 0 : n < 0x7fffffff ? n : 0x7fffffff);
+}
+
+// Rows of a k-contiguous operand: row r of the tile at base + r * ld_bytes,
+// `rows` of them exist; K elements along a row.
+template <class C, int LOADS>
+__device__ __forceinline__ void kcontig_operand(i32x4_t& rs, uint32_t (&o)[LOADS], uint32_t& tail,
+                                                const void* base, int rows, uint32_t ld_bytes,
+                                                int64_t bytes, int K) {
+  const int r0 = threadIdx.x >> 3, ch = threadIdx.x & 7;
+  static_assert(C::RPP % 16 == 0, "a thread's logical chunk is the same in every pass");
+#pragma unroll
+  for (int p = 0; p < LOADS; ++p) {
+    const int r = r0 + p * C::RPP;
+    o[p] = r < rows ? static_cast<uint32_t>(r) * ld_bytes : kInvalidRow;
+  }
+  swizzle_rows<C>(o);
+  const int chunk = ch ^ ((r0 >> 1) & 7);
+  tail = ((K - 1) / BK * BK + chunk * 8 < K) ? 0u : kInvalidRow;
+  rs = rsrc4(base, clamp_bytes(bytes));
+}
+
+// Columns col0 .. of a k-major operand whose first contraction row is at
+// `base`; `bytes` from there to the end of its last row.
+template <class C, int W, int LOADS>
+__device__ __forceinline__ void kmajor_operand(i32x4_t& rs, uint32_t (&o)[LOADS], uint64_t& b,
+                                               int64_t& left, uint32_t& step, const void* base,
+                                               int col0, uint32_t ld_bytes, int64_t bytes) {
+  kmajor_offsets<W, LOADS, C::NT>(o, col0, ld_bytes);
+  b = reinterpret_cast<uint64_t>(base);
+  left = bytes;
+  step = BK * ld_bytes;
+  rs = rsrc4(base, clamp_bytes(bytes));
+}
+
+// The issue side: walks the k-steps of a workgroup's tiles (first, first +
+// nb, ... below total) and loads them into ring stages. Past the last step it
+// loads that step again into stages nobody reads.
+template <class C, bool AKM, bool BKM, class NextOps>
+struct Loader {
+  Ops16<C> op;
+  NextOps& next_ops;
+  uint32_t lds0;
+  int ti, nb, total, ki, wave;
+  bool more;
+  static constexpr int NL = C::A_LOADS + C::B_LOADS;
+
+  __device__ Loader(NextOps& n, uint32_t l0, int first, int nb_, int total_, int wave_)
+      : next_ops(n), lds0(l0), ti(first), nb(nb_), total(total_), ki(0), wave(wave_), more(true) {
+    next_ops(ti, op);
+  }
+  // load i of NL of the current k-step into stage st
+  __device__ __forceinline__ void load(int st, int i) {
+    const uint32_t base =
+        __builtin_amdgcn_readfirstlane(lds0 + (st * C::STAGE + wave * 8 * BK) * 2);
+    const uint32_t kn = static_cast<uint32_t>(ki) * (BK * 2);
+    const bool last = ki == op.nk - 1;
+    if (i < C::A_LOADS) {
+      const uint32_t v = AKM ? op.ao[i] : ((op.ao[i] + kn) | (last ? op.tail_a : 0u));
+      dma16(op.ra, v, base + i * C::RPP * BK * 2);
+    } else {
+      const int j = i - C::A_LOADS;
+      const uint32_t v = BKM ? op.bo[j] : ((op.bo[j] + kn) | (last ? op.tail_b : 0u));
+      const uint32_t at = base + C::BM * BK * 2 + j * C::RPP * BK * 2;
+      if constexpr (C::B_NT)
+        dma16_nt(op.rb, v, at);
+      else
+        dma16(op.rb, v, at);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if (!more) return;
+    if (++ki < op.nk) {
+      if constexpr (AKM) {
+        op.base_a += op.step_a;
+        op.left_a -= op.step_a;
+        op.ra = rsrc4(reinterpret_cast<const void*>(op.base_a), clamp_bytes(op.left_a));
+      }
+      if constexpr (BKM) {
+        op.base_b += op.step_b;
+        op.left_b -= op.step_b;
+        op.rb = rsrc4(reinterpret_cast<const void*>(op.base_b), clamp_bytes(op.left_b));
+      }
+      return;
+    }
+    ki = 0;
+    ti += nb;
+    if (ti < total) {
+      next_ops(ti, op);
+    } else {
+      more = false;
+      ki = op.nk - 1;
+    }
+  }
+};
+
+// Fragment reads of sub-step kk (16 k) of a stage.
+template <class C, bool AKM>
+__device__ __forceinline__ bf16x8_t frag_a(const uint16_t* lds, int st, int row, int kk, int lane) {
+  const uint16_t* s = lds + st * C::STAGE;
+  if constexpr (AKM)
+    return frag_kmajor<C::BM>(lds_addr(s), row, kk * 16, lane);
+  else
+    return *reinterpret_cast<const bf16x8_t*>(s + lds_off(row + (lane & 31), kk * 2 + (lane >> 5)));
+}
+template <class C, bool BKM>
+__device__ __forceinline__ bf16x8_t frag_b(const uint16_t* lds, int st, int row, int kk, int lane) {
+  const uint16_t* s = lds + st * C::STAGE + C::BM * BK;
+  if constexpr (BKM)
+    return frag_kmajor<C::BN>(lds_addr(s), row, kk * 16, lane);
+  else
+    return *reinterpret_cast<const bf16x8_t*>(s + lds_off(row + (lane & 31), kk * 2 + (lane >> 5)));
+}
+
+// acc (+)= the product of two fragments. SWAP: the B fragment goes first and
+// acc holds the transposed tile (lane l: row l % 32 of A's side, four runs of
+// four adjacent columns); without it lane l holds column l % 32 and rows
+// acc_row(l, r).
+template <class T, bool SWAP>
+__device__ __forceinline__ f32x16_t mma16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return SWAP ? T::mfma(b, a, c) : T::mfma(a, b, c);
+}
+
+// Ring loop for small tiles: NST stages, loads NST - 1 k-steps ahead, the
+// fragments of sub-step kk + 1 read between the MFMAs of sub-step kk, one
+// barrier per k-step (before its last sub-step, whose fragments are already
+// in registers).
+template <class C, class T, bool AKM, bool BKM, bool SWAP, class NextOps, class Epilogue>
+__device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, int total,
+                                            NextOps&& next_ops, Epilogue&& epilogue) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  constexpr int NST = C::NST, NL = C::A_LOADS + C::B_LOADS, INFLIGHT = NL * (NST - 2);
+  constexpr int NR = C::MI + C::NJ, NM = C::MI * C::NJ;
+  static_assert(INFLIGHT <= 63, "vmcnt range");
+  Loader<C, AKM, BKM, std::remove_reference_t<NextOps>> ld(next_ops, lds_addr(lds), first, nb,
+                                                            total, wave);
+  bf16x8_t af[2][C::MI], bfr[2][C::NJ];
+  auto rd = [&](int st, int kk, int buf, int i) {
+    if (i < C::NJ)
+      bfr[buf][i] = frag_b<C, BKM>(lds, st, wn * C::WN + i * 32, kk, lane);
+    else
+      af[buf][i - C::NJ] = frag_a<C, AKM>(lds, st, wm * C::WM + (i - C::NJ) * 32, kk, lane);
+  };
+  f32x16_t acc[C::MI][C::NJ];
+  auto sub = [&](int buf, int st_rd, int kk_rd, bool dma, int st_dma) {
+    constexpr int RPS = (NR + NM - 1) / NM, LPS = (NL + NM - 1) / NM;
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      const int mi = i / C::NJ, nj = i % C::NJ;
+      acc[mi][nj] = mma16<T, SWAP>(af[buf][mi], bfr[buf][nj], acc[mi][nj]);
+#pragma unroll
+      for (int q = 0; q < RPS; ++q)
+        if (i * RPS + q < NR) rd(st_rd, kk_rd, buf ^ 1, i * RPS + q);
+      if (dma) {
+#pragma unroll
+        for (int q = 0; q < LPS; ++q)
+          if (i * LPS + q < NL) ld.load(st_dma, i * LPS + q);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) ld.load(j, i);
+    ld.advance();
+  }
+  vm_wait<INFLIGHT>();
+  lds_barrier();
+  int st = 0, sti = NST - 1;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) rd(st, 0, 0, i);
+  for (int tc = first; tc < total; tc += nb) {
+    zero_acc<C>(acc);
+    const int nkc = epilogue.k_steps(tc);
+    for (int kc = 0; kc < nkc; ++kc) {
+      sub(0, st, 1, true, sti);
+      ld.advance();
+      sub(1, st, 2, false, 0);
+      sub(0, st, 3, false, 0);
+      vm_wait<INFLIGHT>();
+      lds_barrier();
+      st = st == NST - 1 ? 0 : st + 1;
+      sti = sti == NST - 1 ? 0 : sti + 1;
+      sub(1, st, 0, false, 0);
+    }
+    epilogue(tc, wm, wn, lane, acc);
+  }
+  vm_wait<0>();
+}
+
+// Two-phase loop for 256 x 256 tiles in 8 waves: the waves of one half
+// multiply (8 MFMAs) while those of the other half read the next sub-step's
+// fragments and issue loads, then they swap, so each SIMD's matrix core has
+// work in every phase. Two stages of 64 KB: the loads of step k + 1 go out in
+// the first two phases of step k and are waited for in its last.
+//
+// Why the stages are safe: the second half runs one phase behind (its extra
+// barrier before the loop; the first half's after it). A stage is read in the
+// memory phases of its step, each of which ends with lgkmcnt(0) before its
+// barrier. Step k + 1's loads overwrite the stage of step k - 1; the first
+// half issues them after the barrier that ends the second half's last memory
+// phase of step k - 1. Every wave waits for its own loads in its last memory
+// phase of step k, and the first half's first read of step k + 1 comes one
+// barrier after the second half's wait.
+template <class C, class T, bool AKM, bool BKM, bool SWAP, class NextOps, class Epilogue>
+__device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, int total,
+                                              NextOps&& next_ops, Epilogue&& epilogue) {
+  static_assert(C::NWAVES == 8 && C::NST == 2, "two halves of four waves, two stages");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  constexpr int NL = C::A_LOADS + C::B_LOADS;
+  Loader<C, AKM, BKM, std::remove_reference_t<NextOps>> ld(next_ops, lds_addr(lds), first, nb,
+                                                            total, wave);
+  bf16x8_t af[C::MI], bfr[C::NJ];
+  f32x16_t acc[C::MI][C::NJ];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) ld.load(0, i);
+  ld.advance();
+  vm_wait<0>();
+  lds_barrier();
+  if (wave >= 4) __builtin_amdgcn_s_barrier();
+  int st = 0;
+  for (int tc = first; tc < total; tc += nb) {
+    zero_acc<C>(acc);
+    const int nkc = epilogue.k_steps(tc);
+    for (int kc = 0; kc < nkc; ++kc) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int i = 0; i < C::NJ; ++i)
+          bfr[i] = frag_b<C, BKM>(lds, st, wn * C::WN + i * 32, kk, lane);
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+          af[i] = frag_a<C, AKM>(lds, st, wm * C::WM + i * 32, kk, lane);
+        if (kk < 2) {
+#pragma unroll
+          for (int i = kk * (NL / 2); i < (kk + 1) * (NL / 2); ++i) ld.load(st ^ 1, i);
+          if (kk == 1) ld.advance();
+        }
+        if (kk == 3) vm_wait<0>();
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+          for (int nj = 0; nj < C::NJ; ++nj)
+            acc[mi][nj] = mma16<T, SWAP>(af[mi], bfr[nj], acc[mi][nj]);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      st ^= 1;
+    }
+    epilogue(tc, wm, wn, lane, acc);
+  }
+  if (wave < 4) __builtin_amdgcn_s_barrier();
+  vm_wait<0>();
+}
+
+}  // namespace
+}  // namespace dsmoe

@@ -1,0 +1,459 @@
+// Matrix products grouped by expert over ragged row groups (definitions in
+// dsmoe_ops.h): forward y = x W_g^T, input gradient dx = dy W_g, weight
+// gradient dw_g = dy_g^T x_g. bf16 operands, fp32 accumulation.
+//
+// One launch per call: every workgroup builds the groups' tile table from the
+// device offsets itself, so no planning kernel runs first.
+#include "device_common.h"
+#include "gemm16_core.h"
+#include "internal.h"
+#include "tile_schedule.h"
+
+namespace dsmoe {
+
+namespace {
+
+enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+// Operands by mode (C[M, N] = A B, contraction K):
+//   forward  A = x rows, B = W_g rows (both k-contiguous);  M = rows of g
+//   dgrad    A = dy rows (k-contiguous), B = W_g (k-major); M = rows of g
+//   wgrad    A = dy rows (k-major), B = x rows (k-major);   K = rows of g
+struct GArgs {
+  const uint16_t* a;
+  const uint16_t* b;
+  const int32_t* offsets;
+  void* out;
+  int64_t rows, lda, ldb, ldo;
+  int G;
+  int n, k;  // output and input features
+  int out_f32, accumulate;
+  int vec;   // outputs can be stored four at a time
+};
+
+// Tile tables of the groups from the device offsets, clamped to an ascending
+// split of [0, rows]: t.off the row offsets, t.gnext[g] the first tile of
+// group g + 1, bm rows and tn column tiles per row tile. Called by all
+// threads of the block.
+__device__ __forceinline__ void build_group_tables(GroupTables& t, const int32_t* offsets, int G,
+                                                   int64_t rows, int bm, int tn) {
+  const int lim = static_cast<int>(rows);
+  for (int i = threadIdx.x; i < kMaxGroups; i += blockDim.x)
+    t.off[i] = i <= G ? min(max(offsets[i], 0), lim) : 0;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int v[8], run = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      run = max(run, t.off[8 * lane + j]);
+      v[j] = run;
+    }
+    // running maximum over the lanes before this one
+    int m = run;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(m, s, 64);
+      if (lane >= s) m = max(m, o);
+    }
+    const int up = __shfl_up(m, 1, 64);
+    const int before = lane ? up : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t.off[8 * lane + j] = max(v[j], before);
+    if (lane == 63) t.off[kMaxGroups - 1] = max(m, t.off[kMaxGroups - 1]);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int c[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int g = 8 * lane + j;
+      const int r = g < G ? t.off[g + 1] - t.off[g] : 0;
+      sum += (r + bm - 1) / bm * tn;
+      c[j] = sum;
+    }
+    int p = sum;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(p, s, 64);
+      if (lane >= s) p += o;
+    }
+    const int before = p - sum;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      t.gnext[8 * lane + j] = 8 * lane + j < G ? before + c[j] : 0x7fffffff;
+    if (lane == 63) t.total = p;
+  }
+  __syncthreads();
+}
+
+// Tile order of the weight gradient inside a group: rows of 8 m-tiles, m
+// fastest, so that the 32 consecutive tiles an XCD runs at a time read 8 A
+// panels and 4 B panels.
+constexpr int kSuper = 8;
+__device__ __forceinline__ void super_tile(int rem, int tm, int tn, int& m, int& n) {
+  const int per = kSuper * tn, gr = rem / per, r2 = rem - gr * per;
+  const int sm = min(kSuper, tm - gr * kSuper);
+  n = r2 / sm;
+  m = gr * kSuper + (r2 - n * sm);
+}
+
+// Bytes from the first element of `rows` rows to the end of the last one.
+__device__ __forceinline__ int64_t span(int rows, uint32_t ld_bytes, int width) {
+  return rows > 0 ? int64_t(rows - 1) * ld_bytes + int64_t(width) * 2 : 0;
+}
+
+struct GTile {
+  int g, m, n;       // group, tile indices
+  int64_t row0;      // first row of the group
+  int rows;          // rows of the group
+};
+
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, int tile) {
+  GTile c;
+  if constexpr (MODE == kWgrad) {
+    const int tm = (a.n + BM - 1) / BM, tn = (a.k + BN - 1) / BN;
+    c.g = tile / (tm * tn);
+    super_tile(tile - c.g * tm * tn, tm, tn, c.m, c.n);
+    const int r0 = __builtin_amdgcn_readfirstlane(t.off[c.g]);
+    c.row0 = r0;
+    c.rows = __builtin_amdgcn_readfirstlane(t.off[c.g + 1]) - r0;
+  } else {
+    const TileCoord tc = tile_coord_lds(t, a.G, 0, tile, BM);
+    c.g = tc.g;
+    c.m = tc.m;
+    c.n = tc.n;
+    c.row0 = tc.rbase;
+    c.rows = tc.rows;
+  }
+  return c;
+}
+
+// Stores (or adds) one value, or four adjacent ones of a row.
+__device__ __forceinline__ void put1(const GArgs& a, int64_t at, float v) {
+  if (a.out_f32) {
+    float* p = static_cast<float*>(a.out) + at;
+    *p = a.accumulate ? *p + v : v;
+  } else {
+    static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+  }
+}
+__device__ __forceinline__ void put4(const GArgs& a, int64_t at, int cnt, float v0, float v1,
+                                     float v2, float v3) {
+  if (a.vec && cnt >= 4) {
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v0, v1, v2, v3);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = pack_bf16x4(v0, v1, v2, v3);
+    return;
+  }
+  const float v[4] = {v0, v1, v2, v3};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < cnt) put1(a, at + j, v[j]);
+}
+
+// Output of a finished tile. Forward and dgrad hold the transposed tile (a
+// lane owns a row and runs of four columns), wgrad the tile itself (a lane
+// owns a column, so one register across the wave is two 128-byte row pieces
+// of fp32).
+template <class C, int MODE>
+__device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int wm, int wn, int lane,
+                                           f32x16_t (&acc)[C::MI][C::NJ]) {
+  if constexpr (MODE == kWgrad) {
+    const int64_t base = int64_t(c.g) * a.n * a.k;
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj) {
+      const int col = c.n * C::BN + wn * C::WN + nj * 32 + (lane & 31);
+#pragma unroll
+      for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = c.m * C::BM + wm * C::WM + mi * 32 + acc_row(lane, r);
+          if (row < a.n && col < a.k) {
+            float* p = static_cast<float*>(a.out) + base + int64_t(row) * a.k + col;
+            if (a.accumulate)
+              *p += acc[mi][nj][r];
+            else
+              __builtin_nontemporal_store(acc[mi][nj][r], p);
+          }
+        }
+    }
+  } else {
+    const int N = MODE == kForward ? a.n : a.k;
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi) {
+      const int r = c.m * C::BM + wm * C::WM + mi * 32 + (lane & 31);
+      if (r >= c.rows) continue;
+      const int64_t at = (c.row0 + r) * a.ldo;
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = c.n * C::BN + wn * C::WN + nj * 32 + 8 * q + 4 * (lane >> 5);
+          if (col >= N) continue;
+          const f32x16_t& v = acc[mi][nj];
+          put4(a, at + col, N - col, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+    }
+  }
+}
+
+// ---- operands of any alignment ------------------------------------------------
+
+// Eight elements at p (any element alignment), of which `cnt` exist.
+__device__ __forceinline__ uint4 chunk_any(const uint16_t* p, int cnt) {
+  uint4 r;
+  if (cnt >= 8) {
+    __builtin_memcpy(&r, p, 16);
+  } else {
+    uint16_t t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = j < cnt ? p[j] : uint16_t(0);
+    __builtin_memcpy(&r, t, 16);
+  }
+  return r;
+}
+
+using TileAny = Tile<128, 128, 64, 64, 2>;
+
+// Odd widths, pitches or base addresses: operands pass through registers
+// (unaligned 16-byte loads, element loads at the ends), one k-step ahead of
+// the MFMAs, into the same LDS layouts.
+template <int MODE>
+__global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
+  using C = TileAny;
+  constexpr bool AKM = MODE == kWgrad, BKM = MODE != kForward, SWAP = MODE != kWgrad;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  __shared__ GroupTables gt;
+  const int N = MODE == kForward ? a.n : a.k, M_w = a.n;
+  const int tn = (N + C::BN - 1) / C::BN;
+  build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, tn);
+  const int total = MODE == kWgrad ? a.G * ((M_w + C::BM - 1) / C::BM) * tn : gt.total;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  for (int tile = xcd_logical_block(blockIdx.x, gridDim.x); tile < total; tile += gridDim.x) {
+    const GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, tile);
+    const int K = MODE == kForward ? a.k : MODE == kDgrad ? a.n : c.rows;
+    const uint16_t* A = a.a + (MODE == kWgrad ? c.row0 : c.row0 + int64_t(c.m) * C::BM) * a.lda;
+    const uint16_t* B = MODE == kWgrad ? a.b + c.row0 * a.ldb : a.b + int64_t(c.g) * a.n * a.k;
+    const int a_rows = MODE == kWgrad ? a.n : c.rows - c.m * C::BM;
+    uint4 ra[C::A_LOADS], rb[C::B_LOADS];
+    // chunk p of the thread in k-step ks: LDS chunk p * NT + tid of its operand
+    auto get = [&](bool km, const uint16_t* P, int64_t ld, int rows, int col0, int width, int W,
+                   int p, int ks) -> uint4 {
+      if (km) {
+        const int cpr = W / 8, row = p * (C::NT / cpr) + tid / cpr;
+        const int kr = ks * BK + row;
+        const int col = col0 + ((tid % cpr) ^ (4 * (row & 3))) * 8;
+        return chunk_any(P + kr * ld + col, kr < K ? width - col : 0);
+      }
+      const int r = (tid >> 3) + p * C::RPP;
+      const int k0 = ks * BK + ((tid & 7) ^ ((r >> 1) & 7)) * 8;
+      return chunk_any(P + r * ld + k0, r < rows ? K - k0 : 0);
+    };
+    auto fetch = [&](int ks) {
+#pragma unroll
+      for (int p = 0; p < C::A_LOADS; ++p)
+        ra[p] = get(AKM, A, a.lda, a_rows, c.m * C::BM, a.n, C::BM, p, ks);
+#pragma unroll
+      for (int p = 0; p < C::B_LOADS; ++p)
+        rb[p] = BKM ? get(true, B, a.ldb, 0, c.n * C::BN, a.k, C::BN, p, ks)
+                    : get(false, B + int64_t(c.n) * C::BN * a.ldb, a.ldb, a.n - c.n * C::BN, 0, 0,
+                          C::BN, p, ks);
+    };
+    auto stash = [&](int st) {
+      uint16_t* s = lds + st * C::STAGE;
+#pragma unroll
+      for (int p = 0; p < C::A_LOADS; ++p)
+        *reinterpret_cast<uint4*>(s + (p * C::NT + tid) * 8) = ra[p];
+#pragma unroll
+      for (int p = 0; p < C::B_LOADS; ++p)
+        *reinterpret_cast<uint4*>(s + C::BM * BK + (p * C::NT + tid) * 8) = rb[p];
+    };
+    f32x16_t acc[C::MI][C::NJ];
+    zero_acc<C>(acc);
+    const int nk = (K + BK - 1) / BK;
+    if (nk > 0) {
+      fetch(0);
+      stash(0);
+    }
+    __syncthreads();
+    for (int ks = 0; ks < nk; ++ks) {
+      const int st = ks & 1;
+      if (ks + 1 < nk) fetch(ks + 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        bf16x8_t af[C::MI], bf[C::NJ];
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+          af[i] = frag_a<C, AKM>(lds, st, wm * C::WM + i * 32, kk, lane);
+#pragma unroll
+        for (int i = 0; i < C::NJ; ++i)
+          bf[i] = frag_b<C, BKM>(lds, st, wn * C::WN + i * 32, kk, lane);
+#pragma unroll
+        for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+          for (int nj = 0; nj < C::NJ; ++nj)
+            acc[mi][nj] = mma16<TypeBf16, SWAP>(af[mi], bf[nj], acc[mi][nj]);
+      }
+      if (ks + 1 < nk) stash(st ^ 1);
+      __syncthreads();
+    }
+    store_tile<C, MODE>(a, c, wm, wn, lane, acc);
+  }
+}
+
+// ---- 16-byte aligned operands --------------------------------------------------
+
+// Operand rows, pitches and base addresses in whole 16-byte chunks: loads go
+// straight into LDS.
+template <class C, int MODE, bool PHASED>
+__global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
+  constexpr bool AKM = MODE == kWgrad, BKM = MODE != kForward, SWAP = MODE != kWgrad;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  __shared__ GroupTables gt;
+  const int N = MODE == kForward ? a.n : a.k;
+  const int tn = (N + C::BN - 1) / C::BN;
+  build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, tn);
+  const int total = MODE == kWgrad ? a.G * ((a.n + C::BM - 1) / C::BM) * tn : gt.total;
+  const int first = xcd_logical_block(blockIdx.x, gridDim.x);
+  if (first >= total) return;
+  const uint32_t lda = static_cast<uint32_t>(a.lda) * 2u, ldb = static_cast<uint32_t>(a.ldb) * 2u;
+  auto steps = [&](int rows) {
+    const int K = MODE == kForward ? a.k : MODE == kDgrad ? a.n : rows;
+    return K > BK ? (K + BK - 1) / BK : 1;
+  };
+  auto next_ops = [&](int tile, Ops16<C>& op) {
+    const GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, tile);
+    op.nk = steps(c.rows);
+    if constexpr (MODE == kWgrad) {
+      kmajor_operand<C, C::BM>(op.ra, op.ao, op.base_a, op.left_a, op.step_a, a.a + c.row0 * a.lda,
+                               c.m * C::BM, lda, span(c.rows, lda, a.n));
+      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, a.b + c.row0 * a.ldb,
+                               c.n * C::BN, ldb, span(c.rows, ldb, a.k));
+    } else {
+      const int K = MODE == kForward ? a.k : a.n;
+      const int left = c.rows - c.m * C::BM;
+      kcontig_operand<C>(op.ra, op.ao, op.tail_a, a.a + (c.row0 + int64_t(c.m) * C::BM) * a.lda,
+                         left, lda, span(min(left, C::BM), lda, K), K);
+      const uint16_t* W = a.b + int64_t(c.g) * a.n * a.k;
+      if constexpr (MODE == kForward) {
+        const int nleft = a.n - c.n * C::BN;
+        kcontig_operand<C>(op.rb, op.bo, op.tail_b, W + int64_t(c.n) * C::BN * a.ldb, nleft, ldb,
+                           int64_t(min(nleft, C::BN)) * ldb, K);
+      } else {
+        kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, W, c.n * C::BN, ldb,
+                                 int64_t(a.n) * ldb);
+      }
+    }
+  };
+  struct Epilogue {
+    const GArgs& a;
+    const GroupTables& gt;
+    decltype(steps)& st;
+    __device__ int k_steps(int tile) const {
+      if constexpr (MODE == kWgrad)
+        return st(tile_of<MODE, C::BM, C::BN>(a, gt, tile).rows);
+      else
+        return st(0);
+    }
+    __device__ void operator()(int tile, int wm, int wn, int lane,
+                               f32x16_t (&acc)[C::MI][C::NJ]) const {
+      store_tile<C, MODE>(a, tile_of<MODE, C::BM, C::BN>(a, gt, tile), wm, wn, lane, acc);
+    }
+  } ep{a, gt, steps};
+  if constexpr (PHASED)
+    stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
+  else
+    stream_ring<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
+}
+
+// Workgroups of a persistent launch of kernel K: the resident ones, or no more
+// than the tiles there can be (whole XCD rounds).
+template <auto K>
+unsigned grid_of(int threads, int64_t tiles) {
+  static int res = 0;
+  if (!res) {
+    int nb = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, K, threads, 0) != hipSuccess || nb < 1)
+      nb = 1;
+    res = (device_cu_count() * nb + 7) / 8 * 8;
+  }
+  const int64_t t = (tiles + 7) / 8 * 8;
+  return static_cast<unsigned>(t < res ? (t < 8 ? 8 : t) : res);
+}
+
+template <int MODE, class C>
+int64_t tile_bound(const GArgs& a) {
+  const int64_t tn = ((MODE == kForward ? a.n : a.k) + C::BN - 1) / C::BN;
+  if (MODE == kWgrad) return int64_t(a.G) * ((a.n + C::BM - 1) / C::BM) * tn;
+  const int64_t full = a.rows / C::BM + (a.rows < a.G ? a.rows : a.G);
+  return full * tn;
+}
+
+template <int MODE, class C, bool PHASED>
+void launch_fast(const GArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((grouped_kernel<C, MODE, PHASED>),
+                     dim3(grid_of<grouped_kernel<C, MODE, PHASED>>(C::NT, tile_bound<MODE, C>(a))),
+                     dim3(C::NT), 0, s, a);
+}
+
+using TileBig = Tile<256, 256, 128, 64, 2>;  // 128 KB LDS
+
+template <int MODE>
+hipError_t launch_mode(const GArgs& a, bool aligned, hipStream_t s) {
+  if (aligned) {
+    launch_fast<MODE, TileBig, true>(a, s);
+  } else {
+    const int64_t tiles = tile_bound<MODE, TileAny>(a);
+    hipLaunchKernelGGL(grouped_any_kernel<MODE>,
+                       dim3(grid_of<grouped_any_kernel<MODE>>(TileAny::NT, tiles)),
+                       dim3(TileAny::NT), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+hipError_t launch_grouped(const GroupedArgs& p, hipStream_t s) {
+  GArgs a{};
+  a.a = static_cast<const uint16_t*>(p.a);
+  a.b = static_cast<const uint16_t*>(p.b);
+  a.offsets = p.offsets;
+  a.out = p.out;
+  a.rows = p.rows;
+  a.G = p.n_groups;
+  a.n = p.n;
+  a.k = p.k;
+  a.out_f32 = p.out_f32;
+  a.accumulate = p.accumulate;
+  const bool base = on16(p.a) && on16(p.b);
+  if (p.mode == kForward) {
+    a.lda = p.ld_k;
+    a.ldb = p.k;
+    a.ldo = p.ld_n;
+  } else if (p.mode == kDgrad) {
+    a.lda = p.ld_n;
+    a.ldb = p.k;
+    a.ldo = p.ld_k;
+  } else {
+    a.lda = p.ld_n;
+    a.ldb = p.ld_k;
+    a.ldo = p.k;
+  }
+  a.vec = !a.accumulate && a.ldo % 4 == 0 && on16(p.out);
+  if (p.mode == kWgrad)
+    return launch_mode<kWgrad>(a, base && a.lda % 8 == 0 && a.ldb % 8 == 0, s);
+  if (p.rows == 0) return hipSuccess;
+  // the contraction of a k-contiguous operand ends on a chunk, every pitch on one
+  if (p.mode == kForward)
+    return launch_mode<kForward>(a, base && a.lda % 8 == 0 && p.k % 8 == 0, s);
+  return launch_mode<kDgrad>(a, base && a.lda % 8 == 0 && p.n % 8 == 0 && p.k % 8 == 0, s);
+}
+
+}  // namespace dsmoe

@@ -255,6 +255,59 @@ hipError_t launch_quant_rows(const void* src, int src_dtype, const int32_t* perm
                              int cols, uint8_t* q, float* scale, hipStream_t s, int fmt = 0,
                              bool kmajor = false);
 
+// ---- operators around the layer (dsmoe_ops.h) -------------------------------
+// norm.hip: x (backward: what was normalized), r residual or dresidual (may be
+// NULL), y output or dy, s sum (may be NULL) or dx.
+struct NormArgs {
+  int64_t n;
+  int d;
+  bool bf16;
+  float eps;
+  const void* x;
+  const void* r;
+  const float* w;
+  const float* b;
+  void* y;
+  void* s;
+  float* mean;
+  float* rstd;
+  int64_t ldx, ldr, ldy, lds;
+};
+// rows of partial column sums [parts][2 d] fp32 the backward writes
+int norm_backward_parts(int64_t n, int d);
+hipError_t launch_norm_forward(const NormArgs& p, hipStream_t s);
+hipError_t launch_norm_backward(const NormArgs& p, float* dw, float* db, float* part,
+                                hipStream_t s);
+
+// grouped.hip: mode 0 forward (a = x, b = w), 1 input gradient (a = dy, b = w),
+// 2 weight gradient (a = dy, b = x). ld_k: stride of x or dx, ld_n: of y or dy.
+struct GroupedArgs {
+  int mode;
+  const void* a;
+  const void* b;
+  const int32_t* offsets;
+  void* out;
+  int64_t rows, ld_k, ld_n;
+  int n_groups, n, k;
+  bool out_f32, accumulate;
+};
+hipError_t launch_grouped(const GroupedArgs& p, hipStream_t s);
+
+// orth.hip
+struct OrthArgs {
+  int64_t mats;
+  int rows, cols, steps;
+  bool bf16, nesterov;
+  float momentum;
+  const void* grad;
+  const float* m_in;
+  float* m_out;
+  void* out;
+  void* ws;
+};
+size_t orth_workspace(int64_t mats, int rows, int cols);
+hipError_t launch_orth(const OrthArgs& p, hipStream_t s);
+
 // number of compute units of the current device (cached per device)
 int device_cu_count();
 

@@ -1,0 +1,443 @@
+// Orthogonalized updates of weight matrices by Newton-Schulz products
+// (definition in dsmoe_ops.h). With n = min(rows, cols), m = max(rows, cols)
+// every matrix is worked on as X [n, m] (transposed on entry and exit where
+// rows > cols).
+//
+// Number format. Every product takes fp16 operands and adds in fp32. fp16
+// rather than bf16 because all values have known bounds (|X| <= 1.21, since
+// the polynomial maps [0, 1.21] into itself; |A| <= 1.47; |b A + c A A| <= 7),
+// so that fixed power-of-two scales use its 11 significant bits without range
+// trouble. Three things are kept out of the 16-bit roundings:
+//   X  = (hi + lo 2^-11) 2^-12, two fp16 planes: hi feeds the products, both
+//        carry X through the a X term. A rank-deficient update needs this:
+//        rounding noise in its null space would grow 3.44 times per step.
+//   A  = D + R with the diagonal D in fp32, R (zero diagonal) in fp16:
+//        A A = R R + D R + R D + D D, of which only R R is a product;
+//   B  = b A + c A A = Q + S the same way: X <- (a + Q) X + S X.
+// Near convergence D and Q dominate their matrices, so their fp16 roundings
+// would be most of the error: on random matrices the result is 5e-4 off (2-norm)
+// this way, 1.7e-3 with the diagonals inside, 1.1e-2 in bf16 throughout.
+//
+// A and A A are symmetric: tiles on and below the diagonal are computed and
+// stored twice. Per step that leaves n^2 m + n^3 + 2 n^2 m operations.
+#include "device_common.h"
+#include "gemm16_core.h"
+#include "internal.h"
+
+namespace dsmoe {
+
+namespace {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 4096.0f;     // 2^12: X planes
+constexpr float kScaleLo = 2048.0f;    // 2^11: lo against hi
+constexpr float kScaleR = 4096.0f;     // 2^12: off-diagonal of A
+constexpr float kScaleS = 1024.0f;     // 2^10: off-diagonal of B
+constexpr double kNormEps = 1e-7;
+
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+
+// Workspace of one matrix (offsets in bytes, planes in rows of pitches mp, np:
+// m, n rounded up to whole k-steps, the padding columns zero).
+struct OrthShape {
+  int n, m, np, mp;
+  bool tall;
+  int chunks;  // partial sums of squares per matrix
+  size_t hi0, hi1, lo, r, s, d, q, part, bytes;
+};
+
+constexpr int kSumChunk = 16384;  // elements of one partial sum of squares
+
+OrthShape shape_of(int rows, int cols) {
+  OrthShape o{};
+  o.tall = rows > cols;
+  o.n = o.tall ? cols : rows;
+  o.m = o.tall ? rows : cols;
+  o.np = (o.n + 63) / 64 * 64;
+  o.mp = (o.m + 63) / 64 * 64;
+  const int64_t el = int64_t(rows) * cols;
+  o.chunks = static_cast<int>((el + kSumChunk - 1) / kSumChunk);
+  if (o.chunks > 256) o.chunks = 256;
+  size_t at = 0;
+  auto take = [&](size_t b) {
+    const size_t r = at;
+    at = (at + b + 255) & ~size_t(255);
+    return r;
+  };
+  const size_t plane = size_t(o.n) * o.mp * 2, sq = size_t(o.n) * o.np * 2;
+  o.hi0 = take(plane);
+  o.hi1 = take(plane);
+  o.lo = take(plane);
+  o.r = take(sq);
+  o.s = take(sq);
+  o.d = take(size_t(o.np) * 4);
+  o.q = take(size_t(o.np) * 4);
+  o.part = take(size_t(o.chunks) * 8);
+  o.bytes = at;
+  return o;
+}
+
+struct PrepArgs {
+  const void* grad;
+  const float* m_in;
+  float* m_out;
+  char* ws;
+  OrthShape o;
+  int rows, cols;
+  float momentum;
+  int nesterov;
+};
+
+__device__ __forceinline__ float load_grad(const float* p) { return *p; }
+__device__ __forceinline__ float load_grad(const uint16_t* p) { return bf16_to_f32(*p); }
+
+// Momentum, and the partial sums of squares of u (fp64: any scale of the
+// gradient squares without overflow or underflow). Block (chunk, matrix).
+template <class T, bool MOM>
+__global__ __launch_bounds__(256) void orth_sum_kernel(PrepArgs a) {
+  __shared__ double red[4];
+  const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.y;
+  const T* g = static_cast<const T*>(a.grad) + mat * el;
+  const int64_t per = ((el + a.o.chunks - 1) / a.o.chunks + 255) / 256 * 256;
+  const int64_t e0 = int64_t(blockIdx.x) * per, e1 = min(e0 + per, el);
+  double s = 0.0;
+  for (int64_t i = e0 + threadIdx.x; i < e1; i += 256) {
+    float u = load_grad(g + i);
+    if constexpr (MOM) {
+      const float mo = a.momentum * a.m_in[mat * el + i] + u;
+      a.m_out[mat * el + i] = mo;
+      u = a.nesterov ? u + a.momentum * mo : mo;
+    }
+    s += double(u) * u;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    reinterpret_cast<double*>(a.ws + mat * a.o.bytes + a.o.part)[blockIdx.x] =
+        ((red[0] + red[1]) + red[2]) + red[3];
+}
+
+__device__ __forceinline__ void split_x(float v, _Float16& hi, _Float16& lo) {
+  hi = static_cast<_Float16>(v);
+  lo = static_cast<_Float16>((v - static_cast<float>(hi)) * kScaleLo);
+}
+
+// X_0 = u / (|u| + eps) into the planes, 64 x 64 elements per block
+// (transposed through LDS where rows > cols), padding columns zero.
+template <class T, bool MOM, bool TALL>
+__global__ __launch_bounds__(256) void orth_scale_kernel(PrepArgs a) {
+  __shared__ float tile[TALL ? 64 : 1][65];
+  __shared__ double red[4];
+  __shared__ float scale_s;
+  const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.z;
+  char* ws = a.ws + mat * a.o.bytes;
+  const double* part = reinterpret_cast<const double*>(ws + a.o.part);
+  double s = static_cast<int>(threadIdx.x) < a.o.chunks ? part[threadIdx.x] : 0.0;
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    scale_s = static_cast<float>(kScaleX / (sqrt(((red[0] + red[1]) + red[2]) + red[3]) + kNormEps));
+  __syncthreads();
+  const float scale = scale_s;
+  const T* g = static_cast<const T*>(a.grad) + mat * el;
+  const float* mo = MOM ? a.m_out + mat * el : nullptr;
+  auto u_at = [&](int64_t i) {
+    const float u = load_grad(g + i);
+    if constexpr (MOM) return a.nesterov ? u + a.momentum * mo[i] : mo[i];
+    return u;
+  };
+  _Float16* hi = reinterpret_cast<_Float16*>(ws + a.o.hi0);
+  _Float16* lo = reinterpret_cast<_Float16*>(ws + a.o.lo);
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // of X
+  if constexpr (TALL) {
+    for (int i = ty; i < 64; i += 4) {  // row c0 + i of u, columns r0 ..
+      const int ur = c0 + i, uc = r0 + tx;
+      tile[i][tx] = (ur < a.rows && uc < a.cols) ? u_at(int64_t(ur) * a.cols + uc) : 0.0f;
+    }
+    __syncthreads();
+  }
+  for (int i = ty; i < 64; i += 4) {
+    const int r = r0 + i, c = c0 + tx;
+    if (r >= a.o.n || c >= a.o.mp) continue;
+    float v;
+    if constexpr (TALL)
+      v = tile[tx][i];
+    else
+      v = c < a.o.m ? u_at(int64_t(r) * a.cols + c) : 0.0f;
+    _Float16 h, l;
+    split_x(v * scale, h, l);
+    hi[int64_t(r) * a.o.mp + c] = h;
+    lo[int64_t(r) * a.o.mp + c] = l;
+  }
+}
+
+// ---- the three products of a step ------------------------------------------------
+
+enum Kind { kGram = 0, kSquare = 1, kApply = 2, kApplyLast = 3 };
+
+struct StepArgs {
+  char* ws;
+  OrthShape o;
+  size_t hi_in, hi_out;  // planes of X read and written
+  void* out;             // last step: bf16 [rows, cols]
+  int64_t mats;
+};
+
+// Lower-triangular tile p (row by row) of a symmetric product.
+__device__ __forceinline__ void triangle(int p, int& i, int& j) {
+  i = static_cast<int>((sqrtf(8.0f * p + 1.0f) - 1.0f) * 0.5f);
+  while (i * (i + 1) / 2 > p) --i;
+  while ((i + 1) * (i + 2) / 2 <= p) ++i;
+  j = p - i * (i + 1) / 2;
+}
+
+struct OTile {
+  int64_t mat;
+  int m, n;
+};
+
+template <class C, int KIND>
+__device__ __forceinline__ OTile orth_tile(const StepArgs& a, int tile) {
+  const int tm = (a.o.n + C::BM - 1) / C::BM;
+  OTile t;
+  if constexpr (KIND == kGram || KIND == kSquare) {
+    static_assert(C::BM == C::BN, "square tiles on the diagonal");
+    const int per = tm * (tm + 1) / 2;
+    t.mat = tile / per;
+    triangle(tile - static_cast<int>(t.mat) * per, t.m, t.n);
+  } else {
+    const int tn = (a.o.m + C::BN - 1) / C::BN, per = tm * tn;
+    t.mat = tile / per;
+    const int r = tile - static_cast<int>(t.mat) * per;
+    t.n = r / tm;  // m fastest: the row tiles that share columns of X run together
+    t.m = r - t.n * tm;
+  }
+  return t;
+}
+
+template <class C, int KIND, bool TALL, bool PHASED>
+__global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a, int total) {
+  constexpr bool BKM = KIND >= kApply;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  const int first = xcd_logical_block(blockIdx.x, gridDim.x);
+  if (first >= total) return;
+  const int K = KIND == kGram ? a.o.mp : a.o.np;
+  auto next_ops = [&](int tile, Ops16<C>& op) {
+    const OTile t = orth_tile<C, KIND>(a, tile);
+    const char* ws = a.ws + t.mat * a.o.bytes;
+    const uint32_t ldx = a.o.mp * 2, lds_ = a.o.np * 2;
+    const int left = min(a.o.n - t.m * C::BM, C::BM);
+    op.nk = K / BK;
+    const char* A = ws + (KIND == kGram ? a.hi_in : KIND == kSquare ? a.o.r : a.o.s);
+    const uint32_t lda = KIND == kGram ? ldx : lds_;
+    kcontig_operand<C>(op.ra, op.ao, op.tail_a, A + int64_t(t.m) * C::BM * lda, left, lda,
+                       int64_t(left) * lda, K);
+    if constexpr (BKM) {
+      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, ws + a.hi_in,
+                               t.n * C::BN, ldx, int64_t(a.o.n) * ldx);
+    } else {
+      const int nleft = min(a.o.n - t.n * C::BN, C::BN);
+      kcontig_operand<C>(op.rb, op.bo, op.tail_b, A + int64_t(t.n) * C::BN * lda, nleft, lda,
+                         int64_t(nleft) * lda, K);
+    }
+  };
+  struct Epilogue {
+    const StepArgs& a;
+    int nk;
+    __device__ int k_steps(int) const { return nk; }
+    __device__ void operator()(int tile, int wm, int wn, int lane,
+                               f32x16_t (&acc)[C::MI][C::NJ]) const {
+      const OTile t = orth_tile<C, KIND>(a, tile);
+      char* ws = a.ws + t.mat * a.o.bytes;
+      const int n = a.o.n, np = a.o.np, mp = a.o.mp;
+      const float* D = reinterpret_cast<const float*>(ws + a.o.d);
+      const float* Q = reinterpret_cast<const float*>(ws + a.o.q);
+#pragma unroll
+      for (int mi = 0; mi < C::MI; ++mi) {
+        const int row = t.m * C::BM + wm * C::WM + mi * 32 + (lane & 31);
+        // rows n .. np - 1 of a symmetric product only put their zeros into
+        // the padding columns of the mirrored tile
+        if (row >= (KIND < kApply ? np : n)) continue;
+#pragma unroll
+        for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int col = t.n * C::BN + wn * C::WN + nj * 32 + 8 * g + 4 * (lane >> 5);
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = acc[mi][nj][4 * g + j];
+            if constexpr (KIND == kGram || KIND == kSquare) {
+              if (col >= np) continue;
+              f16x4_t o;
+              if constexpr (KIND == kGram) {
+                float* d = reinterpret_cast<float*>(ws + a.o.d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float x = v[j] * (1.0f / (kScaleX * kScaleX));
+                  if (col + j == row && row < n) d[row] = x;
+                  o[j] = static_cast<_Float16>(col + j == row ? 0.0f : x * kScaleR);
+                }
+              } else {
+                f16x4_t r4 = {};
+                float di = 0.0f;
+                if (row < n) {
+                  r4 = *reinterpret_cast<const f16x4_t*>(ws + a.o.r +
+                                                         (int64_t(row) * np + col) * 2);
+                  di = D[row];
+                }
+                float* q = reinterpret_cast<float*>(ws + a.o.q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float rij = static_cast<float>(r4[j]) * (1.0f / kScaleR);
+                  const float dj = col + j < n ? D[col + j] : 0.0f;
+                  const float rr = v[j] * (1.0f / (kScaleR * kScaleR));
+                  if (col + j == row && row < n) q[row] = kB * di + kC * (rr + di * di);
+                  const float s = kB * rij + kC * (rr + (di + dj) * rij);
+                  o[j] = static_cast<_Float16>(col + j == row ? 0.0f : s * kScaleS);
+                }
+              }
+              _Float16* dst = reinterpret_cast<_Float16*>(ws + (KIND == kGram ? a.o.r : a.o.s));
+              if (row < n) *reinterpret_cast<f16x4_t*>(dst + int64_t(row) * np + col) = o;
+              if (t.m != t.n) {  // the mirrored tile
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (col + j < n) dst[int64_t(col + j) * np + row] = o[j];
+              }
+            } else {
+              if (col >= mp) continue;
+              const int64_t at = int64_t(row) * mp + col;
+              const f16x4_t h = *reinterpret_cast<const f16x4_t*>(ws + a.hi_in + at * 2);
+              const f16x4_t l = *reinterpret_cast<const f16x4_t*>(ws + a.o.lo + at * 2);
+              const float f = kA + Q[row];
+              float x[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[j] = f * (static_cast<float>(h[j]) + static_cast<float>(l[j]) * (1.0f / kScaleLo)) +
+                       v[j] * (1.0f / kScaleS);
+              if constexpr (KIND == kApply) {
+                f16x4_t ho, lo;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  _Float16 hh, ll;
+                  split_x(x[j], hh, ll);
+                  ho[j] = hh;
+                  lo[j] = ll;
+                }
+                *reinterpret_cast<f16x4_t*>(ws + a.hi_out + at * 2) = ho;
+                *reinterpret_cast<f16x4_t*>(ws + a.o.lo + at * 2) = lo;
+              } else {
+                const int m = a.o.m;
+                uint16_t* out = static_cast<uint16_t*>(a.out) + t.mat * n * int64_t(m);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] *= 1.0f / kScaleX;
+                if (!TALL && m % 4 == 0) {
+                  if (col < m)
+                    *reinterpret_cast<uint2*>(out + int64_t(row) * m + col) =
+                        pack_bf16x4(x[0], x[1], x[2], x[3]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (col + j < m)
+                      out[TALL ? int64_t(col + j) * n + row : int64_t(row) * m + col + j] =
+                          f32_to_bf16(x[j]);
+                }
+              }
+            }
+          }
+      }
+    }
+  } ep{a, K / BK};
+  if constexpr (PHASED)
+    stream_phased<C, TypeF16, false, BKM, true>(lds, first, gridDim.x, total, next_ops, ep);
+  else
+    stream_ring<C, TypeF16, false, BKM, true>(lds, first, gridDim.x, total, next_ops, ep);
+}
+
+template <auto K>
+unsigned grid_of(int threads, int64_t tiles) {
+  static int res = 0;
+  if (!res) {
+    int nb = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, K, threads, 0) != hipSuccess || nb < 1)
+      nb = 1;
+    res = (device_cu_count() * nb + 7) / 8 * 8;
+  }
+  const int64_t t = (tiles + 7) / 8 * 8;
+  return static_cast<unsigned>(t < res ? t : res);
+}
+
+template <class C, int KIND, bool TALL, bool PHASED>
+void product(const StepArgs& a, hipStream_t s) {
+  const int64_t tm = (a.o.n + C::BM - 1) / C::BM, tn = (a.o.m + C::BN - 1) / C::BN;
+  const int64_t total = a.mats * (KIND < kApply ? tm * (tm + 1) / 2 : tm * tn);
+  hipLaunchKernelGGL((orth_product_kernel<C, KIND, TALL, PHASED>),
+                     dim3(grid_of<orth_product_kernel<C, KIND, TALL, PHASED>>(C::NT, total)),
+                     dim3(C::NT), 0, s, a, static_cast<int>(total));
+}
+
+using TileBig = Tile<256, 256, 128, 64, 2>;
+
+template <class C, bool PHASED>
+void steps(StepArgs a, const OrthArgs& p, hipStream_t s) {
+  for (int i = 0; i < p.steps; ++i) {
+    a.hi_in = i & 1 ? a.o.hi1 : a.o.hi0;
+    a.hi_out = i & 1 ? a.o.hi0 : a.o.hi1;
+    product<C, kGram, false, PHASED>(a, s);
+    product<C, kSquare, false, PHASED>(a, s);
+    if (i + 1 < p.steps)
+      product<C, kApply, false, PHASED>(a, s);
+    else if (a.o.tall)
+      product<C, kApplyLast, true, PHASED>(a, s);
+    else
+      product<C, kApplyLast, false, PHASED>(a, s);
+  }
+}
+
+template <class T, bool MOM>
+void prepare(const PrepArgs& a, int64_t mats, hipStream_t s) {
+  hipLaunchKernelGGL((orth_sum_kernel<T, MOM>), dim3(a.o.chunks, static_cast<unsigned>(mats)),
+                     dim3(256), 0, s, a);
+  const dim3 g((a.o.mp + 63) / 64, (a.o.n + 63) / 64, static_cast<unsigned>(mats));
+  if (a.o.tall)
+    hipLaunchKernelGGL((orth_scale_kernel<T, MOM, true>), g, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((orth_scale_kernel<T, MOM, false>), g, dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+size_t orth_workspace(int64_t mats, int rows, int cols) {
+  return static_cast<size_t>(mats) * shape_of(rows, cols).bytes;
+}
+
+hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
+  if (p.mats == 0) return hipSuccess;
+  PrepArgs a{};
+  a.grad = p.grad;
+  a.m_in = p.m_in;
+  a.m_out = p.m_out;
+  a.ws = static_cast<char*>(p.ws);
+  a.o = shape_of(p.rows, p.cols);
+  a.rows = p.rows;
+  a.cols = p.cols;
+  a.momentum = p.momentum;
+  a.nesterov = p.nesterov;
+  if (p.bf16)
+    p.m_in ? prepare<uint16_t, true>(a, p.mats, s) : prepare<uint16_t, false>(a, p.mats, s);
+  else
+    p.m_in ? prepare<float, true>(a, p.mats, s) : prepare<float, false>(a, p.mats, s);
+  StepArgs st{};
+  st.ws = a.ws;
+  st.o = a.o;
+  st.out = p.out;
+  st.mats = p.mats;
+  steps<TileBig, true>(st, p, s);
+  return hipGetLastError();
+}
+
+}  // namespace dsmoe
