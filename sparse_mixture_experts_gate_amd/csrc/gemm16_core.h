@@ -172,10 +172,52 @@ __device__ __forceinline__ f32x16_t mma16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return SWAP ? T::mfma(b, a, c) : T::mfma(a, b, c);
 }
 
+// Output through LDS: the fragments' layout gives a lane 4 adjacent columns of
+// its row, which as stores would be 16-byte pieces of 32 rows. 32 rows of a
+// wave's WN columns at a time pass through its part of LDS (fp32, 16-byte
+// chunks XOR-swizzled with the row, free of bank conflicts both ways), and
+// come back as 8 adjacent columns of one row per lane: whole 128-byte lines
+// for 16-bit outputs.
+template <class C>
+struct RowPasses {
+  static constexpr int CPR = C::WN / 4;            // chunks of a row
+  static constexpr int LPR = C::WN / 8;            // lanes of a row
+  static constexpr int RPP = 64 / LPR;             // rows of a pass
+  static constexpr int N = 32 / RPP;               // passes over 32 rows
+  static constexpr int FLOATS = 32 * C::WN;        // LDS floats per wave
+
+  // row (0..31) and first column (within the wave's) of this lane in pass p
+  __device__ static int row(int p, int lane) { return p * RPP + lane / LPR; }
+  __device__ static int col(int lane) { return (lane % LPR) * 8; }
+
+  __device__ static void put(float* stage, int lane, const f32x16_t (&acc)[C::NJ]) {
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = (nj * 8 + 2 * g + h) ^ (r & (CPR - 1));
+        const f32x4_t v = {acc[nj][4 * g], acc[nj][4 * g + 1], acc[nj][4 * g + 2],
+                           acc[nj][4 * g + 3]};
+        *reinterpret_cast<f32x4_t*>(stage + r * C::WN + c * 4) = v;
+      }
+  }
+  __device__ static void get(const float* stage, int lane, int p, float (&v)[8]) {
+    const int r = row(p, lane), c = (lane % LPR) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4_t x =
+          *reinterpret_cast<const f32x4_t*>(stage + r * C::WN + ((c + i) ^ (r & (CPR - 1))) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
+    }
+  }
+};
+
 // Ring loop for small tiles: NST stages, loads NST - 1 k-steps ahead, the
 // fragments of sub-step kk + 1 read between the MFMAs of sub-step kk, one
 // barrier per k-step (before its last sub-step, whose fragments are already
-// in registers).
+// in registers). LDS: C::LDS_ELEMS for the ring, then the waves' output stages.
 template <class C, class T, bool AKM, bool BKM, bool SWAP, class NextOps, class Epilogue>
 __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, int total,
                                             NextOps&& next_ops, Epilogue&& epilogue) {
@@ -237,7 +279,8 @@ __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, in
       sti = sti == NST - 1 ? 0 : sti + 1;
       sub(1, st, 0, false, 0);
     }
-    epilogue(tc, wm, wn, lane, acc);
+    epilogue(tc, wm, wn, lane, acc,
+             reinterpret_cast<float*>(lds + C::LDS_ELEMS) + wave * RowPasses<C>::FLOATS);
   }
   vm_wait<0>();
 }
@@ -248,14 +291,19 @@ __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, in
 // work in every phase. Two stages of 64 KB: the loads of step k + 1 go out in
 // the first two phases of step k and are waited for in its last.
 //
-// Why the stages are safe: the second half runs one phase behind (its extra
-// barrier before the loop; the first half's after it). A stage is read in the
+// The halves fall into step again for a tile's epilogue: staggered, each half
+// would wait at a barrier for the other's stores.
+//
+// Why the stages are safe: within a tile the second half runs one phase behind
+// (its extra barrier before the k-loop; the first half's after it). A stage is read in the
 // memory phases of its step, each of which ends with lgkmcnt(0) before its
 // barrier. Step k + 1's loads overwrite the stage of step k - 1; the first
 // half issues them after the barrier that ends the second half's last memory
 // phase of step k - 1. Every wave waits for its own loads in its last memory
 // phase of step k, and the first half's first read of step k + 1 comes one
-// barrier after the second half's wait.
+// barrier after the second half's wait. The output stages lie in the stage of
+// the tile's last step, which every wave has read when the halves are in step;
+// the barrier after the epilogue keeps the next loads out of it until then.
 template <class C, class T, bool AKM, bool BKM, bool SWAP, class NextOps, class Epilogue>
 __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, int total,
                                               NextOps&& next_ops, Epilogue&& epilogue) {
@@ -273,11 +321,11 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
   ld.advance();
   vm_wait<0>();
   lds_barrier();
-  if (wave >= 4) __builtin_amdgcn_s_barrier();
   int st = 0;
   for (int tc = first; tc < total; tc += nb) {
     zero_acc<C>(acc);
     const int nkc = epilogue.k_steps(tc);
+    if (wave >= 4) __builtin_amdgcn_s_barrier();
     for (int kc = 0; kc < nkc; ++kc) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
@@ -306,9 +354,13 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
       }
       st ^= 1;
     }
-    epilogue(tc, wm, wn, lane, acc);
+    if (wave < 4) __builtin_amdgcn_s_barrier();
+    // the stage just read is free until the next tile's first loads
+    static_assert(8 * RowPasses<C>::FLOATS * 4 <= C::STAGE * 2, "output stages fit");
+    epilogue(tc, wm, wn, lane, acc,
+             reinterpret_cast<float*>(lds + (st ^ 1) * C::STAGE) + wave * RowPasses<C>::FLOATS);
+    lds_barrier();
   }
-  if (wave < 4) __builtin_amdgcn_s_barrier();
   vm_wait<0>();
 }
 

@@ -28,7 +28,7 @@ struct GArgs {
   int G;
   int n, k;  // output and input features
   int out_f32, accumulate;
-  int vec;   // outputs can be stored four at a time
+  int vec;   // rows of outputs can be stored eight at a time
 };
 
 // Tile tables of the groups from the device offsets, clamped to an ascending
@@ -131,37 +131,37 @@ __device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, i
   return c;
 }
 
-// Stores (or adds) one value, or four adjacent ones of a row.
-__device__ __forceinline__ void put1(const GArgs& a, int64_t at, float v) {
+// Stores eight adjacent values of a row, of which `cnt` exist.
+__device__ __forceinline__ void put8(const GArgs& a, int64_t at, int cnt, const float (&v)[8]) {
   if (a.out_f32) {
     float* p = static_cast<float*>(a.out) + at;
-    *p = a.accumulate ? *p + v : v;
-  } else {
-    static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
-  }
-}
-__device__ __forceinline__ void put4(const GArgs& a, int64_t at, int cnt, float v0, float v1,
-                                     float v2, float v3) {
-  if (a.vec && cnt >= 4) {
-    if (a.out_f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v0, v1, v2, v3);
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = pack_bf16x4(v0, v1, v2, v3);
-    return;
-  }
-  const float v[4] = {v0, v1, v2, v3};
+    if (a.vec && cnt >= 8) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < cnt) put1(a, at + j, v[j]);
+      for (int j = 0; j < 8; ++j)
+        if (j < cnt) p[j] = v[j];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+    if (a.vec && cnt >= 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cnt) p[j] = f32_to_bf16(v[j]);
+    }
+  }
 }
 
-// Output of a finished tile. Forward and dgrad hold the transposed tile (a
-// lane owns a row and runs of four columns), wgrad the tile itself (a lane
-// owns a column, so one register across the wave is two 128-byte row pieces
-// of fp32).
+// Output of a finished tile. Forward and dgrad hold the transposed tile and
+// store rows through LDS; wgrad holds the tile itself (a lane owns a column, so
+// one register across the wave is two 128-byte row pieces of fp32).
 template <class C, int MODE>
 __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int wm, int wn, int lane,
-                                           f32x16_t (&acc)[C::MI][C::NJ]) {
+                                           f32x16_t (&acc)[C::MI][C::NJ], float* stage) {
   if constexpr (MODE == kWgrad) {
     const int64_t base = int64_t(c.g) * a.n * a.k;
 #pragma unroll
@@ -182,21 +182,19 @@ __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int w
         }
     }
   } else {
+    using P = RowPasses<C>;
     const int N = MODE == kForward ? a.n : a.k;
+    const int col = c.n * C::BN + wn * C::WN + P::col(lane);
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) {
-      const int r = c.m * C::BM + wm * C::WM + mi * 32 + (lane & 31);
-      if (r >= c.rows) continue;
-      const int64_t at = (c.row0 + r) * a.ldo;
+      P::put(stage, lane, acc[mi]);
 #pragma unroll
-      for (int nj = 0; nj < C::NJ; ++nj)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = c.n * C::BN + wn * C::WN + nj * 32 + 8 * q + 4 * (lane >> 5);
-          if (col >= N) continue;
-          const f32x16_t& v = acc[mi][nj];
-          put4(a, at + col, N - col, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
+      for (int p = 0; p < P::N; ++p) {
+        float v[8];
+        P::get(stage, lane, p, v);
+        const int r = c.m * C::BM + wm * C::WM + mi * 32 + P::row(p, lane);
+        if (r < c.rows && col < N) put8(a, (c.row0 + r) * a.ldo + col, N - col, v);
+      }
     }
   }
 }
@@ -226,7 +224,9 @@ template <int MODE>
 __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
   using C = TileAny;
   constexpr bool AKM = MODE == kWgrad, BKM = MODE != kForward, SWAP = MODE != kWgrad;
+  // after the k-loop the stages are free and hold the output rows
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  static_assert(C::NWAVES * RowPasses<C>::FLOATS * 2 <= C::LDS_ELEMS, "output stages fit");
   __shared__ GroupTables gt;
   const int N = MODE == kForward ? a.n : a.k, M_w = a.n;
   const int tn = (N + C::BN - 1) / C::BN;
@@ -302,7 +302,9 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
       if (ks + 1 < nk) stash(st ^ 1);
       __syncthreads();
     }
-    store_tile<C, MODE>(a, c, wm, wn, lane, acc);
+    store_tile<C, MODE>(a, c, wm, wn, lane, acc,
+                        reinterpret_cast<float*>(lds) + wave * RowPasses<C>::FLOATS);
+    __syncthreads();
   }
 }
 
@@ -313,7 +315,8 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
 template <class C, int MODE, bool PHASED>
 __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   constexpr bool AKM = MODE == kWgrad, BKM = MODE != kForward, SWAP = MODE != kWgrad;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  constexpr int kStageElems = PHASED || MODE == kWgrad ? 0 : C::NWAVES * RowPasses<C>::FLOATS * 2;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS + kStageElems];
   __shared__ GroupTables gt;
   const int N = MODE == kForward ? a.n : a.k;
   const int tn = (N + C::BN - 1) / C::BN;
@@ -361,8 +364,8 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
         return st(0);
     }
     __device__ void operator()(int tile, int wm, int wn, int lane,
-                               f32x16_t (&acc)[C::MI][C::NJ]) const {
-      store_tile<C, MODE>(a, tile_of<MODE, C::BM, C::BN>(a, gt, tile), wm, wn, lane, acc);
+                               f32x16_t (&acc)[C::MI][C::NJ], float* stage) const {
+      store_tile<C, MODE>(a, tile_of<MODE, C::BM, C::BN>(a, gt, tile), wm, wn, lane, acc, stage);
     }
   } ep{a, gt, steps};
   if constexpr (PHASED)
@@ -446,7 +449,7 @@ hipError_t launch_grouped(const GroupedArgs& p, hipStream_t s) {
     a.ldb = p.ld_k;
     a.ldo = p.k;
   }
-  a.vec = !a.accumulate && a.ldo % 4 == 0 && on16(p.out);
+  a.vec = a.ldo % 8 == 0 && on16(p.out);
   if (p.mode == kWgrad)
     return launch_mode<kWgrad>(a, base && a.lda % 8 == 0 && a.ldb % 8 == 0, s);
   if (p.rows == 0) return hipSuccess;

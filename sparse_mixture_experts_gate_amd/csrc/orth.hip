@@ -90,6 +90,14 @@ struct PrepArgs {
 
 __device__ __forceinline__ float load_grad(const float* p) { return *p; }
 __device__ __forceinline__ float load_grad(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float4 load_grad4(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ float4 load_grad4(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
 
 // Momentum, and the partial sums of squares of u (fp64: any scale of the
 // gradient squares without overflow or underflow). Block (chunk, matrix).
@@ -98,17 +106,36 @@ __global__ __launch_bounds__(256) void orth_sum_kernel(PrepArgs a) {
   __shared__ double red[4];
   const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.y;
   const T* g = static_cast<const T*>(a.grad) + mat * el;
-  const int64_t per = ((el + a.o.chunks - 1) / a.o.chunks + 255) / 256 * 256;
+  const int64_t per = ((el + a.o.chunks - 1) / a.o.chunks + 1023) / 1024 * 1024;
   const int64_t e0 = int64_t(blockIdx.x) * per, e1 = min(e0 + per, el);
   double s = 0.0;
-  for (int64_t i = e0 + threadIdx.x; i < e1; i += 256) {
-    float u = load_grad(g + i);
+  auto one = [&](float u, float mi, float& mo) {
     if constexpr (MOM) {
-      const float mo = a.momentum * a.m_in[mat * el + i] + u;
-      a.m_out[mat * el + i] = mo;
+      mo = a.momentum * mi + u;
       u = a.nesterov ? u + a.momentum * mo : mo;
     }
     s += double(u) * u;
+  };
+  const float* mi = MOM ? a.m_in + mat * el : nullptr;
+  float* mo = MOM ? a.m_out + mat * el : nullptr;
+  if (el % 4 == 0) {  // every matrix starts on a vector
+#pragma unroll 4
+    for (int64_t i = e0 + threadIdx.x * 4; i < e1; i += 1024) {
+      const float4 u = load_grad4(g + i);
+      float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = m;
+      if constexpr (MOM) m = *reinterpret_cast<const float4*>(mi + i);
+      one(u.x, m.x, o.x);
+      one(u.y, m.y, o.y);
+      one(u.z, m.z, o.z);
+      one(u.w, m.w, o.w);
+      if constexpr (MOM) *reinterpret_cast<float4*>(mo + i) = o;
+    }
+  } else {
+    for (int64_t i = e0 + threadIdx.x; i < e1; i += 256) {
+      float o = 0.0f;
+      one(load_grad(g + i), MOM ? mi[i] : 0.0f, o);
+      if constexpr (MOM) mo[i] = o;
+    }
   }
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k, 64);
@@ -154,6 +181,37 @@ __global__ __launch_bounds__(256) void orth_scale_kernel(PrepArgs a) {
   _Float16* lo = reinterpret_cast<_Float16*>(ws + a.o.lo);
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // of X
+  if (!TALL && a.o.m % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + k * 16 + (threadIdx.x >> 4), c = c0 + (threadIdx.x & 15) * 4;
+      if (r >= a.o.n) continue;  // c < mp: blocks cover whole k-steps
+      float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c < a.o.m) {
+        const int64_t i = int64_t(r) * a.cols + c;
+        u = load_grad4(g + i);
+        if constexpr (MOM) {
+          const float4 m = *reinterpret_cast<const float4*>(mo + i);
+          u = a.nesterov ? make_float4(u.x + a.momentum * m.x, u.y + a.momentum * m.y,
+                                       u.z + a.momentum * m.z, u.w + a.momentum * m.w)
+                         : m;
+        }
+      }
+      f16x4_t h, l;
+      _Float16 hh, ll;
+      split_x(u.x * scale, hh, ll);
+      h[0] = hh, l[0] = ll;
+      split_x(u.y * scale, hh, ll);
+      h[1] = hh, l[1] = ll;
+      split_x(u.z * scale, hh, ll);
+      h[2] = hh, l[2] = ll;
+      split_x(u.w * scale, hh, ll);
+      h[3] = hh, l[3] = ll;
+      *reinterpret_cast<f16x4_t*>(hi + int64_t(r) * a.o.mp + c) = h;
+      *reinterpret_cast<f16x4_t*>(lo + int64_t(r) * a.o.mp + c) = l;
+    }
+    return;
+  }
   if constexpr (TALL) {
     for (int i = ty; i < 64; i += 4) {  // row c0 + i of u, columns r0 ..
       const int ur = c0 + i, uc = r0 + tx;
@@ -223,7 +281,8 @@ __device__ __forceinline__ OTile orth_tile(const StepArgs& a, int tile) {
 template <class C, int KIND, bool TALL, bool PHASED>
 __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a, int total) {
   constexpr bool BKM = KIND >= kApply;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
+  constexpr int kStageElems = PHASED ? 0 : C::NWAVES * RowPasses<C>::FLOATS * 2;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS + kStageElems];
   const int first = xcd_logical_block(blockIdx.x, gridDim.x);
   if (first >= total) return;
   const int K = KIND == kGram ? a.o.mp : a.o.np;
@@ -250,105 +309,122 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
     const StepArgs& a;
     int nk;
     __device__ int k_steps(int) const { return nk; }
-    __device__ void operator()(int tile, int wm, int wn, int lane,
-                               f32x16_t (&acc)[C::MI][C::NJ]) const {
+    __device__ void operator()(int tile, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
+                               float* stage) const {
+      using P = RowPasses<C>;
       const OTile t = orth_tile<C, KIND>(a, tile);
       char* ws = a.ws + t.mat * a.o.bytes;
-      const int n = a.o.n, np = a.o.np, mp = a.o.mp;
-      const float* D = reinterpret_cast<const float*>(ws + a.o.d);
-      const float* Q = reinterpret_cast<const float*>(ws + a.o.q);
+      const int n = a.o.n, np = a.o.np, mp = a.o.mp, m = a.o.m;
+      const int row0 = t.m * C::BM + wm * C::WM, col0 = t.n * C::BN + wn * C::WN;
+      const int col = col0 + P::col(lane);
+      float* D = reinterpret_cast<float*>(ws + a.o.d);
+      float* Q = reinterpret_cast<float*>(ws + a.o.q);
+      const _Float16* R = reinterpret_cast<const _Float16*>(ws + a.o.r);
 #pragma unroll
       for (int mi = 0; mi < C::MI; ++mi) {
-        const int row = t.m * C::BM + wm * C::WM + mi * 32 + (lane & 31);
-        // rows n .. np - 1 of a symmetric product only put their zeros into
-        // the padding columns of the mirrored tile
-        if (row >= (KIND < kApply ? np : n)) continue;
+        P::put(stage, lane, acc[mi]);
+        if constexpr (KIND == kGram || KIND == kSquare) {
+          _Float16* dst = reinterpret_cast<_Float16*>(ws + (KIND == kGram ? a.o.r : a.o.s));
+          // eight outputs from the products v: rows `row`, columns `c` (both
+          // below n, or in the padding, where everything is zero)
+          auto finish = [&](float (&v)[8], int row, int c, bool diag) {
+            f16x8_t o;
+            if constexpr (KIND == kGram) {
 #pragma unroll
-        for (int nj = 0; nj < C::NJ; ++nj)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int col = t.n * C::BN + wn * C::WN + nj * 32 + 8 * g + 4 * (lane >> 5);
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = acc[mi][nj][4 * g + j];
-            if constexpr (KIND == kGram || KIND == kSquare) {
-              if (col >= np) continue;
-              f16x4_t o;
-              if constexpr (KIND == kGram) {
-                float* d = reinterpret_cast<float*>(ws + a.o.d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float x = v[j] * (1.0f / (kScaleX * kScaleX));
-                  if (col + j == row && row < n) d[row] = x;
-                  o[j] = static_cast<_Float16>(col + j == row ? 0.0f : x * kScaleR);
-                }
-              } else {
-                f16x4_t r4 = {};
-                float di = 0.0f;
-                if (row < n) {
-                  r4 = *reinterpret_cast<const f16x4_t*>(ws + a.o.r +
-                                                         (int64_t(row) * np + col) * 2);
-                  di = D[row];
-                }
-                float* q = reinterpret_cast<float*>(ws + a.o.q);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float rij = static_cast<float>(r4[j]) * (1.0f / kScaleR);
-                  const float dj = col + j < n ? D[col + j] : 0.0f;
-                  const float rr = v[j] * (1.0f / (kScaleR * kScaleR));
-                  if (col + j == row && row < n) q[row] = kB * di + kC * (rr + di * di);
-                  const float s = kB * rij + kC * (rr + (di + dj) * rij);
-                  o[j] = static_cast<_Float16>(col + j == row ? 0.0f : s * kScaleS);
-                }
-              }
-              _Float16* dst = reinterpret_cast<_Float16*>(ws + (KIND == kGram ? a.o.r : a.o.s));
-              if (row < n) *reinterpret_cast<f16x4_t*>(dst + int64_t(row) * np + col) = o;
-              if (t.m != t.n) {  // the mirrored tile
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (col + j < n) dst[int64_t(col + j) * np + row] = o[j];
+              for (int j = 0; j < 8; ++j) {
+                const float x = v[j] * (1.0f / (kScaleX * kScaleX));
+                if (diag && c + j == row) D[row] = x;
+                o[j] = static_cast<_Float16>(c + j == row ? 0.0f : x * kScaleR);
               }
             } else {
-              if (col >= mp) continue;
-              const int64_t at = int64_t(row) * mp + col;
-              const f16x4_t h = *reinterpret_cast<const f16x4_t*>(ws + a.hi_in + at * 2);
-              const f16x4_t l = *reinterpret_cast<const f16x4_t*>(ws + a.o.lo + at * 2);
-              const float f = kA + Q[row];
-              float x[4];
+              const f16x8_t r8 = *reinterpret_cast<const f16x8_t*>(R + int64_t(row) * np + c);
+              const float di = D[row];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                x[j] = f * (static_cast<float>(h[j]) + static_cast<float>(l[j]) * (1.0f / kScaleLo)) +
-                       v[j] * (1.0f / kScaleS);
-              if constexpr (KIND == kApply) {
-                f16x4_t ho, lo;
+              for (int j = 0; j < 8; ++j) {
+                const float rij = static_cast<float>(r8[j]) * (1.0f / kScaleR);
+                const float dj = c + j < n ? D[c + j] : 0.0f;
+                const float rr = v[j] * (1.0f / (kScaleR * kScaleR));
+                if (diag && c + j == row) Q[row] = kB * di + kC * (rr + di * di);
+                const float x = kB * rij + kC * (rr + (di + dj) * rij);
+                o[j] = static_cast<_Float16>(c + j == row ? 0.0f : x * kScaleS);
+              }
+            }
+            *reinterpret_cast<f16x8_t*>(dst + int64_t(row) * np + c) = o;
+          };
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  _Float16 hh, ll;
-                  split_x(x[j], hh, ll);
-                  ho[j] = hh;
-                  lo[j] = ll;
-                }
-                *reinterpret_cast<f16x4_t*>(ws + a.hi_out + at * 2) = ho;
-                *reinterpret_cast<f16x4_t*>(ws + a.o.lo + at * 2) = lo;
+          for (int p = 0; p < P::N; ++p) {
+            float v[8];
+            P::get(stage, lane, p, v);
+            const int row = row0 + mi * 32 + P::row(p, lane);
+            if (row < n && col < np) finish(v, row, col, t.m == t.n);
+          }
+          if (t.m != t.n) {
+            // the mirrored tile: rows are this tile's columns, 32 of its
+            // columns (this pass's rows) at a time, 8 per lane
+#pragma unroll
+            for (int p = 0; p < C::WN / 16; ++p) {
+              const int i = p * 16 + (lane & 15), k = (lane >> 4) * 8;
+              float v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                v[j] = stage[(k + j) * C::WN + (((i >> 2) ^ ((k + j) & (P::CPR - 1))) << 2) + (i & 3)];
+              const int row = col0 + i, c = row0 + mi * 32 + k;
+              if (row < n && c < np) finish(v, row, c, false);
+            }
+          }
+        } else {
+          f16x8_t h[P::N], l[P::N];
+#pragma unroll
+          for (int p = 0; p < P::N; ++p) {
+            const int row = row0 + mi * 32 + P::row(p, lane);
+            const int64_t at = (int64_t(row < n ? row : n - 1) * mp + (col < mp ? col : 0)) * 2;
+            h[p] = *reinterpret_cast<const f16x8_t*>(ws + a.hi_in + at);
+            l[p] = *reinterpret_cast<const f16x8_t*>(ws + a.o.lo + at);
+          }
+#pragma unroll
+          for (int p = 0; p < P::N; ++p) {
+            float v[8];
+            P::get(stage, lane, p, v);
+            const int row = row0 + mi * 32 + P::row(p, lane);
+            if (row >= n || col >= mp) continue;
+            const float f = kA + Q[row];
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[j] = f * (static_cast<float>(h[p][j]) +
+                          static_cast<float>(l[p][j]) * (1.0f / kScaleLo)) +
+                     v[j] * (1.0f / kScaleS);
+            if constexpr (KIND == kApply) {
+              f16x8_t ho, lo;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                _Float16 hh, ll;
+                split_x(x[j], hh, ll);
+                ho[j] = hh;
+                lo[j] = ll;
+              }
+              const int64_t at = (int64_t(row) * mp + col) * 2;
+              *reinterpret_cast<f16x8_t*>(ws + a.hi_out + at) = ho;
+              *reinterpret_cast<f16x8_t*>(ws + a.o.lo + at) = lo;
+            } else {
+              uint16_t* out = static_cast<uint16_t*>(a.out) + t.mat * n * int64_t(m);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] *= 1.0f / kScaleX;
+              if (!TALL && m % 8 == 0) {
+                if (col < m)
+                  *reinterpret_cast<uint4*>(out + int64_t(row) * m + col) =
+                      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
               } else {
-                const int m = a.o.m;
-                uint16_t* out = static_cast<uint16_t*>(a.out) + t.mat * n * int64_t(m);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= 1.0f / kScaleX;
-                if (!TALL && m % 4 == 0) {
-                  if (col < m)
-                    *reinterpret_cast<uint2*>(out + int64_t(row) * m + col) =
-                        pack_bf16x4(x[0], x[1], x[2], x[3]);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if (col + j < m)
-                      out[TALL ? int64_t(col + j) * n + row : int64_t(row) * m + col + j] =
-                          f32_to_bf16(x[j]);
-                }
+                for (int j = 0; j < 8; ++j)
+                  if (col + j < m)
+                    out[TALL ? int64_t(col + j) * n + row : int64_t(row) * m + col + j] =
+                        f32_to_bf16(x[j]);
               }
             }
           }
+        }
       }
     }
   } ep{a, K / BK};
