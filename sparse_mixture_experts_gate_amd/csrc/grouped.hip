@@ -240,10 +240,44 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
     const uint16_t* A = a.a + (MODE == kWgrad ? c.row0 : c.row0 + int64_t(c.m) * C::BM) * a.lda;
     const uint16_t* B = MODE == kWgrad ? a.b + c.row0 * a.ldb : a.b + int64_t(c.g) * a.n * a.k;
     const int a_rows = MODE == kWgrad ? a.n : c.rows - c.m * C::BM;
+    const uint16_t* Bt = MODE == kForward ? B + int64_t(c.n) * C::BN * a.ldb : B;
+    const int b_rows = a.n - c.n * C::BN;  // forward: rows of W_g from the tile's first
+    const int nk = (K + BK - 1) / BK;
     uint4 ra[C::A_LOADS], rb[C::B_LOADS];
-    // chunk p of the thread in k-step ks: LDS chunk p * NT + tid of its operand
-    auto get = [&](bool km, const uint16_t* P, int64_t ld, int rows, int col0, int width, int W,
-                   int p, int ks) -> uint4 {
+    // Element offset of the thread's chunk p in a k-step (LDS chunk p * NT +
+    // tid). k-contiguous: rows past the operand's last take that one (their
+    // outputs are not stored).
+    uint32_t oa[C::A_LOADS], ob[C::B_LOADS];
+    auto contig = [&](int p, int rows, int64_t ld) {
+      const int r = (tid >> 3) + p * C::RPP;
+      return static_cast<uint32_t>(min(r, rows - 1) * ld) + ((tid & 7) ^ ((r >> 1) & 7)) * 8;
+    };
+    auto kmajor = [&](int p, int W, int64_t ld, int col0, int width) {
+      const int cpr = W / 8, row = p * (C::NT / cpr) + tid / cpr;
+      const int col = col0 + ((tid % cpr) ^ (4 * (row & 3))) * 8;
+      return static_cast<uint32_t>(row * ld) + (col < width ? col : 0);
+    };
+#pragma unroll
+    for (int p = 0; p < C::A_LOADS; ++p)
+      oa[p] = AKM ? kmajor(p, C::BM, a.lda, c.m * C::BM, a.n) : contig(p, a_rows, a.lda);
+#pragma unroll
+    for (int p = 0; p < C::B_LOADS; ++p)
+      ob[p] = BKM ? kmajor(p, C::BN, a.ldb, c.n * C::BN, a.k) : contig(p, b_rows, a.ldb);
+    // A k-step before the last: whole chunks, no checks. A k-major chunk may run
+    // up to 7 elements past its row's end into the next row (columns whose
+    // outputs are not stored): the last row is in the last k-step, and with
+    // rows of fewer than 8 elements every step is checked.
+    const bool inner = (!AKM || a.lda >= 8) && (!BKM || a.ldb >= 8);
+    auto fetch_inner = [&](int ks) {
+      const uint16_t* pa = A + (AKM ? int64_t(ks) * BK * a.lda : int64_t(ks) * BK);
+      const uint16_t* pb = Bt + (BKM ? int64_t(ks) * BK * a.ldb : int64_t(ks) * BK);
+#pragma unroll
+      for (int p = 0; p < C::A_LOADS; ++p) __builtin_memcpy(&ra[p], pa + oa[p], 16);
+#pragma unroll
+      for (int p = 0; p < C::B_LOADS; ++p) __builtin_memcpy(&rb[p], pb + ob[p], 16);
+    };
+    auto checked = [&](bool km, const uint16_t* P, int64_t ld, int rows, int col0, int width, int W,
+                       int p, int ks) -> uint4 {
       if (km) {
         const int cpr = W / 8, row = p * (C::NT / cpr) + tid / cpr;
         const int kr = ks * BK + row;
@@ -255,14 +289,16 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
       return chunk_any(P + r * ld + k0, r < rows ? K - k0 : 0);
     };
     auto fetch = [&](int ks) {
+      if (inner && ks + 1 < nk) {
+        fetch_inner(ks);
+        return;
+      }
 #pragma unroll
       for (int p = 0; p < C::A_LOADS; ++p)
-        ra[p] = get(AKM, A, a.lda, a_rows, c.m * C::BM, a.n, C::BM, p, ks);
+        ra[p] = checked(AKM, A, a.lda, a_rows, c.m * C::BM, a.n, C::BM, p, ks);
 #pragma unroll
       for (int p = 0; p < C::B_LOADS; ++p)
-        rb[p] = BKM ? get(true, B, a.ldb, 0, c.n * C::BN, a.k, C::BN, p, ks)
-                    : get(false, B + int64_t(c.n) * C::BN * a.ldb, a.ldb, a.n - c.n * C::BN, 0, 0,
-                          C::BN, p, ks);
+        rb[p] = checked(BKM, Bt, a.ldb, b_rows, c.n * C::BN, a.k, C::BN, p, ks);
     };
     auto stash = [&](int st) {
       uint16_t* s = lds + st * C::STAGE;
@@ -275,7 +311,6 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
     };
     f32x16_t acc[C::MI][C::NJ];
     zero_acc<C>(acc);
-    const int nk = (K + BK - 1) / BK;
     if (nk > 0) {
       fetch(0);
       stash(0);
