@@ -109,12 +109,22 @@ typedef struct moe_grouped_desc {
   int32_t accumulate;
 } moe_grouped_desc;
 
+enum { MOE_GROUPED_FORWARD = 0, MOE_GROUPED_DGRAD = 1, MOE_GROUPED_WGRAD = 2 };
+
+/* Bytes of workspace for the product `op`: partial sums where the outputs are
+ * too few to occupy the GPU, 0 otherwise (ws may then be NULL). Host only. */
+moe_status moe_grouped_gemm_workspace_size(const moe_grouped_desc* desc, int32_t op,
+                                           size_t* bytes);
+
 moe_status moe_grouped_gemm(const moe_grouped_desc* desc, const void* x, const void* w,
-                            const int32_t* offsets, void* y, hipStream_t stream);
+                            const int32_t* offsets, void* y, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
 moe_status moe_grouped_gemm_dgrad(const moe_grouped_desc* desc, const void* dy, const void* w,
-                                  const int32_t* offsets, void* dx, hipStream_t stream);
+                                  const int32_t* offsets, void* dx, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
 moe_status moe_grouped_gemm_wgrad(const moe_grouped_desc* desc, const void* dy, const void* x,
-                                  const int32_t* offsets, float* dw, hipStream_t stream);
+                                  const int32_t* offsets, float* dw, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
 
 /* ---- Orthogonalized update of weight matrices
  *

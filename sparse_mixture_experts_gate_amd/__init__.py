@@ -8,8 +8,9 @@ from ._lib import (MOE_DT_BF16, MOE_DT_F32, MOE_DT_FP8_E4M3, MoeError, MoeLayerD
                    moe_backward, moe_backward_workspace_size, moe_forward_train,
                    moe_seq_balance_loss, moe_seq_balance_workspace_size,
                    moe_backward_fp8, moe_transpose_fp8_blocks)
-from ._ops import (MoeGroupedDesc, MoeNormDesc, MoeOrthDesc, moe_grouped_gemm,
-                   moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_layernorm_backward,
+from ._ops import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MoeGroupedDesc,
+                   MoeNormDesc, MoeOrthDesc, moe_grouped_gemm, moe_grouped_gemm_dgrad,
+                   moe_grouped_gemm_wgrad, moe_grouped_gemm_workspace_size, moe_layernorm_backward,
                    moe_layernorm_backward_workspace_size, moe_layernorm_forward,
                    moe_orthogonalize, moe_orthogonalize_workspace_size)
 from .blocks import GroupedLinear, LayerNorm, Muon
@@ -25,7 +26,8 @@ __all__ = [
     "make_tokens", "moe_backward", "moe_backward_workspace_size", "moe_forward_train",
     "moe_seq_balance_loss", "moe_seq_balance_workspace_size", "moe_backward_fp8",
     "moe_transpose_fp8_blocks",
-    "MoeGroupedDesc", "MoeNormDesc", "MoeOrthDesc", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+    "MOE_GROUPED_DGRAD", "MOE_GROUPED_FORWARD", "MOE_GROUPED_WGRAD",
+    "moe_grouped_gemm_workspace_size", "MoeGroupedDesc", "MoeNormDesc", "MoeOrthDesc", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
     "moe_grouped_gemm_wgrad", "moe_layernorm_backward", "moe_layernorm_backward_workspace_size",
     "moe_layernorm_forward", "moe_orthogonalize", "moe_orthogonalize_workspace_size",
     "GroupedLinear", "LayerNorm", "Muon",

@@ -50,9 +50,10 @@ def lib() -> ctypes.CDLL:
             "moe_layernorm_forward": [N, P, P, P, P, P, P, P, P, P],
             "moe_layernorm_backward_workspace_size": [N, ctypes.POINTER(Z)],
             "moe_layernorm_backward": [N, P, P, P, P, P, P, P, P, P, P, Z, P],
-            "moe_grouped_gemm": [G, P, P, P, P, P],
-            "moe_grouped_gemm_dgrad": [G, P, P, P, P, P],
-            "moe_grouped_gemm_wgrad": [G, P, P, P, P, P],
+            "moe_grouped_gemm_workspace_size": [G, ctypes.c_int32, ctypes.POINTER(Z)],
+            "moe_grouped_gemm": [G, P, P, P, P, P, Z, P],
+            "moe_grouped_gemm_dgrad": [G, P, P, P, P, P, Z, P],
+            "moe_grouped_gemm_wgrad": [G, P, P, P, P, P, Z, P],
             "moe_orthogonalize_workspace_size": [O, ctypes.POINTER(Z)],
             "moe_orthogonalize": [O, P, P, P, P, P, Z, P],
         }
@@ -71,13 +72,16 @@ def _p(t) -> int | None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor or None")
-    if t.dim() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+    if not t.is_contiguous() and t.stride(-1) != 1:
         raise ValueError("tensors passed to the library must have contiguous columns")
     return t.data_ptr()
 
 
 def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    """Handle of a torch stream, or of the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _nbytes(t) -> int:
@@ -105,19 +109,31 @@ def moe_layernorm_backward(desc, dy, x, weight, mean, rstd, dresidual, dx, dweig
              "moe_layernorm_backward")
 
 
-def moe_grouped_gemm(desc, x, w, offsets, y, stream=None):
-    L._check(lib().moe_grouped_gemm(ctypes.byref(desc), _p(x), _p(w), _p(offsets), _p(y),
-                                    _stream(stream)), "moe_grouped_gemm")
+MOE_GROUPED_FORWARD, MOE_GROUPED_DGRAD, MOE_GROUPED_WGRAD = 0, 1, 2
 
 
-def moe_grouped_gemm_dgrad(desc, dy, w, offsets, dx, stream=None):
+def moe_grouped_gemm_workspace_size(desc, op) -> int:
+    n = ctypes.c_size_t(0)
+    L._check(lib().moe_grouped_gemm_workspace_size(ctypes.byref(desc), op, ctypes.byref(n)),
+             "moe_grouped_gemm_workspace_size")
+    return n.value
+
+
+def moe_grouped_gemm(desc, x, w, offsets, y, ws=None, stream=None):
+    L._check(lib().moe_grouped_gemm(ctypes.byref(desc), _p(x), _p(w), _p(offsets), _p(y), _p(ws),
+                                    _nbytes(ws), _stream(stream)), "moe_grouped_gemm")
+
+
+def moe_grouped_gemm_dgrad(desc, dy, w, offsets, dx, ws=None, stream=None):
     L._check(lib().moe_grouped_gemm_dgrad(ctypes.byref(desc), _p(dy), _p(w), _p(offsets), _p(dx),
-                                          _stream(stream)), "moe_grouped_gemm_dgrad")
+                                          _p(ws), _nbytes(ws), _stream(stream)),
+             "moe_grouped_gemm_dgrad")
 
 
-def moe_grouped_gemm_wgrad(desc, dy, x, offsets, dw, stream=None):
+def moe_grouped_gemm_wgrad(desc, dy, x, offsets, dw, ws=None, stream=None):
     L._check(lib().moe_grouped_gemm_wgrad(ctypes.byref(desc), _p(dy), _p(x), _p(offsets), _p(dw),
-                                          _stream(stream)), "moe_grouped_gemm_wgrad")
+                                          _p(ws), _nbytes(ws), _stream(stream)),
+             "moe_grouped_gemm_wgrad")
 
 
 def moe_orthogonalize_workspace_size(desc) -> int:

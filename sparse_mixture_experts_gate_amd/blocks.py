@@ -13,26 +13,32 @@ from . import _ops as O
 _DT = {torch.float32: L.MOE_DT_F32, torch.bfloat16: L.MOE_DT_BF16}
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocate on the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, d: int) -> int:
     """Row stride of a row matrix [n, d], checked."""
-    if t.dtype != dtype or t.shape != (n, d):
+    if t.dtype is not dtype or t.shape != (n, d):
         raise ValueError(f"{name}: expected {dtype} [{n}, {d}], got {t.dtype} {list(t.shape)}")
-    if d > 1 and n and t.stride(1) != 1:
-        raise ValueError(f"{name}: columns must be contiguous")
-    if n <= 1:
+    if n <= 1 or t.is_contiguous():
+        if d > 1 and n and t.stride(1) != 1:
+            raise ValueError(f"{name}: columns must be contiguous")
         return d
-    if t.stride(0) < d:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {d})")
-    return t.stride(0)
+    rows, cols = t.stride()
+    if d > 1 and cols != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    if rows < d:
+        raise ValueError(f"{name}: rows overlap (stride {rows} < {d})")
+    return rows
 
 
 def _vector(t, name: str, dtype: torch.dtype, n: int) -> None:
-    if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError(f"{name}: expected contiguous {dtype} [{n}], got {t.dtype} "
                          f"{list(t.shape)}")
 
@@ -59,15 +65,18 @@ class LayerNorm:
                  eps: float = 1e-5):
         self.weight, self.bias, self.eps = weight, bias, eps
         self._ws = _Workspace()
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _vector(t, name, torch.float32, t.numel())
+        self.dims = {t.numel() for t in (weight, bias) if t is not None}
 
     def _desc(self, x: torch.Tensor) -> O.MoeNormDesc:
         if x.dim() != 2 or x.dtype not in _DT:
             raise ValueError(f"x: expected bf16 or fp32 [n, d], got {x.dtype} {list(x.shape)}")
         n, d = x.shape
-        _vector(self.weight, "weight", torch.float32, d)
-        _vector(self.bias, "bias", torch.float32, d)
-        return O.MoeNormDesc(n=n, d=d, dtype=_DT[x.dtype], eps=self.eps,
-                             ld_x=_rows(x, "x", x.dtype, n, d))
+        if self.dims - {d}:
+            raise ValueError(f"x: rows of {d} values, weight and bias have {sorted(self.dims)}")
+        return O.MoeNormDesc(n, d, _DT[x.dtype], self.eps, _rows(x, "x", x.dtype, n, d), 0, 0, 0)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 stream=None) -> dict:
@@ -79,10 +88,10 @@ class LayerNorm:
         if residual is not None:
             desc.ld_r = _rows(residual, "residual", x.dtype, n, d)
         with _on(stream):
-            y = torch.empty(n, d, dtype=x.dtype, device=x.device)
-            total = torch.empty_like(y) if residual is not None else None
-            mean = torch.empty(n, dtype=torch.float32, device=x.device)
-            rstd = torch.empty_like(mean)
+            y = x.new_empty(n, d)
+            total = x.new_empty(n, d) if residual is not None else None
+            mean = x.new_empty(n, dtype=torch.float32)
+            rstd = x.new_empty(n, dtype=torch.float32)
         O.moe_layernorm_forward(desc, x, residual, self.weight, self.bias, y, total, mean, rstd,
                                 stream)
         return {"y": y, "mean": mean, "rstd": rstd, "sum": x if residual is None else total}
@@ -120,6 +129,13 @@ class GroupedLinear:
                              f"{weight.dtype} {list(weight.shape)}")
         self.weight = weight
 
+    _ws = _Workspace()  # partial sums of small products, shared by all maps of a stream
+
+    @staticmethod
+    def _workspace(desc, op, device, stream):
+        need = O.moe_grouped_gemm_workspace_size(desc, op)
+        return GroupedLinear._ws.get(need, device, stream) if need else None
+
     @staticmethod
     def _desc(rows, groups, n, k, offsets, out_dtype=torch.float32) -> O.MoeGroupedDesc:
         _vector(offsets, "offsets", torch.int32, groups + 1)
@@ -135,7 +151,8 @@ class GroupedLinear:
         desc.ld_k = _rows(x, "x", torch.bfloat16, x.shape[0], k)
         with _on(stream):
             y = torch.empty(x.shape[0], n, dtype=out_dtype, device=x.device)
-        O.moe_grouped_gemm(desc, x, self.weight, offsets, y, stream)
+            ws = self._workspace(desc, O.MOE_GROUPED_FORWARD, x.device, stream)
+        O.moe_grouped_gemm(desc, x, self.weight, offsets, y, ws, stream)
         return y
 
     def input_grad(self, dy: torch.Tensor, offsets: torch.Tensor, out_dtype=torch.bfloat16,
@@ -146,7 +163,8 @@ class GroupedLinear:
         desc.ld_n = _rows(dy, "dy", torch.bfloat16, dy.shape[0], n)
         with _on(stream):
             dx = torch.empty(dy.shape[0], k, dtype=out_dtype, device=dy.device)
-        O.moe_grouped_gemm_dgrad(desc, dy, self.weight, offsets, dx, stream)
+            ws = self._workspace(desc, O.MOE_GROUPED_DGRAD, dy.device, stream)
+        O.moe_grouped_gemm_dgrad(desc, dy, self.weight, offsets, dx, ws, stream)
         return dx
 
     @staticmethod
@@ -160,13 +178,15 @@ class GroupedLinear:
         desc.ld_n = _rows(dy, "dy", torch.bfloat16, rows, n)
         desc.ld_k = _rows(x, "x", torch.bfloat16, rows, k)
         desc.accumulate = into is not None
-        if into is None:
-            with _on(stream):
-                into = torch.empty(G, n, k, dtype=torch.float32, device=dy.device)
-        elif into.dtype != torch.float32 or into.shape != (G, n, k) or not into.is_contiguous():
+        if into is not None and (into.dtype != torch.float32 or into.shape != (G, n, k)
+                                 or not into.is_contiguous()):
             raise ValueError(f"into: expected contiguous fp32 [{G}, {n}, {k}], got {into.dtype} "
                              f"{list(into.shape)}")
-        O.moe_grouped_gemm_wgrad(desc, dy, x, offsets, into, stream)
+        with _on(stream):
+            if into is None:
+                into = torch.empty(G, n, k, dtype=torch.float32, device=dy.device)
+            ws = GroupedLinear._workspace(desc, O.MOE_GROUPED_WGRAD, dy.device, stream)
+        O.moe_grouped_gemm_wgrad(desc, dy, x, offsets, into, ws, stream)
         return into
 
 

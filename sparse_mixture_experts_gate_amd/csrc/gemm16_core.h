@@ -77,6 +77,7 @@ template <class C, int W, int LOADS>
 __device__ __forceinline__ void kmajor_operand(i32x4_t& rs, uint32_t (&o)[LOADS], uint64_t& b,
                                                int64_t& left, uint32_t& step, const void* base,
                                                int col0, uint32_t ld_bytes, int64_t bytes) {
+  static_assert(W >= 128, "the row swizzle of a k-major stage spans 16 chunks");
   kmajor_offsets<W, LOADS, C::NT>(o, col0, ld_bytes);
   b = reinterpret_cast<uint64_t>(base);
   left = bytes;

@@ -4,6 +4,8 @@
 //
 // One launch per call: every workgroup builds the groups' tile table from the
 // device offsets itself, so no planning kernel runs first.
+#include <cmath>
+
 #include "device_common.h"
 #include "gemm16_core.h"
 #include "internal.h"
@@ -29,7 +31,21 @@ struct GArgs {
   int n, k;  // output and input features
   int out_f32, accumulate;
   int vec;   // rows of outputs can be stored eight at a time
+  // The contraction is split over `splits` workgroups per tile: split s writes
+  // fp32 partial sums at out + s * split_stride, which grouped_finish_kernel
+  // adds in split order (one split: the output itself).
+  int splits;
+  int64_t split_stride;
 };
+
+// k-steps [k0, k1) of split s.
+struct KRange {
+  int k0, k1;
+};
+__device__ __forceinline__ KRange split_range(int nk, int s, int splits) {
+  return {static_cast<int>(int64_t(nk) * s / splits),
+          static_cast<int>(int64_t(nk) * (s + 1) / splits)};
+}
 
 // Tile tables of the groups from the device offsets, clamped to an ascending
 // split of [0, rows]: t.off the row offsets, t.gnext[g] the first tile of
@@ -105,14 +121,16 @@ __device__ __forceinline__ int64_t span(int rows, uint32_t ld_bytes, int width) 
 }
 
 struct GTile {
-  int g, m, n;       // group, tile indices
+  int g, m, n, s;    // group, tile indices, split
   int64_t row0;      // first row of the group
   int rows;          // rows of the group
 };
 
 template <int MODE, int BM, int BN>
-__device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, int tile) {
+__device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, int unit) {
   GTile c;
+  const int tile = unit / a.splits;
+  c.s = unit - tile * a.splits;
   if constexpr (MODE == kWgrad) {
     const int tm = (a.n + BM - 1) / BM, tn = (a.k + BN - 1) / BN;
     c.g = tile / (tm * tn);
@@ -163,7 +181,7 @@ template <class C, int MODE>
 __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int wm, int wn, int lane,
                                            f32x16_t (&acc)[C::MI][C::NJ], float* stage) {
   if constexpr (MODE == kWgrad) {
-    const int64_t base = int64_t(c.g) * a.n * a.k;
+    const int64_t base = int64_t(c.g) * a.n * a.k + c.s * a.split_stride;
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
       const int col = c.n * C::BN + wn * C::WN + nj * 32 + (lane & 31);
@@ -193,7 +211,8 @@ __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int w
         float v[8];
         P::get(stage, lane, p, v);
         const int r = c.m * C::BM + wm * C::WM + mi * 32 + P::row(p, lane);
-        if (r < c.rows && col < N) put8(a, (c.row0 + r) * a.ldo + col, N - col, v);
+        if (r < c.rows && col < N)
+          put8(a, c.s * a.split_stride + (c.row0 + r) * a.ldo + col, N - col, v);
       }
     }
   }
@@ -231,7 +250,7 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
   const int N = MODE == kForward ? a.n : a.k, M_w = a.n;
   const int tn = (N + C::BN - 1) / C::BN;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, tn);
-  const int total = MODE == kWgrad ? a.G * ((M_w + C::BM - 1) / C::BM) * tn : gt.total;
+  const int total = (MODE == kWgrad ? a.G * ((M_w + C::BM - 1) / C::BM) * tn : gt.total) * a.splits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   for (int tile = xcd_logical_block(blockIdx.x, gridDim.x); tile < total; tile += gridDim.x) {
@@ -311,14 +330,15 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
     };
     f32x16_t acc[C::MI][C::NJ];
     zero_acc<C>(acc);
-    if (nk > 0) {
-      fetch(0);
-      stash(0);
+    const KRange kr = split_range(nk, c.s, a.splits);
+    if (kr.k0 < kr.k1) {
+      fetch(kr.k0);
+      stash(kr.k0 & 1);
     }
     __syncthreads();
-    for (int ks = 0; ks < nk; ++ks) {
+    for (int ks = kr.k0; ks < kr.k1; ++ks) {
       const int st = ks & 1;
-      if (ks + 1 < nk) fetch(ks + 1);
+      if (ks + 1 < kr.k1) fetch(ks + 1);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         bf16x8_t af[C::MI], bf[C::NJ];
@@ -334,7 +354,7 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
           for (int nj = 0; nj < C::NJ; ++nj)
             acc[mi][nj] = mma16<TypeBf16, SWAP>(af[mi], bf[nj], acc[mi][nj]);
       }
-      if (ks + 1 < nk) stash(st ^ 1);
+      if (ks + 1 < kr.k1) stash(st ^ 1);
       __syncthreads();
     }
     store_tile<C, MODE>(a, c, wm, wn, lane, acc,
@@ -356,53 +376,56 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   const int N = MODE == kForward ? a.n : a.k;
   const int tn = (N + C::BN - 1) / C::BN;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, tn);
-  const int total = MODE == kWgrad ? a.G * ((a.n + C::BM - 1) / C::BM) * tn : gt.total;
+  const int total =
+      (MODE == kWgrad ? a.G * ((a.n + C::BM - 1) / C::BM) * tn : gt.total) * a.splits;
   const int first = xcd_logical_block(blockIdx.x, gridDim.x);
   if (first >= total) return;
   const uint32_t lda = static_cast<uint32_t>(a.lda) * 2u, ldb = static_cast<uint32_t>(a.ldb) * 2u;
-  auto steps = [&](int rows) {
-    const int K = MODE == kForward ? a.k : MODE == kDgrad ? a.n : rows;
-    return K > BK ? (K + BK - 1) / BK : 1;
+  auto depth = [&](const GTile& c) { return MODE == kForward ? a.k : MODE == kDgrad ? a.n : c.rows; };
+  auto range = [&](const GTile& c) {
+    return split_range((depth(c) + BK - 1) / BK, c.s, a.splits);
   };
-  auto next_ops = [&](int tile, Ops16<C>& op) {
-    const GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, tile);
-    op.nk = steps(c.rows);
+  auto next_ops = [&](int unit, Ops16<C>& op) {
+    const GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, unit);
+    const KRange kr = range(c);
+    // an empty range (an empty group, or fewer k-steps than splits) reads one
+    // k-step of zeros
+    op.nk = max(kr.k1 - kr.k0, 1);
+    const int64_t k0 = int64_t(kr.k0) * BK;
+    const int K = static_cast<int>(min(int64_t(depth(c)), int64_t(kr.k1) * BK) - k0);
     if constexpr (MODE == kWgrad) {
-      kmajor_operand<C, C::BM>(op.ra, op.ao, op.base_a, op.left_a, op.step_a, a.a + c.row0 * a.lda,
-                               c.m * C::BM, lda, span(c.rows, lda, a.n));
-      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, a.b + c.row0 * a.ldb,
-                               c.n * C::BN, ldb, span(c.rows, ldb, a.k));
+      kmajor_operand<C, C::BM>(op.ra, op.ao, op.base_a, op.left_a, op.step_a,
+                               a.a + (c.row0 + k0) * a.lda, c.m * C::BM, lda, span(K, lda, a.n));
+      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b,
+                               a.b + (c.row0 + k0) * a.ldb, c.n * C::BN, ldb, span(K, ldb, a.k));
     } else {
-      const int K = MODE == kForward ? a.k : a.n;
       const int left = c.rows - c.m * C::BM;
-      kcontig_operand<C>(op.ra, op.ao, op.tail_a, a.a + (c.row0 + int64_t(c.m) * C::BM) * a.lda,
+      kcontig_operand<C>(op.ra, op.ao, op.tail_a, a.a + (c.row0 + int64_t(c.m) * C::BM) * a.lda + k0,
                          left, lda, span(min(left, C::BM), lda, K), K);
       const uint16_t* W = a.b + int64_t(c.g) * a.n * a.k;
       if constexpr (MODE == kForward) {
         const int nleft = a.n - c.n * C::BN;
-        kcontig_operand<C>(op.rb, op.bo, op.tail_b, W + int64_t(c.n) * C::BN * a.ldb, nleft, ldb,
-                           int64_t(min(nleft, C::BN)) * ldb, K);
+        kcontig_operand<C>(op.rb, op.bo, op.tail_b, W + int64_t(c.n) * C::BN * a.ldb + k0, nleft,
+                           ldb, span(min(nleft, C::BN), ldb, K), K);
       } else {
-        kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, W, c.n * C::BN, ldb,
-                                 int64_t(a.n) * ldb);
+        kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, W + k0 * a.ldb,
+                                 c.n * C::BN, ldb, span(K, ldb, a.k));
       }
     }
   };
   struct Epilogue {
     const GArgs& a;
     const GroupTables& gt;
-    decltype(steps)& st;
-    __device__ int k_steps(int tile) const {
-      if constexpr (MODE == kWgrad)
-        return st(tile_of<MODE, C::BM, C::BN>(a, gt, tile).rows);
-      else
-        return st(0);
+    decltype(range)& steps;
+    __device__ int k_steps(int unit) const {
+      const KRange r = steps(tile_of<MODE, C::BM, C::BN>(a, gt, unit));
+      return max(r.k1 - r.k0, 1);
     }
     __device__ void operator()(int tile, int wm, int wn, int lane,
                                f32x16_t (&acc)[C::MI][C::NJ], float* stage) const {
       store_tile<C, MODE>(a, tile_of<MODE, C::BM, C::BN>(a, gt, tile), wm, wn, lane, acc, stage);
     }
-  } ep{a, gt, steps};
+  } ep{a, gt, range};
   if constexpr (PHASED)
     stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
   else
@@ -424,6 +447,60 @@ unsigned grid_of(int threads, int64_t tiles) {
   return static_cast<unsigned>(t < res ? (t < 8 ? 8 : t) : res);
 }
 
+// Sums of the splits' partial outputs, in split order, eight columns of a row
+// per thread. Rows [offsets[0], max offsets) exist (forward, dgrad), or all
+// (offsets NULL).
+struct FinishArgs {
+  const float* part;
+  const int32_t* offsets;
+  void* out;
+  int64_t rows, ldp, ldo, split_stride;
+  int G, N, splits, out_f32, accumulate;
+};
+__global__ __launch_bounds__(256) void grouped_finish_kernel(FinishArgs a) {
+  const int per = (a.N + 7) / 8;
+  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = id / per;
+  const int c0 = static_cast<int>(id - row * per) * 8;
+  if (a.offsets) {
+    __shared__ int last[4];
+    int end = 0;
+    for (int g = threadIdx.x; g <= a.G; g += 256) end = max(end, a.offsets[g]);
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) end = max(end, wave_shfl_xor(end, k));
+    if ((threadIdx.x & 63) == 0) last[threadIdx.x >> 6] = end;
+    __syncthreads();
+    end = max(max(last[0], last[1]), max(last[2], last[3]));
+    if (row < max(a.offsets[0], 0) || row >= end) return;
+  }
+  if (row >= a.rows) return;
+  const int cnt = min(a.N - c0, 8);
+  float v[8] = {};
+  const float* p = a.part + row * a.ldp + c0;
+  for (int s = 0; s < a.splits; ++s, p += a.split_stride) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < cnt) v[j] += p[j];
+  }
+  const int64_t at = row * a.ldo + c0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < cnt) {
+      if (a.out_f32) {
+        float* o = static_cast<float*>(a.out) + at + j;
+        *o = a.accumulate ? *o + v[j] : v[j];
+      } else {
+        static_cast<uint16_t*>(a.out)[at + j] = f32_to_bf16(v[j]);
+      }
+    }
+}
+
+// ---- choice of the kernel -------------------------------------------------------
+
+using TileBig = Tile<256, 256, 128, 64, 2>;          // 8 waves, two-phase loop, 128 KB LDS
+using TileMid = Tile<128, 128, 64, 32, 3>;           // 8 waves
+using TileDec = Tile<32, 128, 32, 64, 6, true>;      // 2 waves, weights streamed past L2
+
 template <int MODE, class C>
 int64_t tile_bound(const GArgs& a) {
   const int64_t tn = ((MODE == kForward ? a.n : a.k) + C::BN - 1) / C::BN;
@@ -432,66 +509,176 @@ int64_t tile_bound(const GArgs& a) {
   return full * tn;
 }
 
-template <int MODE, class C, bool PHASED>
+enum Config { kBig = 0, kMid = 1, kDec = 2, kAny = 3 };
+
+struct Choice {
+  int config, splits;
+  int64_t ldp, stride;  // partial outputs
+};
+
+// Whether every row of both operands starts on a 16-byte chunk, and (rows along
+// the contraction) ends on one.
+bool chunked(const GroupedArgs& p) {
+  if (p.mode == kForward) return p.k % 8 == 0 && p.ld_k % 8 == 0;
+  if (p.mode == kDgrad) return p.n % 8 == 0 && p.k % 8 == 0 && p.ld_n % 8 == 0;
+  return p.ld_n % 8 == 0 && p.ld_k % 8 == 0;
+}
+
+// Time model of a tile (microseconds), fitted to measured products: `busy` and
+// `idle` per k-step with the GPU full or at most half full of tiles, `fixed` for
+// a tile's first loads and its output, `slots` tiles at a time.
+struct TileCost {
+  int config, bm, bn, slots;
+  double busy, idle, fixed, fixed_wgrad;
+};
+constexpr TileCost kCosts[] = {
+    {kBig, 256, 256, 256, 1.7, 1.05, 8.0, 12.0},
+    {kMid, 128, 128, 256, 0.65, 0.38, 4.0, 4.0},
+    {kDec, 32, 128, 256, 0.6, 0.35, 3.0, 0.0},
+    {kAny, 128, 128, 512, 1.8, 1.2, 4.0, 4.0},
+};
+
+// The rule: the tile and the number of splits with the least modelled time.
+// Row counts per group live on the device, so the expected number of row tiles
+// stands in for them: one per group while groups are smaller than a tile, else
+// rows / BM and half a tile per group. What it decides, as measured (us):
+//   x [128, 7168], 256 experts x 4096       32 x 128: 864, 128^2: 998, 256^2: 1258
+//   x [1000, 2048], 8 x 1408                128^2: 21, 32 x 128: 32, 256^2: 43
+//   x [2048, 7168], 32 x 4096               128^2: 335, 256^2: 399, 32 x 128: 563
+//   x [8192, 7168], 32 x 4096               256^2: 610, 128^2: 717
+//   dw of 8000 rows, 2 x 256 x 256          4 splits: 26, 1: 53 (128^2), 129 (256^2)
+//   x [8, 4096], 1 x 2048                   4 splits: 22, 1: 26 (32 x 128)
+// Splits add the finishing launch and the partial sums' traffic, so they pay
+// only where few tiles leave most of the GPU idle for many k-steps.
+Choice choose(const GroupedArgs& p, bool aligned) {
+  const int64_t N = p.mode == kForward ? p.n : p.k;
+  const double touched = static_cast<double>(p.rows < p.n_groups ? p.rows : p.n_groups);
+  Choice best{};
+  best.ldp = p.mode == kWgrad ? N : (N + 7) / 8 * 8;
+  best.stride =
+      ((p.mode == kWgrad ? int64_t(p.n_groups) * p.n : p.rows) * best.ldp + 63) / 64 * 64;
+  double least = 0.0;
+  for (const TileCost& t : kCosts) {
+    if ((t.config == kAny) == aligned || (t.config == kDec && p.mode == kWgrad)) continue;
+    const double nt = static_cast<double>((N + t.bn - 1) / t.bn);
+    double tiles, depth;
+    if (p.mode == kWgrad) {
+      tiles = p.n_groups * nt * ((p.n + t.bm - 1) / t.bm);
+      depth = static_cast<double>(p.rows) / p.n_groups;
+    } else {
+      const double mt = p.rows / static_cast<double>(t.bm) + 0.5 * touched;
+      tiles = nt * (mt > touched ? mt : touched);
+      depth = p.mode == kForward ? p.k : p.n;
+    }
+    const double nk = std::ceil(depth / BK);
+    for (int splits = 1; splits <= 16 && (splits == 1 || splits * 4 <= nk); splits *= 2) {
+      const double units = tiles * splits;
+      const double step = units <= t.slots / 2 ? t.idle : t.busy;
+      double us = std::ceil(units / t.slots) * (std::ceil(nk / splits) * step +
+                                                (p.mode == kWgrad ? t.fixed_wgrad : t.fixed));
+      if (splits > 1) us += 6.0 + splits * best.stride * 8.0 / 1.5e6;
+      if (!best.splits || us < least) {
+        least = us;
+        best.config = t.config;
+        best.splits = splits;
+      }
+    }
+  }
+  return best;
+}
+
+template <class C, int MODE, bool PHASED>
 void launch_fast(const GArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((grouped_kernel<C, MODE, PHASED>),
-                     dim3(grid_of<grouped_kernel<C, MODE, PHASED>>(C::NT, tile_bound<MODE, C>(a))),
+                     dim3(grid_of<grouped_kernel<C, MODE, PHASED>>(
+                         C::NT, tile_bound<MODE, C>(a) * a.splits)),
                      dim3(C::NT), 0, s, a);
 }
 
-using TileBig = Tile<256, 256, 128, 64, 2>;  // 128 KB LDS
-
 template <int MODE>
-hipError_t launch_mode(const GArgs& a, bool aligned, hipStream_t s) {
-  if (aligned) {
-    launch_fast<MODE, TileBig, true>(a, s);
-  } else {
-    const int64_t tiles = tile_bound<MODE, TileAny>(a);
+void launch_config(const GArgs& a, int config, hipStream_t s) {
+  if (config == kAny) {
+    const int64_t units = tile_bound<MODE, TileAny>(a) * a.splits;
     hipLaunchKernelGGL(grouped_any_kernel<MODE>,
-                       dim3(grid_of<grouped_any_kernel<MODE>>(TileAny::NT, tiles)),
+                       dim3(grid_of<grouped_any_kernel<MODE>>(TileAny::NT, units)),
                        dim3(TileAny::NT), 0, s, a);
+  } else if (config == kMid) {
+    launch_fast<TileMid, MODE, false>(a, s);
+  } else if (config == kDec) {
+    if constexpr (MODE != kWgrad) launch_fast<TileDec, MODE, false>(a, s);
+  } else {
+    launch_fast<TileBig, MODE, true>(a, s);
   }
-  return hipGetLastError();
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
-hipError_t launch_grouped(const GroupedArgs& p, hipStream_t s) {
+size_t grouped_workspace(const GroupedArgs& p) {
+  // the pointers' alignment is not known yet: enough for either kernel
+  size_t bytes = 0;
+  for (int aligned = 0; aligned <= chunked(p); ++aligned) {
+    const Choice c = choose(p, aligned);
+    const size_t b = c.splits > 1 ? size_t(c.splits) * c.stride * sizeof(float) : 0;
+    if (b > bytes) bytes = b;
+  }
+  return bytes;
+}
+
+hipError_t launch_grouped(const GroupedArgs& p, void* ws, hipStream_t s) {
+  if (p.rows == 0 && p.mode != kWgrad) return hipSuccess;
+  const Choice c = choose(p, chunked(p) && on16(p.a) && on16(p.b));
   GArgs a{};
   a.a = static_cast<const uint16_t*>(p.a);
   a.b = static_cast<const uint16_t*>(p.b);
   a.offsets = p.offsets;
-  a.out = p.out;
   a.rows = p.rows;
   a.G = p.n_groups;
   a.n = p.n;
   a.k = p.k;
-  a.out_f32 = p.out_f32;
-  a.accumulate = p.accumulate;
-  const bool base = on16(p.a) && on16(p.b);
-  if (p.mode == kForward) {
-    a.lda = p.ld_k;
-    a.ldb = p.k;
-    a.ldo = p.ld_n;
-  } else if (p.mode == kDgrad) {
-    a.lda = p.ld_n;
-    a.ldb = p.k;
-    a.ldo = p.ld_k;
+  a.lda = p.mode == kForward ? p.ld_k : p.ld_n;
+  a.ldb = p.mode == kWgrad ? p.ld_k : p.k;
+  a.splits = c.splits;
+  const int64_t ldo = p.mode == kForward ? p.ld_n : p.mode == kDgrad ? p.ld_k : p.k;
+  if (c.splits > 1) {
+    a.out = ws;
+    a.ldo = c.ldp;
+    a.out_f32 = 1;
+    a.split_stride = c.stride;
+    a.vec = 1;
   } else {
-    a.lda = p.ld_n;
-    a.ldb = p.ld_k;
-    a.ldo = p.k;
+    a.out = p.out;
+    a.ldo = ldo;
+    a.out_f32 = p.out_f32;
+    a.accumulate = p.accumulate;
+    a.vec = ldo % 8 == 0 && on16(p.out);
   }
-  a.vec = a.ldo % 8 == 0 && on16(p.out);
-  if (p.mode == kWgrad)
-    return launch_mode<kWgrad>(a, base && a.lda % 8 == 0 && a.ldb % 8 == 0, s);
-  if (p.rows == 0) return hipSuccess;
-  // the contraction of a k-contiguous operand ends on a chunk, every pitch on one
   if (p.mode == kForward)
-    return launch_mode<kForward>(a, base && a.lda % 8 == 0 && p.k % 8 == 0, s);
-  return launch_mode<kDgrad>(a, base && a.lda % 8 == 0 && p.n % 8 == 0 && p.k % 8 == 0, s);
+    launch_config<kForward>(a, c.config, s);
+  else if (p.mode == kDgrad)
+    launch_config<kDgrad>(a, c.config, s);
+  else
+    launch_config<kWgrad>(a, c.config, s);
+  if (c.splits > 1) {
+    FinishArgs f{};
+    f.part = static_cast<const float*>(ws);
+    f.offsets = p.mode == kWgrad ? nullptr : p.offsets;
+    f.out = p.out;
+    f.rows = p.mode == kWgrad ? int64_t(p.n_groups) * p.n : p.rows;
+    f.ldp = c.ldp;
+    f.ldo = ldo;
+    f.split_stride = c.stride;
+    f.G = p.n_groups;
+    f.N = p.mode == kForward ? p.n : p.k;
+    f.splits = c.splits;
+    f.out_f32 = p.out_f32;
+    f.accumulate = p.accumulate;
+    const int64_t threads = f.rows * ((f.N + 7) / 8);
+    hipLaunchKernelGGL(grouped_finish_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)),
+                       dim3(256), 0, s, f);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace dsmoe

@@ -291,7 +291,9 @@ struct GroupedArgs {
   int n_groups, n, k;
   bool out_f32, accumulate;
 };
-hipError_t launch_grouped(const GroupedArgs& p, hipStream_t s);
+// bytes of partial sums for calls that split the contraction (0: none)
+size_t grouped_workspace(const GroupedArgs& p);
+hipError_t launch_grouped(const GroupedArgs& p, void* ws, hipStream_t s);
 
 // orth.hip
 struct OrthArgs {

@@ -124,6 +124,15 @@ GroupedArgs grouped_args(const moe_grouped_desc* d, int mode, const void* a, con
   return g;
 }
 
+moe_status check_ws(const GroupedArgs& g, const void* ws, size_t ws_bytes) {
+  const size_t need = grouped_workspace(g);
+  if (!need) return MOE_OK;
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "this product needs %zu workspace bytes, got %zu", need,
+                ws_bytes);
+  return check({{ws, "ws", 16, true}});
+}
+
 // ---- orthogonalized updates ------------------------------------------------------------
 
 moe_status validate(const moe_orth_desc* d) {
@@ -218,41 +227,61 @@ moe_status moe_layernorm_backward(const moe_norm_desc* desc, const void* dy, con
   return MOE_OK;
 }
 
+moe_status moe_grouped_gemm_workspace_size(const moe_grouped_desc* desc, int32_t op,
+                                           size_t* bytes) {
+  if (op < 0 || op > 2) return fail(MOE_ERR_INVALID_ARGUMENT, "op = %d: 0, 1 or 2", op);
+  moe_status st = validate(desc, op == MOE_GROUPED_WGRAD);
+  if (st) return st;
+  if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  *bytes = grouped_workspace(grouped_args(desc, op, nullptr, nullptr, nullptr, nullptr));
+  return MOE_OK;
+}
+
 moe_status moe_grouped_gemm(const moe_grouped_desc* desc, const void* x, const void* w,
-                            const int32_t* offsets, void* y, hipStream_t stream) {
+                            const int32_t* offsets, void* y, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
   moe_status st = validate(desc, false);
   if (st) return st;
   if (desc->rows == 0) return MOE_OK;
   st = check({{x, "x", 2, true}, {w, "w", 2, true}, {offsets, "offsets", 4, true},
               {y, "y", desc->out_dtype == MOE_DT_F32 ? 4u : 2u, true}});
   if (st) return st;
-  HIP_TRY(launch_grouped(grouped_args(desc, 0, x, w, offsets, y), stream), "grouped product");
+  const GroupedArgs g = grouped_args(desc, MOE_GROUPED_FORWARD, x, w, offsets, y);
+  st = check_ws(g, ws, ws_bytes);
+  if (st) return st;
+  HIP_TRY(launch_grouped(g, ws, stream), "grouped product");
   return MOE_OK;
 }
 
 moe_status moe_grouped_gemm_dgrad(const moe_grouped_desc* desc, const void* dy, const void* w,
-                                  const int32_t* offsets, void* dx, hipStream_t stream) {
+                                  const int32_t* offsets, void* dx, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
   moe_status st = validate(desc, false);
   if (st) return st;
   if (desc->rows == 0) return MOE_OK;
   st = check({{dy, "dy", 2, true}, {w, "w", 2, true}, {offsets, "offsets", 4, true},
               {dx, "dx", desc->out_dtype == MOE_DT_F32 ? 4u : 2u, true}});
   if (st) return st;
-  HIP_TRY(launch_grouped(grouped_args(desc, 1, dy, w, offsets, dx), stream),
-          "grouped input gradient");
+  const GroupedArgs g = grouped_args(desc, MOE_GROUPED_DGRAD, dy, w, offsets, dx);
+  st = check_ws(g, ws, ws_bytes);
+  if (st) return st;
+  HIP_TRY(launch_grouped(g, ws, stream), "grouped input gradient");
   return MOE_OK;
 }
 
 moe_status moe_grouped_gemm_wgrad(const moe_grouped_desc* desc, const void* dy, const void* x,
-                                  const int32_t* offsets, float* dw, hipStream_t stream) {
+                                  const int32_t* offsets, float* dw, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
   moe_status st = validate(desc, true);
   if (st) return st;
   const bool rows = desc->rows > 0;
   st = check({{dy, "dy", 2, rows}, {x, "x", 2, rows}, {offsets, "offsets", 4, true},
               {dw, "dw", 4, true}});
   if (st) return st;
-  HIP_TRY(launch_grouped(grouped_args(desc, 2, dy, x, offsets, dw), stream),
-          "grouped weight gradient");
+  const GroupedArgs g = grouped_args(desc, MOE_GROUPED_WGRAD, dy, x, offsets, dw);
+  st = check_ws(g, ws, ws_bytes);
+  if (st) return st;
+  HIP_TRY(launch_grouped(g, ws, stream), "grouped weight gradient");
   return MOE_OK;
 }
 

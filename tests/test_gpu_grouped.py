@@ -33,6 +33,12 @@ def _off(lens, first=0):
     return o, torch.tensor(o, dtype=torch.int32, device="cuda:0")
 
 
+def _ws(desc, op):
+    import sparse_mixture_experts_gate_amd as M
+    n = M.moe_grouped_gemm_workspace_size(desc, op)
+    return torch.empty(n, dtype=torch.uint8, device="cuda:0") if n else None
+
+
 def _close(got, ref, mag, terms, rnd, what):
     got = host(got).astype(np.float64)
     bad = ~(np.abs(got - ref) <= rnd * np.abs(ref) + (terms + 2) * U * mag + 1e-30)
@@ -71,6 +77,11 @@ CASES = [
     (257, 3, 256, 128, 0.8), (777, 64, 136, 88, 1.1), (900, 2, 512, 320, 0.2),
     (1000, 9, 407, 213, 0.5), (40, 16, 264, 1416, 0.0), (600, 1, 1032, 520, 0.0),
     (2048, 8, 248, 72, 0.6),
+    # enough tiles for the 256 x 256 kernels: forward, input gradient, weight gradient
+    (6000, 3, 2056, 264, 0.4), (6000, 3, 264, 2056, 0.4), (1500, 3, 2056, 2056, 0.3),
+    # long contractions of few outputs: partial sums of several workgroups
+    (20, 1, 64, 4104, 0.0), (20, 1, 4104, 72, 0.0), (9000, 2, 136, 72, 0.5),
+    (20, 3, 65, 4001, 0.0), (21, 2, 4001, 65, 0.0), (9000, 2, 133, 71, 0.5),
 ]
 
 
@@ -95,8 +106,8 @@ def test_empty_groups_and_rows_outside():
         y = torch.full((rows, 80), 7.0, device="cuda:0")
         dx = torch.full((rows, k), 7.0, device="cuda:0")
         desc = M.MoeGroupedDesc(rows=rows, n_groups=len(lens), n=80, k=k, out_dtype=M.MOE_DT_F32)
-        M.moe_grouped_gemm(desc, x, w, off, y)
-        M.moe_grouped_gemm_dgrad(desc, dy, w, off, dx)
+        M.moe_grouped_gemm(desc, x, w, off, y, _ws(desc, M.MOE_GROUPED_FORWARD))
+        M.moe_grouped_gemm_dgrad(desc, dy, w, off, dx, _ws(desc, M.MOE_GROUPED_DGRAD))
         for t in (y, dx):
             assert bool((t[:7] == 7).all()) and bool((t[7 + sum(lens):] == 7).all())
         none = torch.zeros(len(lens) + 1, dtype=torch.int32, device="cuda:0")
@@ -123,7 +134,7 @@ def test_strides(pad, n, k):
     Y = torch.full((rows, ldn), 7.0, device="cuda:0").bfloat16()
     desc = M.MoeGroupedDesc(rows=rows, n_groups=G, n=n, k=k, out_dtype=M.MOE_DT_BF16, ld_k=ldk,
                             ld_n=ldn)
-    M.moe_grouped_gemm(desc, x, w, off, Y[:, pad:pad + n])
+    M.moe_grouped_gemm(desc, x, w, off, Y[:, pad:pad + n], _ws(desc, M.MOE_GROUPED_FORWARD))
     assert torch.equal(Y[:, pad:pad + n], M.GroupedLinear(w).forward(x, off))
     assert bool((Y[:, :pad] == 7).all()) and bool((Y[:, pad + n:] == 7).all())
 
@@ -209,7 +220,7 @@ def test_row_offsets_past_32_bits():
     assert torch.equal(y, M.GroupedLinear(w).forward(x.contiguous(), off, torch.float32))
     desc = M.MoeGroupedDesc(rows=rows, n_groups=2, n=64, k=64, out_dtype=M.MOE_DT_BF16, ld_k=ld,
                             ld_n=ld)
-    M.moe_grouped_gemm(desc, x, w, off, X[:, 128:192])
+    M.moe_grouped_gemm(desc, x, w, off, X[:, 128:192], _ws(desc, M.MOE_GROUPED_FORWARD))
     assert torch.equal(X[:, 128:192], y.bfloat16())
     dw = M.GroupedLinear.weight_grad(X[:, 128:192], x, off)
     ref = M.GroupedLinear.weight_grad(X[:, 128:192].contiguous(), x.contiguous(), off)

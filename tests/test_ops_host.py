@@ -25,7 +25,7 @@ def test_every_declared_symbol_is_exported_and_bound(O):
     assert set(names) == {
         "moe_layernorm_forward", "moe_layernorm_backward_workspace_size", "moe_layernorm_backward",
         "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
-        "moe_orthogonalize_workspace_size", "moe_orthogonalize"}
+        "moe_grouped_gemm_workspace_size", "moe_orthogonalize_workspace_size", "moe_orthogonalize"}
     out = subprocess.run(["nm", "-D", "--defined-only", LIB], capture_output=True, text=True).stdout
     exported = {ln.split()[-1] for ln in out.splitlines() if " T " in ln}
     import sparse_mixture_experts_gate_amd as M
@@ -79,24 +79,32 @@ def test_grouped_refusals(O):
     lib = O.lib()
     fns = [lib.moe_grouped_gemm, lib.moe_grouped_gemm_dgrad, lib.moe_grouped_gemm_wgrad]
     for f in fns:
-        assert f(None, P, P, P, P, None) == 1
+        assert f(None, P, P, P, P, P, 1 << 40, None) == 1
         for kw, st in [(dict(rows=-1), 1), (dict(rows=(1 << 31) - 1), 2), (dict(n_groups=0), 1),
                        (dict(n_groups=513), 2), (dict(n=0), 1), (dict(k=0), 1),
                        (dict(n=1 << 15, k=1 << 14), 2), (dict(ld_k=63), 1), (dict(ld_n=31), 1),
                        (dict(ld_k=1 << 21), 2), (dict(ld_n=1 << 21), 2)]:
-            assert f(ctypes.byref(_grouped(O, **kw)), P, P, P, P, None) == st, kw
+            assert f(ctypes.byref(_grouped(O, **kw)), P, P, P, P, P, 1 << 40, None) == st, kw
         d = _grouped(O)
         for i in range(4):
             args = [P] * 4
             args[i] = None
-            assert f(ctypes.byref(d), *args, None) == 1
+            assert f(ctypes.byref(d), *args, P, 1 << 40, None) == 1
             args[i] = P + 1
-            assert f(ctypes.byref(d), *args, None) == 3
+            assert f(ctypes.byref(d), *args, P, 1 << 40, None) == 3
     for f in fns[:2]:
-        assert f(ctypes.byref(_grouped(O, out_dtype=2)), P, P, P, P, None) == 2
-        assert f(ctypes.byref(_grouped(O, out_dtype=0)), P, P, P, P + 2, None) == 3
-        assert f(ctypes.byref(_grouped(O, rows=0)), None, None, None, None, None) == 0
+        assert f(ctypes.byref(_grouped(O, out_dtype=2)), P, P, P, P, P, 1 << 40, None) == 2
+        assert f(ctypes.byref(_grouped(O, out_dtype=0)), P, P, P, P + 2, P, 1 << 40, None) == 3
+        assert f(ctypes.byref(_grouped(O, rows=0)), None, None, None, None, None, 0, None) == 0
     assert b"" != lib.moe_last_error()
+    # few outputs of a long contraction: partial sums need a workspace
+    d, n = _grouped(O, rows=4, n_groups=1, n=64, k=8192), ctypes.c_size_t()
+    size = lib.moe_grouped_gemm_workspace_size
+    assert size(ctypes.byref(d), 0, ctypes.byref(n)) == 0 and n.value > 0
+    assert size(ctypes.byref(d), 3, ctypes.byref(n)) == size(ctypes.byref(d), -1, ctypes.byref(n)) == 1
+    assert size(None, 0, ctypes.byref(n)) == size(ctypes.byref(d), 0, None) == 1
+    run = lambda ws, b: lib.moe_grouped_gemm(ctypes.byref(d), P, P, P, P, ws, b, None)
+    assert run(P, n.value - 1) == 4 and run(None, n.value) == 1 and run(P + 4, n.value) == 3
 
 
 def test_orthogonalize_refusals(O):
