@@ -156,7 +156,8 @@ typedef struct moe_orth_desc {
   int32_t nesterov;
 } moe_orth_desc;
 
-/* Host only. */
+/* Bytes of workspace, 0 for matrices of up to 128 x 256 (ws may then be NULL).
+ * Host only. */
 moe_status moe_orthogonalize_workspace_size(const moe_orth_desc* desc, size_t* bytes);
 
 /* grad [n_mats, rows, cols]; m_in, m_out fp32 of the same shape, both or

@@ -111,7 +111,8 @@ class LayerNorm:
             dx = torch.empty(n, d, dtype=x.dtype, device=x.device)
             dw = torch.empty(d, dtype=torch.float32, device=x.device)
             db = torch.empty_like(dw)
-            ws = self._ws.get(O.moe_layernorm_backward_workspace_size(desc), x.device, stream)
+            need = O.moe_layernorm_backward_workspace_size(desc)
+            ws = self._ws.get(need, x.device, stream) if need else None
         O.moe_layernorm_backward(desc, dy, x, self.weight, mean, rstd, dresidual, dx, dw, db, ws,
                                  stream)
         return {"dx": dx, "dweight": dw, "dbias": db}
@@ -222,6 +223,6 @@ class Muon:
             out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
             if momentum is not None and out_momentum is None:
                 out_momentum = torch.empty_like(momentum)
-            ws = self._ws.get(need, grad.device, stream)
+            ws = self._ws.get(need, grad.device, stream) if need else None
         O.moe_orthogonalize(desc, grad, momentum, out_momentum, out, ws, stream)
         return out, out_momentum

@@ -300,13 +300,15 @@ moe_status moe_orthogonalize(const moe_orth_desc* desc, const void* grad, const 
   if (st) return st;
   if (desc->n_mats == 0) return MOE_OK;
   st = check({{grad, "grad", 16, true}, {m_in, "m_in", 16, false}, {m_out, "m_out", 16, false},
-              {out, "out", 16, true}, {ws, "ws", 16, true}});
+              {out, "out", 16, true}});
   if (st) return st;
   if (!m_in != !m_out) return fail(MOE_ERR_INVALID_ARGUMENT, "m_in and m_out: both or neither");
   const size_t need = orth_workspace(desc->n_mats, desc->rows, desc->cols);
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "moe_orthogonalize needs %zu workspace bytes, got %zu",
                 need, ws_bytes);
+  st = check({{ws, "ws", 16, need > 0}});
+  if (st) return st;
   OrthArgs a{};
   a.mats = desc->n_mats;
   a.rows = desc->rows;

@@ -434,6 +434,253 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
     stream_ring<C, TypeF16, false, BKM, true>(lds, first, gridDim.x, total, next_ops, ep);
 }
 
+// ---- small matrices ---------------------------------------------------------------
+
+// One workgroup per matrix of up to 128 x 256, all steps in one launch: X stays
+// in fp32 registers (the master) and as fp16 in LDS (the operand), the n x n
+// matrices share one LDS buffer. Launch-bound otherwise: 17 launches a call
+// took 233 us for 32 matrices of 128 x 256.
+//
+// X [128][256] serves row reads (16-byte fragments of 16 rows at a time, for X
+// X^T) and transpose reads (4 rows of 32 bytes, for S X), so its 16-byte chunks
+// are XOR-swizzled with 2 (r & 7) + (r >> 3 & 1): 16 distinct values over 16
+// rows, and distinct pairs of chunks over 4 rows.
+constexpr int kSmallN = 128, kSmallM = 256;
+
+struct SmallArgs {
+  const void* grad;
+  const float* m_in;
+  float* m_out;
+  uint16_t* out;
+  int rows, cols, n, m, steps;
+  float momentum;
+  int nesterov;
+};
+
+__device__ __forceinline__ int x_off(int r, int c) {  // elements, c a multiple of 4
+  const int f = ((r & 7) << 1) | ((r >> 3) & 1);
+  return r * kSmallM + (((c >> 3) ^ f) << 3) + (c & 7);
+}
+__device__ __forceinline__ int r_off(int r, int c) {
+  return r * kSmallN + (((c >> 3) ^ (r & 15)) << 3) + (c & 7);
+}
+
+template <class T, bool MOM, bool TALL>
+__global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
+  __shared__ __attribute__((aligned(16))) _Float16 X[kSmallN * kSmallM];
+  __shared__ __attribute__((aligned(16))) _Float16 R[kSmallN * kSmallN];
+  __shared__ float D[kSmallN], Q[kSmallN];
+  __shared__ double red[8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 2, wn = wave & 3, half = lane >> 5;
+  const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.x;
+  const T* g = static_cast<const T*>(a.grad) + mat * el;
+
+  // this wave's 64 x 64 of X: lane row, runs of four columns
+  f32x16_t x[2][2];
+  double sum = 0.0;
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = wm * 64 + mi * 32 + (lane & 31);
+        const int c = wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+        float u = 0.0f;
+        if (r < a.n && c < a.m) {
+          const int64_t i = TALL ? int64_t(c) * a.cols + r : int64_t(r) * a.cols + c;
+          u = load_grad(g + i);
+          if constexpr (MOM) {
+            const float mo = a.momentum * a.m_in[mat * el + i] + u;
+            a.m_out[mat * el + i] = mo;
+            u = a.nesterov ? u + a.momentum * mo : mo;
+          }
+        }
+        x[mi][nj][e] = u;
+        sum += double(u) * u;
+      }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
+  if (lane == 0) red[wave] = sum;
+  __syncthreads();
+  sum = red[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) sum += red[w];
+  const float scale = static_cast<float>(kScaleX / (sqrt(sum) + kNormEps));
+
+  auto store_x = [&]() {
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = wm * 64 + mi * 32 + (lane & 31);
+          const int c = wn * 64 + nj * 32 + 8 * q + 4 * half;
+          f16x4_t h;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = static_cast<_Float16>(x[mi][nj][4 * q + j]);
+          *reinterpret_cast<f16x4_t*>(X + x_off(r, c)) = h;
+        }
+  };
+  // fragments: 32 rows of X or R from r0, k columns 16 kk ..; columns c0 .. of
+  // X over rows 16 kk .. (transpose reads)
+  auto x_rows = [&](int r0, int kk) {
+    return *reinterpret_cast<const bf16x8_t*>(X + x_off(r0 + (lane & 31), kk * 16 + 8 * half));
+  };
+  auto r_rows = [&](int r0, int kk) {
+    return *reinterpret_cast<const bf16x8_t*>(R + r_off(r0 + (lane & 31), kk * 16 + 8 * half));
+  };
+  auto x_cols = [&](int c0, int kk) {
+    const int gr = lane >> 4, j = (lane >> 2) & 3, q = lane & 3;
+    const int c = c0 + 16 * (gr & 1) + 4 * q, k = kk * 16 + 8 * (gr >> 1) + j;
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4_t*)(uintptr_t)lds_addr(X + x_off(k, c)));
+    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4_t*)(uintptr_t)lds_addr(X + x_off(k + 4, c)));
+    typedef short i16x8_t __attribute__((ext_vector_type(8)));
+    const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8_t, v);
+  };
+
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[mi][nj][e] *= scale;
+  store_x();
+  __syncthreads();
+
+  // steps past the matrix's own rows and columns would multiply zeros
+  const int nk = (a.n + 15) / 16, mk = (a.m + 15) / 16;
+  for (int step = 0; step < a.steps; ++step) {
+    // A = X X^T, this wave's 64 x 32
+    f32x16_t r[2];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) r[mi][e] = 0.0f;
+#pragma unroll 4
+    for (int kk = 0; kk < mk; ++kk) {
+      const bf16x8_t b = x_rows(wn * 32, kk);
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+        r[mi] = mma16<TypeF16, true>(x_rows(wm * 64 + mi * 32, kk), b, r[mi]);
+    }
+    auto put_r = [&](const f32x16_t (&v)[2], float s, float* diag) {
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = wm * 64 + mi * 32 + (lane & 31), c = wn * 32 + 8 * q + 4 * half;
+          f16x4_t h;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w = v[mi][4 * q + j];
+            if (c + j == row) diag[row] = w;
+            h[j] = static_cast<_Float16>(c + j == row ? 0.0f : w * s);
+          }
+          *reinterpret_cast<f16x4_t*>(R + r_off(row, c)) = h;
+        }
+    };
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) r[mi][e] *= 1.0f / (kScaleX * kScaleX);
+    put_r(r, kScaleR, D);
+    __syncthreads();
+    // B = b A + c A A, diagonal apart
+    f32x16_t p[2];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) p[mi][e] = 0.0f;
+#pragma unroll 4
+    for (int kk = 0; kk < nk; ++kk) {
+      const bf16x8_t b = r_rows(wn * 32, kk);
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+        p[mi] = mma16<TypeF16, true>(r_rows(wm * 64 + mi * 32, kk), b, p[mi]);
+    }
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi) {
+      const int row = wm * 64 + mi * 32 + (lane & 31);
+      const float di = D[row];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int c = wn * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+        const float rr = p[mi][e] * (1.0f / (kScaleR * kScaleR));
+        const float rij = r[mi][e];
+        p[mi][e] = c == row ? kB * di + kC * (rr + di * di)
+                            : kB * rij + kC * (rr + (di + D[c]) * rij);
+      }
+    }
+    __syncthreads();  // every wave has read R
+    put_r(p, kScaleS, Q);
+    __syncthreads();
+    // X <- (a + Q) X + S X
+    f32x16_t y[2][2];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[mi][nj][e] = 0.0f;
+#pragma unroll 2
+    for (int kk = 0; kk < nk; ++kk) {
+      bf16x8_t b[2];
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj) b[nj] = x_cols(wn * 64 + nj * 32, kk);
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi) {
+        const bf16x8_t s = r_rows(wm * 64 + mi * 32, kk);
+#pragma unroll
+        for (int nj = 0; nj < 2; ++nj) y[mi][nj] = mma16<TypeF16, true>(s, b[nj], y[mi][nj]);
+      }
+    }
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi) {
+      const float f = kA + Q[wm * 64 + mi * 32 + (lane & 31)];
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          x[mi][nj][e] = f * x[mi][nj][e] + y[mi][nj][e] * (1.0f / kScaleS);
+    }
+    __syncthreads();  // every wave has read X and S
+    if (step + 1 < a.steps) {
+      store_x();
+      __syncthreads();
+    }
+  }
+  uint16_t* out = a.out + mat * el;
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = wm * 64 + mi * 32 + (lane & 31);
+        const int c = wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+        if (r < a.n && c < a.m)
+          out[TALL ? int64_t(c) * a.cols + r : int64_t(r) * a.cols + c] =
+              f32_to_bf16(x[mi][nj][e] * (1.0f / kScaleX));
+      }
+}
+
+template <class T, bool MOM>
+void small(const SmallArgs& a, bool tall, int64_t mats, hipStream_t s) {
+  const dim3 g(static_cast<unsigned>(mats));
+  if (tall)
+    hipLaunchKernelGGL((orth_small_kernel<T, MOM, true>), g, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((orth_small_kernel<T, MOM, false>), g, dim3(512), 0, s, a);
+}
+
+// ---- launches ------------------------------------------------------------------------
+
 template <auto K>
 unsigned grid_of(int threads, int64_t tiles) {
   static int res = 0;
@@ -447,30 +694,51 @@ unsigned grid_of(int threads, int64_t tiles) {
   return static_cast<unsigned>(t < res ? t : res);
 }
 
-template <class C, int KIND, bool TALL, bool PHASED>
-void product(const StepArgs& a, hipStream_t s) {
+using TileBig = Tile<256, 256, 128, 64, 2>;  // 8 waves, two-phase loop
+using TileMid = Tile<128, 128, 64, 32, 3>;   // 8 waves, ring
+
+template <class C, int KIND>
+int64_t tile_count(const StepArgs& a) {
   const int64_t tm = (a.o.n + C::BM - 1) / C::BM, tn = (a.o.m + C::BN - 1) / C::BN;
-  const int64_t total = a.mats * (KIND < kApply ? tm * (tm + 1) / 2 : tm * tn);
+  return a.mats * (KIND < kApply ? tm * (tm + 1) / 2 : tm * tn);
+}
+
+template <class C, int KIND, bool TALL, bool PHASED>
+void launch_product(const StepArgs& a, hipStream_t s) {
+  const int64_t total = tile_count<C, KIND>(a);
   hipLaunchKernelGGL((orth_product_kernel<C, KIND, TALL, PHASED>),
                      dim3(grid_of<orth_product_kernel<C, KIND, TALL, PHASED>>(C::NT, total)),
                      dim3(C::NT), 0, s, a, static_cast<int>(total));
 }
 
-using TileBig = Tile<256, 256, 128, 64, 2>;
+// Big tiles run at the higher rate, small ones fill the GPU: rounds of 256
+// tiles at the measured times per k-step (256 x 256: 1.7 us with the GPU full,
+// 1.05 us half full; 128 x 128: 0.65 and 0.38) and per tile (8 and 4 us).
+template <int KIND, bool TALL>
+void product(const StepArgs& a, hipStream_t s) {
+  const double nk = (KIND == kGram ? a.o.mp : a.o.np) / BK;
+  auto us = [&](int64_t tiles, double busy, double idle, double fixed) {
+    return static_cast<double>((tiles + 255) / 256) * (nk * (tiles <= 128 ? idle : busy) + fixed);
+  };
+  if (us(tile_count<TileBig, KIND>(a), 1.7, 1.05, 8.0) <=
+      us(tile_count<TileMid, KIND>(a), 0.65, 0.38, 4.0))
+    launch_product<TileBig, KIND, TALL, true>(a, s);
+  else
+    launch_product<TileMid, KIND, TALL, false>(a, s);
+}
 
-template <class C, bool PHASED>
 void steps(StepArgs a, const OrthArgs& p, hipStream_t s) {
   for (int i = 0; i < p.steps; ++i) {
     a.hi_in = i & 1 ? a.o.hi1 : a.o.hi0;
     a.hi_out = i & 1 ? a.o.hi0 : a.o.hi1;
-    product<C, kGram, false, PHASED>(a, s);
-    product<C, kSquare, false, PHASED>(a, s);
+    product<kGram, false>(a, s);
+    product<kSquare, false>(a, s);
     if (i + 1 < p.steps)
-      product<C, kApply, false, PHASED>(a, s);
+      product<kApply, false>(a, s);
     else if (a.o.tall)
-      product<C, kApplyLast, true, PHASED>(a, s);
+      product<kApplyLast, true>(a, s);
     else
-      product<C, kApplyLast, false, PHASED>(a, s);
+      product<kApplyLast, false>(a, s);
   }
 }
 
@@ -488,17 +756,30 @@ void prepare(const PrepArgs& a, int64_t mats, hipStream_t s) {
 }  // namespace
 
 size_t orth_workspace(int64_t mats, int rows, int cols) {
-  return static_cast<size_t>(mats) * shape_of(rows, cols).bytes;
+  const OrthShape o = shape_of(rows, cols);
+  if (o.n <= kSmallN && o.m <= kSmallM) return 0;
+  return static_cast<size_t>(mats) * o.bytes;
 }
 
 hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
   if (p.mats == 0) return hipSuccess;
+  const OrthShape o = shape_of(p.rows, p.cols);
+  if (o.n <= kSmallN && o.m <= kSmallM) {
+    const SmallArgs a{p.grad, p.m_in, p.m_out, static_cast<uint16_t*>(p.out), p.rows, p.cols, o.n,
+                      o.m, p.steps, p.momentum, p.nesterov};
+    if (p.bf16)
+      p.m_in ? small<uint16_t, true>(a, o.tall, p.mats, s)
+             : small<uint16_t, false>(a, o.tall, p.mats, s);
+    else
+      p.m_in ? small<float, true>(a, o.tall, p.mats, s) : small<float, false>(a, o.tall, p.mats, s);
+    return hipGetLastError();
+  }
   PrepArgs a{};
   a.grad = p.grad;
   a.m_in = p.m_in;
   a.m_out = p.m_out;
   a.ws = static_cast<char*>(p.ws);
-  a.o = shape_of(p.rows, p.cols);
+  a.o = o;
   a.rows = p.rows;
   a.cols = p.cols;
   a.momentum = p.momentum;
@@ -512,7 +793,7 @@ hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
   st.o = a.o;
   st.out = p.out;
   st.mats = p.mats;
-  steps<TileBig, true>(st, p, s);
+  steps(st, p, s);
   return hipGetLastError();
 }
 

@@ -38,7 +38,9 @@ def _check(out, grad, mom=None, beta=0.95, nesterov=True, steps=5, new=None, tol
             assert (np.abs(got - m) <= 2.0 ** -23 * mag).all()
 
 
-SIZES = [(1, 1, 1), (2, 1, 40), (2, 40, 1), (3, 16, 16), (2, 7, 100), (1, 100, 7), (4, 63, 65),
+# one workgroup a matrix up to 128 x 256, else 128 x 128 tiles, else 256 x 256
+SIZES = [(1, 128, 256), (300, 20, 30), (1, 256, 128), (1, 129, 256), (1, 128, 257), (80, 270, 400),
+         (1, 1, 1), (2, 1, 40), (2, 40, 1), (3, 16, 16), (2, 7, 100), (1, 100, 7), (4, 63, 65),
          (3, 128, 256), (2, 129, 130), (1, 257, 300), (1, 300, 257), (2, 64, 1000), (1, 520, 776),
          (1, 777, 521), (33, 24, 40)]
 
@@ -100,11 +102,12 @@ def test_step_counts(steps):
     _check(out, g, steps=steps)
 
 
-def test_zero_nan_and_neighbours():
+@pytest.mark.parametrize("rows,cols", [(70, 90), (150, 290), (300, 130)])
+def test_zero_nan_and_neighbours(rows, cols):
     """A zero matrix stays zero; NaN fills its own matrix only; results do not
     depend on what else is in the batch or in the workspace."""
     import sparse_mixture_experts_gate_amd as M
-    g = _rand(1, 4, 70, 90)
+    g = _rand(1, 4, rows, cols)
     alone = [M.Muon().direction(g[i:i + 1].contiguous())[0][0] for i in range(4)]
     g[1] = 0
     g[2, 3, 4] = float("nan")

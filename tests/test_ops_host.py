@@ -109,7 +109,7 @@ def test_grouped_refusals(O):
 
 def test_orthogonalize_refusals(O):
     lib = O.lib()
-    mk = lambda **kw: O.MoeOrthDesc(**{**dict(n_mats=2, rows=32, cols=64, grad_dtype=0, steps=5,
+    mk = lambda **kw: O.MoeOrthDesc(**{**dict(n_mats=2, rows=32, cols=640, grad_dtype=0, steps=5,
                                               momentum=0.95, nesterov=1), **kw})
     n = ctypes.c_size_t()
     assert lib.moe_orthogonalize_workspace_size(None, ctypes.byref(n)) == 1
@@ -127,6 +127,10 @@ def test_orthogonalize_refusals(O):
     assert run(size=n.value - 1) == 4
     assert run(g=None) == run(out=None) == run(ws=None) == run(mi=P) == run(mo=P) == 1
     assert run(g=P + 4) == run(ws=P + 8) == 3
+    # small matrices are worked on in LDS
+    small = ctypes.c_size_t(1)
+    assert lib.moe_orthogonalize_workspace_size(ctypes.byref(mk(cols=64)), ctypes.byref(small)) == 0
+    assert small.value == 0 and n.value > 0
     assert lib.moe_orthogonalize(ctypes.byref(mk(n_mats=0)), None, None, None, None, None, 0,
                                  None) == 0
 
