@@ -469,15 +469,56 @@ template <class T, bool MOM, bool TALL>
 __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
   __shared__ __attribute__((aligned(16))) _Float16 X[kSmallN * kSmallM];
   __shared__ __attribute__((aligned(16))) _Float16 R[kSmallN * kSmallN];
-  __shared__ float D[kSmallN], Q[kSmallN];
+  __shared__ __attribute__((aligned(16))) float D[kSmallN];
+  __shared__ float Q[kSmallN];
   __shared__ double red[8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, half = lane >> 5;
   const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.x;
   const T* g = static_cast<const T*>(a.grad) + mat * el;
 
-  // this wave's 64 x 64 of X: lane row, runs of four columns
+  // This wave's 64 x 64 of X: lane row, runs of four columns. All loads go out
+  // before the first use: addresses past the matrix are clamped into it and
+  // their values dropped, so no load hides behind a branch. (With one branch
+  // per element the loads ran one after the other: 71 us for a call that takes
+  // 27.)
   f32x16_t x[2][2];
+  const bool runs = !TALL && a.m % 4 == 0;  // whole runs of four, aligned
+  auto at = [&](int mi, int nj, int e) {
+    const int r = min(wm * 64 + mi * 32 + (lane & 31), a.n - 1);
+    const int c = min(wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3), a.m - 1);
+    return TALL ? int64_t(c) * a.cols + r : int64_t(r) * a.cols + c;
+  };
+  auto inside = [&](int mi, int nj, int e) {
+    return wm * 64 + mi * 32 + (lane & 31) < a.n &&
+           wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3) < a.m;
+  };
+  auto fetch = [&](auto* src, f32x16_t (&v)[2][2]) {
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj) {
+        if (runs) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // a run past the last column starts on the last one
+            const int c = min(wn * 64 + nj * 32 + 8 * q + 4 * half, a.m - 4);
+            const int r = min(wm * 64 + mi * 32 + (lane & 31), a.n - 1);
+            const float4 w = load_grad4(src + int64_t(r) * a.cols + c);
+            v[mi][nj][4 * q] = w.x;
+            v[mi][nj][4 * q + 1] = w.y;
+            v[mi][nj][4 * q + 2] = w.z;
+            v[mi][nj][4 * q + 3] = w.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[mi][nj][e] = load_grad(src + at(mi, nj, e));
+        }
+      }
+  };
+  fetch(g, x);
+  f32x16_t mom[2][2];
+  if constexpr (MOM) fetch(a.m_in + mat * el, mom);
   double sum = 0.0;
 #pragma unroll
   for (int mi = 0; mi < 2; ++mi)
@@ -485,21 +526,40 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
     for (int nj = 0; nj < 2; ++nj)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int r = wm * 64 + mi * 32 + (lane & 31);
-        const int c = wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-        float u = 0.0f;
-        if (r < a.n && c < a.m) {
-          const int64_t i = TALL ? int64_t(c) * a.cols + r : int64_t(r) * a.cols + c;
-          u = load_grad(g + i);
-          if constexpr (MOM) {
-            const float mo = a.momentum * a.m_in[mat * el + i] + u;
-            a.m_out[mat * el + i] = mo;
-            u = a.nesterov ? u + a.momentum * mo : mo;
-          }
+        float u = x[mi][nj][e];
+        if constexpr (MOM) {
+          const float mo = a.momentum * mom[mi][nj][e] + u;
+          mom[mi][nj][e] = mo;
+          u = a.nesterov ? u + a.momentum * mo : mo;
         }
+        u = inside(mi, nj, e) ? u : 0.0f;
         x[mi][nj][e] = u;
         sum += double(u) * u;
       }
+  if constexpr (MOM) {
+    // m_out may be m_in: every value is stored by the lane that read it, and
+    // clamped reads take values of this lane's row or a neighbour's that no
+    // inside element uses
+    __syncthreads();
+    float* mo = a.m_out + mat * el;
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < 2; ++nj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (runs) {
+            if (inside(mi, nj, 4 * q))
+              *reinterpret_cast<float4*>(mo + at(mi, nj, 4 * q)) =
+                  make_float4(mom[mi][nj][4 * q], mom[mi][nj][4 * q + 1], mom[mi][nj][4 * q + 2],
+                              mom[mi][nj][4 * q + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (inside(mi, nj, 4 * q + j)) mo[at(mi, nj, 4 * q + j)] = mom[mi][nj][4 * q + j];
+          }
+        }
+  }
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
   if (lane == 0) red[wave] = sum;
@@ -556,49 +616,59 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
   // steps past the matrix's own rows and columns would multiply zeros
   const int nk = (a.n + 15) / 16, mk = (a.m + 15) / 16;
   for (int step = 0; step < a.steps; ++step) {
+    const f32x16_t zero = {};
     // A = X X^T, this wave's 64 x 32
     f32x16_t r[2];
+    {
+      const bf16x8_t b = x_rows(wn * 32, 0);
 #pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) r[mi][e] = 0.0f;
-#pragma unroll 4
-    for (int kk = 0; kk < mk; ++kk) {
+      for (int mi = 0; mi < 2; ++mi)
+        r[mi] = mma16<TypeF16, true>(x_rows(wm * 64 + mi * 32, 0), b, zero);
+    }
+#pragma unroll 5
+    for (int kk = 1; kk < mk; ++kk) {
       const bf16x8_t b = x_rows(wn * 32, kk);
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi)
         r[mi] = mma16<TypeF16, true>(x_rows(wm * 64 + mi * 32, kk), b, r[mi]);
     }
-    auto put_r = [&](const f32x16_t (&v)[2], float s, float* diag) {
+    // v times s into R; only the wave's 32 x 32 block on the diagonal has
+    // entries to keep apart
+    auto put_r = [&](f32x16_t (&v)[2], float s, float* diag, float sd) {
 #pragma unroll
-      for (int mi = 0; mi < 2; ++mi)
+      for (int mi = 0; mi < 2; ++mi) {
+        const int row = wm * 64 + mi * 32 + (lane & 31);
+        if (wm * 2 + mi == wn) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (8 * (e >> 2) + 4 * half + (e & 3) == (lane & 31)) {
+              diag[row] = v[mi][e] * sd;
+              v[mi][e] = 0.0f;
+            }
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int row = wm * 64 + mi * 32 + (lane & 31), c = wn * 32 + 8 * q + 4 * half;
           f16x4_t h;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float w = v[mi][4 * q + j];
-            if (c + j == row) diag[row] = w;
-            h[j] = static_cast<_Float16>(c + j == row ? 0.0f : w * s);
-          }
-          *reinterpret_cast<f16x4_t*>(R + r_off(row, c)) = h;
+          for (int j = 0; j < 4; ++j) h[j] = static_cast<_Float16>(v[mi][4 * q + j] * s);
+          *reinterpret_cast<f16x4_t*>(R + r_off(row, wn * 32 + 8 * q + 4 * half)) = h;
         }
+      }
     };
-#pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) r[mi][e] *= 1.0f / (kScaleX * kScaleX);
-    put_r(r, kScaleR, D);
+    constexpr float kUnitX = 1.0f / (kScaleX * kScaleX);  // r times this: A
+    put_r(r, kScaleR * kUnitX, D, kUnitX);
     __syncthreads();
-    // B = b A + c A A, diagonal apart
+    // B = b A + c A A, diagonal apart: off it c (R R)_ij + R_ij (b + c (D_i +
+    // D_j)), on it b D_i + c ((R R)_ii + D_i^2)
     f32x16_t p[2];
+    {
+      const bf16x8_t b = r_rows(wn * 32, 0);
 #pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) p[mi][e] = 0.0f;
-#pragma unroll 4
-    for (int kk = 0; kk < nk; ++kk) {
+      for (int mi = 0; mi < 2; ++mi)
+        p[mi] = mma16<TypeF16, true>(r_rows(wm * 64 + mi * 32, 0), b, zero);
+    }
+#pragma unroll 7
+    for (int kk = 1; kk < nk; ++kk) {
       const bf16x8_t b = r_rows(wn * 32, kk);
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi)
@@ -607,29 +677,30 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
       const int row = wm * 64 + mi * 32 + (lane & 31);
-      const float di = D[row];
+      const float di = D[row], ti = kUnitX * (kB + kC * di);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int c = wn * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-        const float rr = p[mi][e] * (1.0f / (kScaleR * kScaleR));
-        const float rij = r[mi][e];
-        p[mi][e] = c == row ? kB * di + kC * (rr + di * di)
-                            : kB * rij + kC * (rr + (di + D[c]) * rij);
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t dj = *reinterpret_cast<const f32x4_t*>(D + wn * 32 + 8 * q + 4 * half);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = 4 * q + j;
+          p[mi][e] = p[mi][e] * (kC / (kScaleR * kScaleR)) +
+                     r[mi][e] * (ti + (kUnitX * kC) * dj[j]);
+        }
+      }
+      if (wm * 2 + mi == wn) {  // r is zero on the diagonal: the rest of its terms
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (8 * (e >> 2) + 4 * half + (e & 3) == (lane & 31))
+            p[mi][e] += di * (kB + kC * di);
       }
     }
     __syncthreads();  // every wave has read R
-    put_r(p, kScaleS, Q);
+    put_r(p, kScaleS, Q, 1.0f);
     __syncthreads();
     // X <- (a + Q) X + S X
     f32x16_t y[2][2];
-#pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-      for (int nj = 0; nj < 2; ++nj)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[mi][nj][e] = 0.0f;
-#pragma unroll 2
-    for (int kk = 0; kk < nk; ++kk) {
+    auto step_y = [&](int kk, bool first) {
       bf16x8_t b[2];
 #pragma unroll
       for (int nj = 0; nj < 2; ++nj) b[nj] = x_cols(wn * 64 + nj * 32, kk);
@@ -637,9 +708,13 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
       for (int mi = 0; mi < 2; ++mi) {
         const bf16x8_t s = r_rows(wm * 64 + mi * 32, kk);
 #pragma unroll
-        for (int nj = 0; nj < 2; ++nj) y[mi][nj] = mma16<TypeF16, true>(s, b[nj], y[mi][nj]);
+        for (int nj = 0; nj < 2; ++nj)
+          y[mi][nj] = mma16<TypeF16, true>(s, b[nj], first ? zero : y[mi][nj]);
       }
-    }
+    };
+    step_y(0, true);
+#pragma unroll 3
+    for (int kk = 1; kk < nk; ++kk) step_y(kk, false);
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
       const float f = kA + Q[wm * 64 + mi * 32 + (lane & 31)];
@@ -659,15 +734,23 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
 #pragma unroll
   for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-    for (int nj = 0; nj < 2; ++nj)
+    for (int nj = 0; nj < 2; ++nj) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = wm * 64 + mi * 32 + (lane & 31);
-        const int c = wn * 64 + nj * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-        if (r < a.n && c < a.m)
-          out[TALL ? int64_t(c) * a.cols + r : int64_t(r) * a.cols + c] =
-              f32_to_bf16(x[mi][nj][e] * (1.0f / kScaleX));
+      for (int e = 0; e < 16; ++e) x[mi][nj][e] *= 1.0f / kScaleX;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& v = x[mi][nj];
+        if (runs) {
+          if (inside(mi, nj, 4 * q))
+            *reinterpret_cast<uint2*>(out + at(mi, nj, 4 * q)) =
+                pack_bf16x4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (inside(mi, nj, 4 * q + j)) out[at(mi, nj, 4 * q + j)] = f32_to_bf16(v[4 * q + j]);
+        }
       }
+    }
 }
 
 template <class T, bool MOM>
