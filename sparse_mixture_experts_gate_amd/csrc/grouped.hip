@@ -220,28 +220,31 @@ __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int w
 
 // ---- operands of any alignment ------------------------------------------------
 
-// Eight elements at p (any element alignment), of which `cnt` exist.
-__device__ __forceinline__ uint4 chunk_any(const uint16_t* p, int cnt) {
-  uint4 r;
-  if (cnt >= 8) {
-    __builtin_memcpy(&r, p, 16);
-  } else {
-    uint16_t t[8];
+// Eight elements at p (any element alignment), of which the first `cnt` exist;
+// the others are read from `safe` and dropped, so that the loads of all chunks
+// go out without a branch between them.
+__device__ __forceinline__ uint4 chunk_any(const uint16_t* p, int cnt, const uint16_t* safe) {
+  uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = j < cnt ? p[j] : uint16_t(0);
-    __builtin_memcpy(&r, t, 16);
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = *(2 * j < cnt ? p + 2 * j : safe);
+    const uint32_t hi = *(2 * j + 1 < cnt ? p + 2 * j + 1 : safe);
+    w[j] = (2 * j < cnt ? lo : 0u) | (2 * j + 1 < cnt ? hi << 16 : 0u);
   }
-  return r;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-using TileAny = Tile<128, 128, 64, 64, 2>;
+using TileAny = Tile<128, 128, 64, 32, 2>;   // 8 waves
+using TileAnyBig = Tile<128, 256, 64, 64, 2>;  // a quarter fewer loaded bytes per product
 
 // Odd widths, pitches or base addresses: operands pass through registers
-// (unaligned 16-byte loads, element loads at the ends), one k-step ahead of
-// the MFMAs, into the same LDS layouts.
-template <int MODE>
-__global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
-  using C = TileAny;
+// (unaligned 16-byte loads, element loads at the ends) into the same LDS
+// layouts, loaded two k-steps ahead of the MFMAs and stored to LDS one ahead.
+// (The weight gradient's small tile fits 128 registers, two workgroups per CU:
+// 8192 rows, 2047 x 4095: 297 us, 384 with one. The others would spill.)
+template <class C, int MODE>
+__global__ __launch_bounds__(C::NT, MODE == kWgrad && C::BN == 128 ? 4 : 2) void
+grouped_any_kernel(GArgs a) {
   constexpr bool AKM = MODE == kWgrad, BKM = MODE != kForward, SWAP = MODE != kWgrad;
   // after the k-loop the stages are free and hold the output rows
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
@@ -262,7 +265,9 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
     const uint16_t* Bt = MODE == kForward ? B + int64_t(c.n) * C::BN * a.ldb : B;
     const int b_rows = a.n - c.n * C::BN;  // forward: rows of W_g from the tile's first
     const int nk = (K + BK - 1) / BK;
-    uint4 ra[C::A_LOADS], rb[C::B_LOADS];
+    struct Step {
+      uint4 a[C::A_LOADS], b[C::B_LOADS];
+    } s0, s1;
     // Element offset of the thread's chunk p in a k-step (LDS chunk p * NT +
     // tid). k-contiguous: rows past the operand's last take that one (their
     // outputs are not stored).
@@ -287,13 +292,13 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
     // outputs are not stored): the last row is in the last k-step, and with
     // rows of fewer than 8 elements every step is checked.
     const bool inner = (!AKM || a.lda >= 8) && (!BKM || a.ldb >= 8);
-    auto fetch_inner = [&](int ks) {
+    auto fetch_inner = [&](int ks, Step& s) {
       const uint16_t* pa = A + (AKM ? int64_t(ks) * BK * a.lda : int64_t(ks) * BK);
       const uint16_t* pb = Bt + (BKM ? int64_t(ks) * BK * a.ldb : int64_t(ks) * BK);
 #pragma unroll
-      for (int p = 0; p < C::A_LOADS; ++p) __builtin_memcpy(&ra[p], pa + oa[p], 16);
+      for (int p = 0; p < C::A_LOADS; ++p) __builtin_memcpy(&s.a[p], pa + oa[p], 16);
 #pragma unroll
-      for (int p = 0; p < C::B_LOADS; ++p) __builtin_memcpy(&rb[p], pb + ob[p], 16);
+      for (int p = 0; p < C::B_LOADS; ++p) __builtin_memcpy(&s.b[p], pb + ob[p], 16);
     };
     auto checked = [&](bool km, const uint16_t* P, int64_t ld, int rows, int col0, int width, int W,
                        int p, int ks) -> uint4 {
@@ -301,44 +306,39 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
         const int cpr = W / 8, row = p * (C::NT / cpr) + tid / cpr;
         const int kr = ks * BK + row;
         const int col = col0 + ((tid % cpr) ^ (4 * (row & 3))) * 8;
-        return chunk_any(P + kr * ld + col, kr < K ? width - col : 0);
+        return chunk_any(P + kr * ld + col, kr < K ? width - col : 0, P);
       }
       const int r = (tid >> 3) + p * C::RPP;
       const int k0 = ks * BK + ((tid & 7) ^ ((r >> 1) & 7)) * 8;
-      return chunk_any(P + r * ld + k0, r < rows ? K - k0 : 0);
+      return chunk_any(P + r * ld + k0, r < rows ? K - k0 : 0, P);
     };
-    auto fetch = [&](int ks) {
-      if (inner && ks + 1 < nk) {
-        fetch_inner(ks);
+    const KRange kr = split_range(nk, c.s, a.splits);
+    const int k_in = inner ? min(kr.k1, nk - 1) : kr.k0;  // steps below it need no checks
+    auto fetch = [&](int ks, Step& s) {
+      if (ks >= kr.k1) return;
+      if (ks < k_in) {
+        fetch_inner(ks, s);
         return;
       }
 #pragma unroll
       for (int p = 0; p < C::A_LOADS; ++p)
-        ra[p] = checked(AKM, A, a.lda, a_rows, c.m * C::BM, a.n, C::BM, p, ks);
+        s.a[p] = checked(AKM, A, a.lda, a_rows, c.m * C::BM, a.n, C::BM, p, ks);
 #pragma unroll
       for (int p = 0; p < C::B_LOADS; ++p)
-        rb[p] = checked(BKM, Bt, a.ldb, b_rows, c.n * C::BN, a.k, C::BN, p, ks);
+        s.b[p] = checked(BKM, Bt, a.ldb, b_rows, c.n * C::BN, a.k, C::BN, p, ks);
     };
-    auto stash = [&](int st) {
+    auto stash = [&](int st, const Step& r) {
       uint16_t* s = lds + st * C::STAGE;
 #pragma unroll
       for (int p = 0; p < C::A_LOADS; ++p)
-        *reinterpret_cast<uint4*>(s + (p * C::NT + tid) * 8) = ra[p];
+        *reinterpret_cast<uint4*>(s + (p * C::NT + tid) * 8) = r.a[p];
 #pragma unroll
       for (int p = 0; p < C::B_LOADS; ++p)
-        *reinterpret_cast<uint4*>(s + C::BM * BK + (p * C::NT + tid) * 8) = rb[p];
+        *reinterpret_cast<uint4*>(s + C::BM * BK + (p * C::NT + tid) * 8) = r.b[p];
     };
     f32x16_t acc[C::MI][C::NJ];
     zero_acc<C>(acc);
-    const KRange kr = split_range(nk, c.s, a.splits);
-    if (kr.k0 < kr.k1) {
-      fetch(kr.k0);
-      stash(kr.k0 & 1);
-    }
-    __syncthreads();
-    for (int ks = kr.k0; ks < kr.k1; ++ks) {
-      const int st = ks & 1;
-      if (ks + 1 < kr.k1) fetch(ks + 1);
+    auto multiply = [&](int st) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         bf16x8_t af[C::MI], bf[C::NJ];
@@ -354,8 +354,34 @@ __global__ __launch_bounds__(TileAny::NT, 2) void grouped_any_kernel(GArgs a) {
           for (int nj = 0; nj < C::NJ; ++nj)
             acc[mi][nj] = mma16<TypeBf16, SWAP>(af[mi], bf[nj], acc[mi][nj]);
       }
-      if (ks + 1 < kr.k1) stash(st ^ 1);
-      __syncthreads();
+    };
+    // steps ks (stage st, its registers free) and ks + 1 (in `next`)
+    auto step = [&](int ks, int st, Step& free, const Step& next) {
+      fetch(ks + 2, free);
+      multiply(st);
+      if (ks + 1 < kr.k1) stash(st ^ 1, next);
+      lds_barrier();
+    };
+    // the same where step ks + 2 needs no checks: no branch between a load and
+    // its use, so the wait counts stay exact
+    auto step_inner = [&](int ks, int st, Step& free, const Step& next) {
+      fetch_inner(ks + 2, free);
+      multiply(st);
+      stash(st ^ 1, next);
+      lds_barrier();
+    };
+    int ks = kr.k0;
+    fetch(ks, s0);
+    fetch(ks + 1, s1);
+    if (ks < kr.k1) stash(0, s0);
+    lds_barrier();
+    for (; ks + 3 < k_in; ks += 2) {
+      step_inner(ks, 0, s0, s1);
+      step_inner(ks + 1, 1, s1, s0);
+    }
+    for (; ks < kr.k1; ks += 2) {
+      step(ks, 0, s0, s1);
+      if (ks + 1 < kr.k1) step(ks + 1, 1, s1, s0);
     }
     store_tile<C, MODE>(a, c, wm, wn, lane, acc,
                         reinterpret_cast<float*>(lds) + wave * RowPasses<C>::FLOATS);
@@ -509,7 +535,7 @@ int64_t tile_bound(const GArgs& a) {
   return full * tn;
 }
 
-enum Config { kBig = 0, kMid = 1, kDec = 2, kAny = 3 };
+enum Config { kBig = 0, kMid = 1, kDec = 2, kAny = 3, kAnyBig = 4 };
 
 struct Choice {
   int config, splits;
@@ -526,7 +552,7 @@ bool chunked(const GroupedArgs& p) {
 
 // Time model of a tile (microseconds), fitted to measured products: `busy` and
 // `idle` per k-step with the GPU full or at most half full of tiles, `fixed` for
-// a tile's first loads and its output, `slots` tiles at a time.
+// a tile's first loads and its output (no wgrad: 0), `slots` tiles at a time.
 struct TileCost {
   int config, bm, bn, slots;
   double busy, idle, fixed, fixed_wgrad;
@@ -535,7 +561,8 @@ constexpr TileCost kCosts[] = {
     {kBig, 256, 256, 256, 1.7, 1.05, 8.0, 12.0},
     {kMid, 128, 128, 256, 0.65, 0.38, 4.0, 4.0},
     {kDec, 32, 128, 256, 0.6, 0.35, 3.0, 0.0},
-    {kAny, 128, 128, 512, 1.8, 1.2, 4.0, 4.0},
+    {kAny, 128, 128, 256, 0.95, 0.8, 5.0, 5.0},
+    {kAnyBig, 128, 256, 256, 1.45, 1.2, 8.0, 0.0},
 };
 
 // The rule: the tile and the number of splits with the least modelled time.
@@ -546,6 +573,8 @@ constexpr TileCost kCosts[] = {
 //   x [1000, 2048], 8 x 1408                128^2: 21, 32 x 128: 32, 256^2: 43
 //   x [2048, 7168], 32 x 4096               128^2: 335, 256^2: 399, 32 x 128: 563
 //   x [8192, 7168], 32 x 4096               256^2: 610, 128^2: 717
+//   x [8192, 4095], 8 x 2048                128 x 256: 297, 128^2: 326 (any alignment)
+//   x [2311, 613], 9 x 1407                 128^2: 25, 128 x 256: 31 (any alignment)
 //   dw of 8000 rows, 2 x 256 x 256          4 splits: 26, 1: 53 (128^2), 129 (256^2)
 //   x [8, 4096], 1 x 2048                   4 splits: 22, 1: 26 (32 x 128)
 // Splits add the finishing launch and the partial sums' traffic, so they pay
@@ -559,7 +588,7 @@ Choice choose(const GroupedArgs& p, bool aligned) {
       ((p.mode == kWgrad ? int64_t(p.n_groups) * p.n : p.rows) * best.ldp + 63) / 64 * 64;
   double least = 0.0;
   for (const TileCost& t : kCosts) {
-    if ((t.config == kAny) == aligned || (t.config == kDec && p.mode == kWgrad)) continue;
+    if ((t.config >= kAny) == aligned || (t.fixed_wgrad == 0.0 && p.mode == kWgrad)) continue;
     const double nt = static_cast<double>((N + t.bn - 1) / t.bn);
     double tiles, depth;
     if (p.mode == kWgrad) {
@@ -595,13 +624,20 @@ void launch_fast(const GArgs& a, hipStream_t s) {
                      dim3(C::NT), 0, s, a);
 }
 
+template <class C, int MODE>
+void launch_any(const GArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(
+      (grouped_any_kernel<C, MODE>),
+      dim3(grid_of<grouped_any_kernel<C, MODE>>(C::NT, tile_bound<MODE, C>(a) * a.splits)),
+      dim3(C::NT), 0, s, a);
+}
+
 template <int MODE>
 void launch_config(const GArgs& a, int config, hipStream_t s) {
   if (config == kAny) {
-    const int64_t units = tile_bound<MODE, TileAny>(a) * a.splits;
-    hipLaunchKernelGGL(grouped_any_kernel<MODE>,
-                       dim3(grid_of<grouped_any_kernel<MODE>>(TileAny::NT, units)),
-                       dim3(TileAny::NT), 0, s, a);
+    launch_any<TileAny, MODE>(a, s);
+  } else if (config == kAnyBig) {
+    if constexpr (MODE != kWgrad) launch_any<TileAnyBig, MODE>(a, s);
   } else if (config == kMid) {
     launch_fast<TileMid, MODE, false>(a, s);
   } else if (config == kDec) {

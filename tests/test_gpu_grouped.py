@@ -79,6 +79,8 @@ CASES = [
     (2048, 8, 248, 72, 0.6),
     # enough tiles for the 256 x 256 kernels: forward, input gradient, weight gradient
     (6000, 3, 2056, 264, 0.4), (6000, 3, 264, 2056, 0.4), (1500, 3, 2056, 2056, 0.3),
+    # and of any alignment: 128 x 256
+    (6000, 3, 2057, 263, 0.4), (6000, 3, 263, 2057, 0.4),
     # long contractions of few outputs: partial sums of several workgroups
     (20, 1, 64, 4104, 0.0), (20, 1, 4104, 72, 0.0), (9000, 2, 136, 72, 0.5),
     (20, 3, 65, 4001, 0.0), (21, 2, 4001, 65, 0.0), (9000, 2, 133, 71, 0.5),
