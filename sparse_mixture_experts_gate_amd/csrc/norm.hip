@@ -56,26 +56,46 @@ __device__ __forceinline__ void unpack(const Raw32& r, float (&v)[VEC]) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(r.w[j]);
 }
-// fp32 -> bf16 to nearest even; a NaN stays one (its payload's low half could
-// round up into infinity).
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  return f != f ? 0x7FC0u : static_cast<uint32_t>(f32_to_bf16(f));
+// Two fp32 -> bf16 to nearest even (one instruction; NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int cnt) {
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// The first `cnt` of eight values. `stream`: past the caches, for outputs larger
+// than the L2s together, which no reader would find there.
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int cnt,
+                                       bool stream = false) {
   if (cnt >= VEC) {
-    Raw16 r;
+    u32x4_any_t r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = bf16_bits(v[2 * j]) | (bf16_bits(v[2 * j + 1]) << 16);
-    __builtin_memcpy(p, &r, sizeof(r));
+    for (int j = 0; j < 4; ++j) r[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+    if (stream)
+      __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any_t*>(p));
+    else
+      *reinterpret_cast<u32x4_any_t*>(p) = r;
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-      if (j < cnt) p[j] = static_cast<uint16_t>(bf16_bits(v[j]));
+      if (j < cnt) p[j] = static_cast<uint16_t>(bf16_pair(v[j], 0.0f));
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[VEC], int cnt) {
+__device__ __forceinline__ void store8(float* p, const float (&v)[VEC], int cnt,
+                                       bool stream = false) {
   if (cnt >= VEC) {
-    __builtin_memcpy(p, v, sizeof(v));
+    typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+    f32x4_any_t* q = reinterpret_cast<f32x4_any_t*>(p);
+    const f32x4_any_t lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    if (stream) {
+      __builtin_nontemporal_store(lo, q);
+      __builtin_nontemporal_store(hi, q + 1);
+    } else {
+      q[0] = lo;
+      q[1] = hi;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
@@ -91,36 +111,34 @@ __device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC], int cn
   }
 }
 
-struct Moments {
-  float n, mean, m2;
-};
-// Moments of the union of two sets of values (Chan, Golub and LeVeque's
-// update): stable for rows whose mean is large against their spread, with one
-// reduction where two passes over the row would take two.
-__device__ __forceinline__ Moments merge(const Moments& a, const Moments& b) {
-  const float n = a.n + b.n;
-  const float f = n > 0.0f ? b.n / n : 0.0f;
-  const float d = b.mean - a.mean;
-  return {n, a.mean + d * f, a.m2 + b.m2 + d * d * a.n * f};
+// Sum over the wave by DPP adds (rows of 16 lanes, then across rows; lane 63
+// holds it), the same for all lanes.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, true));
 }
-__device__ __forceinline__ Moments wave_merge(Moments m) {
-#pragma unroll
-  for (int s = 1; s < kWave; s <<= 1)
-    m = merge(m, {wave_shfl_xor(m.n, s), wave_shfl_xor(m.mean, s), wave_shfl_xor(m.m2, s)});
-  return m;
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xf>(v);  // row_shr:2
+  v = dpp_add<0x114, 0xf>(v);  // row_shr:4
+  v = dpp_add<0x118, 0xf>(v);  // row_shr:8
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1, 3
+  v = dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2, 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
-// Moments over the waves of a row group, in wave order.
+// Sum over the NW waves of a row group, in wave order. `slot`: NW floats of LDS
+// that the next call does not use.
 template <int NW>
-__device__ __forceinline__ Moments row_merge(Moments m, Moments* slot) {
-  m = wave_merge(m);
+__device__ __forceinline__ float row_sum(float v, float* slot) {
+  v = wave_sum(v);
   if constexpr (NW > 1) {
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = m;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
-    m = slot[0];
+    v = slot[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) m = merge(m, slot[w]);
+    for (int w = 1; w < NW; ++w) v += slot[w];
   }
-  return m;
+  return v;
 }
 
 struct FwdArgs {
@@ -134,21 +152,25 @@ struct FwdArgs {
   float* rstd;
   int64_t n, ldx, ldr, ldy, lds;
   int d;
-  float eps;
+  float eps, inv_d;
+  bool stream;  // row outputs past the caches
 };
 
 // A block of max(NW, 4) waves; NW waves own a row, CH chunks of 8 values per
 // lane. One block per row (NW > 1) or per four rows (NW == 1).
+//
+// Mean first, then the squares of what is left, both from registers: merging
+// per-lane moments in one pass is as stable but took ten times the vector
+// operations, and those then bound the kernel (8192 x 7168 bf16: 73 us).
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdArgs a) {
-  __shared__ Moments slot[NW];
+  __shared__ float slot[2][NW];
   constexpr int LANES = NW * 64;
   const int64_t row = NW == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (NW == 1 && row >= a.n) return;
   const int lane = threadIdx.x & (LANES - 1);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float v[CH][VEC];
-  Moments m{0.0f, 0.0f, 0.0f};
   typename RawOf<T>::type rx[CH], rr[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -156,10 +178,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdAr
     rx[c] = load8(x + i0, a.d - i0);
     if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr + i0, a.d - i0);
   }
+  float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i0 = (c * LANES + lane) * VEC;
-    const int cnt = min(max(a.d - i0, 0), VEC);
     unpack(rx[c], v[c]);
     if constexpr (RES) {
       float r[VEC];
@@ -167,22 +188,30 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdAr
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[c][j] += r[j];
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) s += v[c][j];
-    const float mu = cnt > 0 ? s / static_cast<float>(cnt) : 0.0f;
-    float q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float e = j < cnt ? v[c][j] - mu : 0.0f;
-      q += e * e;
-    }
-    m = merge(m, {static_cast<float>(cnt), mu, q});
+    s += ((v[c][0] + v[c][1]) + (v[c][2] + v[c][3])) + ((v[c][4] + v[c][5]) + (v[c][6] + v[c][7]));
   }
-  m = row_merge<NW>(m, slot);
-  const float rstd = 1.0f / sqrtf(m.m2 / static_cast<float>(a.d) + a.eps);
+  const float mean = row_sum<NW>(s, slot[0]) * a.inv_d;
+  float q = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i0 = (c * LANES + lane) * VEC;
+    const int cnt = a.d - i0;
+    if constexpr (RES) {
+      if (cnt > 0) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v[c], cnt, a.stream);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[c][j] -= mean;
+    if (cnt >= VEC) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) q += v[c][j] * v[c][j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) q += j < cnt ? v[c][j] * v[c][j] : 0.0f;
+    }
+  }
+  const float rstd = rsqrtf(row_sum<NW>(q, slot[1]) * a.inv_d + a.eps);
   if (lane == 0 && a.mean) {
-    a.mean[row] = m.mean;
+    a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
   T* y = static_cast<T*>(a.y) + row * a.ldy;
@@ -191,21 +220,20 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdAr
     const int i0 = (c * LANES + lane) * VEC;
     const int cnt = a.d - i0;
     if (cnt <= 0) continue;
-    if constexpr (RES) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v[c], cnt);
     float w[VEC], b[VEC], o[VEC];
     load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
     load_vec(a.b ? a.b + i0 : nullptr, b, cnt, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = (v[c][j] - m.mean) * rstd * w[j] + b[j];
-    store8(y + i0, o, cnt);
+    for (int j = 0; j < VEC; ++j) o[j] = v[c][j] * rstd * w[j] + b[j];
+    store8(y + i0, o, cnt, a.stream);
   }
 }
 
-// Rows past the register path: 512 threads, the row read once for the moments
-// and once for the output (the second time from L2).
+// Rows past the register path: 512 threads, the row read three times (after the
+// first time from L2).
 template <class T>
 __global__ __launch_bounds__(512) void norm_fwd_long_kernel(FwdArgs a) {
-  __shared__ Moments slot[8];
+  __shared__ float slot[2][8];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
@@ -218,38 +246,35 @@ __global__ __launch_bounds__(512) void norm_fwd_long_kernel(FwdArgs a) {
       for (int j = 0; j < VEC; ++j) v[j] += u[j];
     }
   };
-  Moments m{0.0f, 0.0f, 0.0f};
+  float s = 0.0f, q = 0.0f;
   for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
     float v[VEC];
     get(i0, v);
-    const int cnt = min(a.d - i0, VEC);
-    float s = 0.0f, q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) s += v[j];
-    const float mu = s / static_cast<float>(cnt);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float e = j < cnt ? v[j] - mu : 0.0f;
-      q += e * e;
-    }
-    m = merge(m, {static_cast<float>(cnt), mu, q});
+    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
   }
-  m = row_merge<8>(m, slot);
-  const float rstd = 1.0f / sqrtf(m.m2 / static_cast<float>(a.d) + a.eps);
+  const float mean = row_sum<8>(s, slot[0]) * a.inv_d;
+  for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
+    float v[VEC];
+    get(i0, v);
+    const int cnt = a.d - i0;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) q += j < cnt ? (v[j] - mean) * (v[j] - mean) : 0.0f;
+  }
+  const float rstd = rsqrtf(row_sum<8>(q, slot[1]) * a.inv_d + a.eps);
   if (threadIdx.x == 0 && a.mean) {
-    a.mean[row] = m.mean;
+    a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
   for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
     float v[VEC], w[VEC], b[VEC], o[VEC];
     get(i0, v);
     const int cnt = a.d - i0;
-    if (r) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v, cnt);
+    if (r) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v, cnt, a.stream);
     load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
     load_vec(a.b ? a.b + i0 : nullptr, b, cnt, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = (v[j] - m.mean) * rstd * w[j] + b[j];
-    store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt);
+    for (int j = 0; j < VEC; ++j) o[j] = (v[j] - mean) * rstd * w[j] + b[j];
+    store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
   }
 }
 
@@ -266,15 +291,13 @@ struct BwdNormArgs {
   float* part;  // [gridDim.x][2][d] partial dweight, dbias; NULL: not wanted
   int64_t n, ldx, ldr, ldy, lds;
   int d;
+  bool stream;  // row outputs past the caches
 };
 
 template <int NW>
 __device__ __forceinline__ float2 row_sum2(float2 s, float2* slot) {
-#pragma unroll
-  for (int k = 1; k < kWave; k <<= 1) {
-    s.x += wave_shfl_xor(s.x, k);
-    s.y += wave_shfl_xor(s.y, k);
-  }
+  s.x = wave_sum(s.x);
+  s.y = wave_sum(s.y);
   if constexpr (NW > 1) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = s;
     __syncthreads();
@@ -363,7 +386,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += e[j];
       }
-      store8(dx + i0, o, a.d - i0);
+      store8(dx + i0, o, a.d - i0, a.stream);
     }
   }
   if (!a.part) return;
@@ -561,16 +584,29 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
 
 }  // namespace
 
-// Blocks of the backward, each with a partial row of column sums.
+// Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
+// More blocks hide more latency but write and add more partial rows (8192 x 7168
+// bf16 with dresidual: 97 us with 256 blocks of 8 waves, 113 with 512; 8192 x
+// 2048: 34 us with 512 of 4 waves, 42 with 256, 38 with 768).
 int norm_backward_parts(int64_t n, int d) {
-  const int64_t groups = d > kMaxRow ? n : row_shape(d).nw == 1 ? (n + 3) / 4 : n;
-  return static_cast<int>(groups < 1 ? 1 : groups < 512 ? groups : 512);
+  if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);
+  const int nw = row_shape(d).nw;
+  const int64_t groups = nw == 1 ? (n + 3) / 4 : n, most = nw == 8 ? 256 : 512;
+  return static_cast<int>(groups < 1 ? 1 : groups < most ? groups : most);
 }
+
+// Row outputs of this many bytes or more are stored past the caches: eight L2s
+// of 4 MB (8192 x 7168 fp32: 122 -> 110 us; bf16 equal).
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
+namespace {
+bool streamed(const NormArgs& p) { return p.n * p.d * (p.bf16 ? 2 : 4) >= kStreamBytes; }
+}  // namespace
 
 hipError_t launch_norm_forward(const NormArgs& p, hipStream_t s) {
   if (p.n == 0) return hipSuccess;
   const FwdArgs a{p.x, p.r, p.w, p.b, p.y, p.s, p.mean, p.rstd,
-                  p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, p.eps};
+                  p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, p.eps, 1.0f / p.d, streamed(p)};
   if (p.bf16)
     p.r ? fwd_dispatch<uint16_t, true>(a, s) : fwd_dispatch<uint16_t, false>(a, s);
   else
@@ -584,7 +620,7 @@ hipError_t launch_norm_backward(const NormArgs& p, float* dw, float* db, float* 
   const bool sums = dw || db;
   if (p.n > 0) {
     const BwdNormArgs a{p.y, p.x, p.w, p.mean, p.rstd, p.r, p.s, sums ? part : nullptr,
-                        p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d};
+                        p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, streamed(p)};
     if (p.bf16)
       p.r ? bwd_dispatch<uint16_t, true>(a, parts, s) : bwd_dispatch<uint16_t, false>(a, parts, s);
     else
