@@ -215,6 +215,110 @@ struct RowPasses {
   }
 };
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// ---- tiles of the last round, split along the contraction
+//
+// Tiles run in rounds of one per workgroup, and the last round's may be few. The
+// first `whole` tiles run whole; each of the others is shared by `splits`
+// workgroups, whose fp32 partial tiles meet in memory: the last to arrive adds
+// them in split order (so the sum does not depend on who is last).
+struct Tail {
+  int whole, splits;
+  float* part;     // [(unit - whole)][BM * BN]
+  int32_t* count;  // [tile - whole], zero before and after
+};
+struct Unit {
+  int tile, s, splits;
+};
+__device__ __forceinline__ Unit unit_of(const Tail& t, int unit) {
+  if (unit < t.whole) return {unit, 0, 1};
+  const int v = unit - t.whole, q = v / t.splits;
+  return {t.whole + q, v - q * t.splits, t.splits};
+}
+// k-steps [k0, k1) of split s.
+struct KRange {
+  int k0, k1;
+};
+__device__ __forceinline__ KRange split_range(int nk, int s, int splits) {
+  return {static_cast<int>(int64_t(nk) * s / splits),
+          static_cast<int>(int64_t(nk) * (s + 1) / splits)};
+}
+// Number of splits for `rest` tiles of nk k-steps on `slots` workgroups, by time
+// in microseconds: `step` per k-step, and to share a tile its partial sums'
+// way to memory and back, `kb` KB at the measured 22 (out) and 30 (in) KB/us of
+// one CU.
+inline __host__ __device__ int tail_splits(int rest, int nk, int slots, float step, float kb) {
+  if (rest <= 0) return 1;
+  int best = 1;
+  float least = nk * step;
+  for (int s = 2; s <= slots / rest && s <= 8 && s <= nk; ++s) {
+    const float us = (nk + s - 1) / s * step + kb * (1.0f / 22.0f + s * (1.0f / 30.0f));
+    if (us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
+}
+// Called by all threads of the workgroup at a unit's end. True where acc holds
+// the tile's sum. `flag`: an int in LDS.
+//
+// The workgroups may run on different XCDs, whose L2s are not coherent with each
+// other: partial sums are written through to memory and read from it (device
+// scope, the sc1 bit), so waiting for the stores is all the ordering there is to
+// do. Fences around plain stores write back and invalidate a whole L2 each: an
+// update of 1408 x 2816 took 888 us with them, 329 so.
+constexpr int kDevice = 16;  // sc1
+template <class C>
+__device__ __forceinline__ bool join_splits(f32x16_t (&acc)[C::MI][C::NJ], const Tail& t, int unit,
+                                            const Unit& u, int* flag) {
+  if (u.splits == 1) return true;
+  constexpr int BYTES = C::BM * C::BN * 4;
+  // the thread's 16-byte pieces at i * NT * 16 (a scalar offset: addresses in
+  // vector registers would push the k-loop's out)
+  auto rsrc = [&](int v) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<char*>(t.part) + int64_t(v) * BYTES, 0, BYTES, 0x00020000);
+  };
+  const int off = threadIdx.x * 16;
+  const auto mine = rsrc(unit - t.whole);
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t v = {acc[mi][nj][4 * q], acc[mi][nj][4 * q + 1], acc[mi][nj][4 * q + 2],
+                           acc[mi][nj][4 * q + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), mine, off,
+                                               ((mi * C::NJ + nj) * 4 + q) * C::NT * 16, kDevice);
+      }
+  vm_wait<0>();  // the wave's partial sums have reached memory before the count
+  lds_barrier();
+  if (threadIdx.x == 0) *flag = atomicAdd(t.count + (u.tile - t.whole), 1);
+  lds_barrier();
+  if (*flag != u.splits - 1) return false;
+  zero_acc<C>(acc);
+  for (int s = 0; s < u.splits; ++s) {
+    const auto other = rsrc(unit - t.whole - u.s + s);
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t v = __builtin_bit_cast(
+              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                           other, off, ((mi * C::NJ + nj) * 4 + q) * C::NT * 16, kDevice));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[mi][nj][4 * q + j] += v[j];
+        }
+  }
+  if (threadIdx.x == 0) t.count[u.tile - t.whole] = 0;
+  return true;
+}
+
 // Ring loop for small tiles: NST stages, loads NST - 1 k-steps ahead, the
 // fragments of sub-step kk + 1 read between the MFMAs of sub-step kk, one
 // barrier per k-step (before its last sub-step, whose fragments are already
@@ -291,6 +395,10 @@ __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, in
 // fragments and issue loads, then they swap, so each SIMD's matrix core has
 // work in every phase. Two stages of 64 KB: the loads of step k + 1 go out in
 // the first two phases of step k and are waited for in its last.
+//
+// Rows of a tile past its data are multiplied all the same: leaving out waves
+// whose part of the tile is empty took as long (the loads set the pace there),
+// and a branch per 32-row part twice as long (the accumulators were copied).
 //
 // The halves fall into step again for a tile's epilogue: staggered, each half
 // would wait at a barrier for the other's stores.

@@ -15,6 +15,8 @@ namespace dsmoe {
 
 namespace {
 
+constexpr float kBigStep = 1.4f;  // us per k-step of 256 x 256 tiles, operands from L2
+
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 // Operands by mode (C[M, N] = A B, contraction K):
@@ -36,16 +38,10 @@ struct GArgs {
   // adds in split order (one split: the output itself).
   int splits;
   int64_t split_stride;
+  // 256 x 256 tiles: workspace of the last round's shared tiles (NULL: none)
+  float* tail_part;
+  int32_t* tail_count;
 };
-
-// k-steps [k0, k1) of split s.
-struct KRange {
-  int k0, k1;
-};
-__device__ __forceinline__ KRange split_range(int nk, int s, int splits) {
-  return {static_cast<int>(int64_t(nk) * s / splits),
-          static_cast<int>(int64_t(nk) * (s + 1) / splits)};
-}
 
 // Tile tables of the groups from the device offsets, clamped to an ascending
 // split of [0, rows]: t.off the row offsets, t.gnext[g] the first tile of
@@ -104,9 +100,10 @@ __device__ __forceinline__ void build_group_tables(GroupTables& t, const int32_t
   __syncthreads();
 }
 
-// Tile order of the weight gradient inside a group: rows of 8 m-tiles, m
-// fastest, so that the 32 consecutive tiles an XCD runs at a time read 8 A
-// panels and 4 B panels.
+// Tile order inside a group: rows of 8 m-tiles, m fastest, so that the 32
+// consecutive tiles an XCD runs at a time read 8 A panels and 4 B panels (one
+// group of 8192 rows, 4096 x 7168: 431 us with m fastest over all 32 m-tiles,
+// 380 this way).
 constexpr int kSuper = 8;
 __device__ __forceinline__ void super_tile(int rem, int tm, int tn, int& m, int& n) {
   const int per = kSuper * tn, gr = rem / per, r2 = rem - gr * per;
@@ -121,7 +118,8 @@ __device__ __forceinline__ int64_t span(int rows, uint32_t ld_bytes, int width) 
 }
 
 struct GTile {
-  int g, m, n, s;    // group, tile indices, split
+  int g, m, n;       // group, tile indices
+  int s, splits;     // split of the contraction
   int64_t row0;      // first row of the group
   int rows;          // rows of the group
 };
@@ -131,6 +129,7 @@ __device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, i
   GTile c;
   const int tile = unit / a.splits;
   c.s = unit - tile * a.splits;
+  c.splits = a.splits;
   if constexpr (MODE == kWgrad) {
     const int tm = (a.n + BM - 1) / BM, tn = (a.k + BN - 1) / BN;
     c.g = tile / (tm * tn);
@@ -141,10 +140,10 @@ __device__ __forceinline__ GTile tile_of(const GArgs& a, const GroupTables& t, i
   } else {
     const TileCoord tc = tile_coord_lds(t, a.G, 0, tile, BM);
     c.g = tc.g;
-    c.m = tc.m;
-    c.n = tc.n;
     c.row0 = tc.rbase;
     c.rows = tc.rows;
+    const int tm = (tc.rows + BM - 1) / BM;
+    super_tile(tc.n * tm + tc.m, tm, ((MODE == kForward ? a.n : a.k) + BN - 1) / BN, c.m, c.n);
   }
   return c;
 }
@@ -402,17 +401,35 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   const int N = MODE == kForward ? a.n : a.k;
   const int tn = (N + C::BN - 1) / C::BN;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, tn);
-  const int total =
+  __shared__ int flag;
+  const int tiles =
       (MODE == kWgrad ? a.G * ((a.n + C::BM - 1) / C::BM) * tn : gt.total) * a.splits;
+  Tail tail{tiles, 1, a.tail_part, a.tail_count};
+  if (a.tail_part) {
+    const int whole = tiles / gridDim.x * gridDim.x;
+    const int nk = ((MODE == kForward ? a.k : a.n) + BK - 1) / BK;
+    tail.splits = tail_splits(tiles - whole, nk, gridDim.x, kBigStep, C::BM * C::BN / 256);
+    if (tail.splits > 1) tail.whole = whole;
+  }
+  const int total = tail.whole + (tiles - tail.whole) * tail.splits;
   const int first = xcd_logical_block(blockIdx.x, gridDim.x);
   if (first >= total) return;
+  auto locate = [&](int unit) {
+    const Unit u = unit_of(tail, unit);
+    GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, u.tile);
+    if (u.splits > 1) {
+      c.s = u.s;
+      c.splits = u.splits;
+    }
+    return c;
+  };
   const uint32_t lda = static_cast<uint32_t>(a.lda) * 2u, ldb = static_cast<uint32_t>(a.ldb) * 2u;
   auto depth = [&](const GTile& c) { return MODE == kForward ? a.k : MODE == kDgrad ? a.n : c.rows; };
   auto range = [&](const GTile& c) {
-    return split_range((depth(c) + BK - 1) / BK, c.s, a.splits);
+    return split_range((depth(c) + BK - 1) / BK, c.s, c.splits);
   };
   auto next_ops = [&](int unit, Ops16<C>& op) {
-    const GTile c = tile_of<MODE, C::BM, C::BN>(a, gt, unit);
+    const GTile c = locate(unit);
     const KRange kr = range(c);
     // an empty range (an empty group, or fewer k-steps than splits) reads one
     // k-step of zeros
@@ -441,17 +458,24 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   };
   struct Epilogue {
     const GArgs& a;
-    const GroupTables& gt;
+    const Tail& tail;
+    int* flag;
+    decltype(locate)& at;
     decltype(range)& steps;
     __device__ int k_steps(int unit) const {
-      const KRange r = steps(tile_of<MODE, C::BM, C::BN>(a, gt, unit));
+      const KRange r = steps(at(unit));
       return max(r.k1 - r.k0, 1);
     }
-    __device__ void operator()(int tile, int wm, int wn, int lane,
-                               f32x16_t (&acc)[C::MI][C::NJ], float* stage) const {
-      store_tile<C, MODE>(a, tile_of<MODE, C::BM, C::BN>(a, gt, tile), wm, wn, lane, acc, stage);
+    __device__ void operator()(int unit, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
+                               float* stage) const {
+      GTile c = at(unit);
+      if constexpr (PHASED && MODE != kWgrad) {
+        if (!join_splits<C>(acc, tail, unit, unit_of(tail, unit), flag)) return;
+        c.s = 0;
+      }
+      store_tile<C, MODE>(a, c, wm, wn, lane, acc, stage);
     }
-  } ep{a, gt, range};
+  } ep{a, tail, &flag, locate, range};
   if constexpr (PHASED)
     stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
   else
@@ -539,8 +563,13 @@ enum Config { kBig = 0, kMid = 1, kDec = 2, kAny = 3, kAnyBig = 4 };
 
 struct Choice {
   int config, splits;
+  bool tail;            // share the last round's tiles
   int64_t ldp, stride;  // partial outputs
 };
+// Workspace of shared tiles: one partial tile per workgroup, one counter per tile.
+constexpr int kTailSlots = 256;
+constexpr size_t kTailPart = size_t(kTailSlots) * TileBig::BM * TileBig::BN * sizeof(float);
+constexpr size_t kTailBytes = kTailPart + kTailSlots * sizeof(int32_t);
 
 // Whether every row of both operands starts on a 16-byte chunk, and (rows along
 // the contraction) ends on one.
@@ -595,7 +624,8 @@ Choice choose(const GroupedArgs& p, bool aligned) {
       tiles = p.n_groups * nt * ((p.n + t.bm - 1) / t.bm);
       depth = static_cast<double>(p.rows) / p.n_groups;
     } else {
-      const double mt = p.rows / static_cast<double>(t.bm) + 0.5 * touched;
+      const double mt = p.n_groups == 1 ? std::ceil(p.rows / static_cast<double>(t.bm))
+                                        : p.rows / static_cast<double>(t.bm) + 0.5 * touched;
       tiles = nt * (mt > touched ? mt : touched);
       depth = p.mode == kForward ? p.k : p.n;
     }
@@ -603,13 +633,27 @@ Choice choose(const GroupedArgs& p, bool aligned) {
     for (int splits = 1; splits <= 16 && (splits == 1 || splits * 4 <= nk); splits *= 2) {
       const double units = tiles * splits;
       const double step = units <= t.slots / 2 ? t.idle : t.busy;
-      double us = std::ceil(units / t.slots) * (std::ceil(nk / splits) * step +
-                                                (p.mode == kWgrad ? t.fixed_wgrad : t.fixed));
+      // a 256 x 256 tile of a long contraction in the last round is shared by the
+      // workgroups that this round leaves idle; that takes a launch to clear the
+      // counters, so it is left out where little can be won
+      const bool tail = t.config == kBig && p.mode != kWgrad && splits == 1 && nk >= 48.0;
+      double rounds = std::ceil(units / t.slots), us = 0.0;
+      if (tail) {
+        const int rest = static_cast<int>(units) % t.slots, k = static_cast<int>(nk);
+        const int s = tail_splits(rest, k, t.slots, kBigStep, 256.0f);
+        if (s > 1) {
+          rounds = std::floor(units / t.slots);
+          us = 5.0 + (k + s - 1) / s * kBigStep + t.fixed + 256.0 / 22.0 + s * 256.0 / 30.0;
+        }
+      }
+      us += rounds * (std::ceil(nk / splits) * step +
+                      (p.mode == kWgrad ? t.fixed_wgrad : t.fixed));
       if (splits > 1) us += 6.0 + splits * best.stride * 8.0 / 1.5e6;
       if (!best.splits || us < least) {
         least = us;
         best.config = t.config;
         best.splits = splits;
+        best.tail = tail;
       }
     }
   }
@@ -656,7 +700,9 @@ size_t grouped_workspace(const GroupedArgs& p) {
   size_t bytes = 0;
   for (int aligned = 0; aligned <= chunked(p); ++aligned) {
     const Choice c = choose(p, aligned);
-    const size_t b = c.splits > 1 ? size_t(c.splits) * c.stride * sizeof(float) : 0;
+    const size_t b = c.splits > 1 ? size_t(c.splits) * c.stride * sizeof(float)
+                     : c.tail     ? kTailBytes
+                                  : 0;
     if (b > bytes) bytes = b;
   }
   return bytes;
@@ -689,6 +735,12 @@ hipError_t launch_grouped(const GroupedArgs& p, void* ws, hipStream_t s) {
     a.out_f32 = p.out_f32;
     a.accumulate = p.accumulate;
     a.vec = ldo % 8 == 0 && on16(p.out);
+  }
+  if (c.tail) {
+    a.tail_part = static_cast<float*>(ws);
+    a.tail_count = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kTailPart);
+    const hipError_t e = launch_fill_i32(a.tail_count, kTailSlots, 0, s);
+    if (e != hipSuccess) return e;
   }
   if (p.mode == kForward)
     launch_config<kForward>(a, c.config, s);

@@ -46,6 +46,7 @@ struct OrthShape {
   size_t hi0, hi1, lo, r, s, d, q, part, bytes;
 };
 
+constexpr int kSlots = 256;       // workgroups of a round, counters of shared tiles
 constexpr int kSumChunk = 16384;  // elements of one partial sum of squares
 
 OrthShape shape_of(int rows, int cols) {
@@ -78,6 +79,7 @@ OrthShape shape_of(int rows, int cols) {
 }
 
 struct PrepArgs {
+  int32_t* count;  // counters of shared tiles, cleared here
   const void* grad;
   const float* m_in;
   float* m_out;
@@ -104,6 +106,8 @@ __device__ __forceinline__ float4 load_grad4(const uint16_t* p) {
 template <class T, bool MOM>
 __global__ __launch_bounds__(256) void orth_sum_kernel(PrepArgs a) {
   __shared__ double red[4];
+  if (blockIdx.x == 0 && blockIdx.y == 0) a.count[threadIdx.x] = 0;
+  static_assert(kSlots == 256, "one counter per thread");
   const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.y;
   const T* g = static_cast<const T*>(a.grad) + mat * el;
   const int64_t per = ((el + a.o.chunks - 1) / a.o.chunks + 1023) / 1024 * 1024;
@@ -244,6 +248,7 @@ struct StepArgs {
   size_t hi_in, hi_out;  // planes of X read and written
   void* out;             // last step: bf16 [rows, cols]
   int64_t mats;
+  Tail tail;
 };
 
 // Lower-triangular tile p (row by row) of a symmetric product.
@@ -283,36 +288,51 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
   constexpr bool BKM = KIND >= kApply;
   constexpr int kStageElems = PHASED ? 0 : C::NWAVES * RowPasses<C>::FLOATS * 2;
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS + kStageElems];
+  __shared__ int flag;
   const int first = xcd_logical_block(blockIdx.x, gridDim.x);
   if (first >= total) return;
-  const int K = KIND == kGram ? a.o.mp : a.o.np;
-  auto next_ops = [&](int tile, Ops16<C>& op) {
-    const OTile t = orth_tile<C, KIND>(a, tile);
+  const int nk = (KIND == kGram ? a.o.mp : a.o.np) / BK;
+  auto next_ops = [&](int unit, Ops16<C>& op) {
+    const Unit u = unit_of(a.tail, unit);
+    const KRange kr = split_range(nk, u.s, u.splits);
+    const OTile t = orth_tile<C, KIND>(a, u.tile);
     const char* ws = a.ws + t.mat * a.o.bytes;
     const uint32_t ldx = a.o.mp * 2, lds_ = a.o.np * 2;
     const int left = min(a.o.n - t.m * C::BM, C::BM);
-    op.nk = K / BK;
-    const char* A = ws + (KIND == kGram ? a.hi_in : KIND == kSquare ? a.o.r : a.o.s);
+    op.nk = kr.k1 - kr.k0;
+    const int K = op.nk * BK;
+    const char* A =
+        ws + (KIND == kGram ? a.hi_in : KIND == kSquare ? a.o.r : a.o.s) + int64_t(kr.k0) * BK * 2;
     const uint32_t lda = KIND == kGram ? ldx : lds_;
+    // rows end with the split's last k-step: the bytes after it are not read
+    const int64_t cut = lda - int64_t(K) * 2;
     kcontig_operand<C>(op.ra, op.ao, op.tail_a, A + int64_t(t.m) * C::BM * lda, left, lda,
-                       int64_t(left) * lda, K);
+                       int64_t(left) * lda - cut, K);
     if constexpr (BKM) {
-      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b, ws + a.hi_in,
-                               t.n * C::BN, ldx, int64_t(a.o.n) * ldx);
+      const int64_t k0 = int64_t(kr.k0) * BK;
+      kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b,
+                               ws + a.hi_in + k0 * ldx, t.n * C::BN, ldx, (a.o.n - k0) * ldx);
     } else {
       const int nleft = min(a.o.n - t.n * C::BN, C::BN);
       kcontig_operand<C>(op.rb, op.bo, op.tail_b, A + int64_t(t.n) * C::BN * lda, nleft, lda,
-                         int64_t(nleft) * lda, K);
+                         int64_t(nleft) * lda - cut, K);
     }
   };
   struct Epilogue {
     const StepArgs& a;
     int nk;
-    __device__ int k_steps(int) const { return nk; }
-    __device__ void operator()(int tile, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
+    int* flag;
+    __device__ int k_steps(int unit) const {
+      const Unit u = unit_of(a.tail, unit);
+      const KRange r = split_range(nk, u.s, u.splits);
+      return r.k1 - r.k0;
+    }
+    __device__ void operator()(int unit, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
                                float* stage) const {
       using P = RowPasses<C>;
-      const OTile t = orth_tile<C, KIND>(a, tile);
+      const Unit u = unit_of(a.tail, unit);
+      if (!join_splits<C>(acc, a.tail, unit, u, flag)) return;
+      const OTile t = orth_tile<C, KIND>(a, u.tile);
       char* ws = a.ws + t.mat * a.o.bytes;
       const int n = a.o.n, np = a.o.np, mp = a.o.mp, m = a.o.m;
       const int row0 = t.m * C::BM + wm * C::WM, col0 = t.n * C::BN + wn * C::WN;
@@ -427,7 +447,7 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
         }
       }
     }
-  } ep{a, K / BK};
+  } ep{a, nk, &flag};
   if constexpr (PHASED)
     stream_phased<C, TypeF16, false, BKM, true>(lds, first, gridDim.x, total, next_ops, ep);
   else
@@ -780,34 +800,72 @@ unsigned grid_of(int threads, int64_t tiles) {
 using TileBig = Tile<256, 256, 128, 64, 2>;  // 8 waves, two-phase loop
 using TileMid = Tile<128, 128, 64, 32, 3>;   // 8 waves, ring
 
-template <class C, int KIND>
-int64_t tile_count(const StepArgs& a) {
-  const int64_t tm = (a.o.n + C::BM - 1) / C::BM, tn = (a.o.m + C::BN - 1) / C::BN;
-  return a.mats * (KIND < kApply ? tm * (tm + 1) / 2 : tm * tn);
+// Tiles of a product and how its last round is shared. Big tiles run at the
+// higher rate, small ones fill the GPU: the one with the lesser modelled time,
+// rounds of 256 tiles at the measured times per k-step (256 x 256: 1.4 us with
+// the GPU full, 1.05 us half full; 128 x 128: 0.65 and 0.38) and per tile (8 and
+// 4 us).
+struct Plan {
+  bool big;
+  int tiles, whole, splits;
+  size_t bytes() const {  // of partial tiles
+    return splits > 1 ? size_t(tiles - whole) * splits * (big ? 256 * 256 : 128 * 128) * 4 : 0;
+  }
+};
+Plan plan(const OrthShape& o, int64_t mats, int kind) {
+  const int nk = (kind == kGram ? o.mp : o.np) / BK;
+  Plan best{};
+  double least = 0.0;
+  for (int big = 0; big < 2; ++big) {
+    const int b = big ? 256 : 128;
+    const int64_t tm = (o.n + b - 1) / b, tn = (o.m + b - 1) / b;
+    Plan p{};
+    p.big = big;
+    p.tiles = static_cast<int>(mats * (kind < kApply ? tm * (tm + 1) / 2 : tm * tn));
+    p.whole = p.tiles / kSlots * kSlots;
+    const float busy = big ? 1.4f : 0.65f, kb = b * b / 256;
+    p.splits = tail_splits(p.tiles - p.whole, nk, kSlots, busy, kb);
+    if (p.splits == 1) p.whole = p.tiles;
+    const double step = p.tiles * p.splits <= kSlots / 2 ? (big ? 1.05 : 0.38) : busy;
+    const double fixed = big ? 8.0 : 4.0;
+    double us = (p.whole + kSlots - 1) / kSlots * (nk * step + fixed);
+    if (p.splits > 1)
+      us += (nk + p.splits - 1) / p.splits * step + fixed + kb / 22.0 + p.splits * kb / 30.0;
+    if (big == 0 || us <= least) {
+      best = p;
+      least = us;
+    }
+  }
+  return best;
 }
 
 template <class C, int KIND, bool TALL, bool PHASED>
-void launch_product(const StepArgs& a, hipStream_t s) {
-  const int64_t total = tile_count<C, KIND>(a);
+void launch_product(const StepArgs& a, const Plan& p, hipStream_t s) {
+  const int units = p.whole + (p.tiles - p.whole) * p.splits;
   hipLaunchKernelGGL((orth_product_kernel<C, KIND, TALL, PHASED>),
-                     dim3(grid_of<orth_product_kernel<C, KIND, TALL, PHASED>>(C::NT, total)),
-                     dim3(C::NT), 0, s, a, static_cast<int>(total));
+                     dim3(grid_of<orth_product_kernel<C, KIND, TALL, PHASED>>(C::NT, units)),
+                     dim3(C::NT), 0, s, a, units);
 }
 
-// Big tiles run at the higher rate, small ones fill the GPU: rounds of 256
-// tiles at the measured times per k-step (256 x 256: 1.7 us with the GPU full,
-// 1.05 us half full; 128 x 128: 0.65 and 0.38) and per tile (8 and 4 us).
 template <int KIND, bool TALL>
-void product(const StepArgs& a, hipStream_t s) {
-  const double nk = (KIND == kGram ? a.o.mp : a.o.np) / BK;
-  auto us = [&](int64_t tiles, double busy, double idle, double fixed) {
-    return static_cast<double>((tiles + 255) / 256) * (nk * (tiles <= 128 ? idle : busy) + fixed);
-  };
-  if (us(tile_count<TileBig, KIND>(a), 1.7, 1.05, 8.0) <=
-      us(tile_count<TileMid, KIND>(a), 0.65, 0.38, 4.0))
-    launch_product<TileBig, KIND, TALL, true>(a, s);
+void product(StepArgs a, hipStream_t s) {
+  const Plan p = plan(a.o, a.mats, KIND);
+  a.tail.whole = p.whole;
+  a.tail.splits = p.splits;
+  if (p.big)
+    launch_product<TileBig, KIND, TALL, true>(a, p, s);
   else
-    launch_product<TileMid, KIND, TALL, false>(a, s);
+    launch_product<TileMid, KIND, TALL, false>(a, p, s);
+}
+
+// Partial tiles and counters behind the matrices' workspaces.
+size_t tail_part_bytes(const OrthShape& o, int64_t mats) {
+  size_t most = 0;
+  for (int kind = kGram; kind <= kApply; ++kind) {
+    const size_t b = plan(o, mats, kind).bytes();
+    if (b > most) most = b;
+  }
+  return most;
 }
 
 void steps(StepArgs a, const OrthArgs& p, hipStream_t s) {
@@ -841,7 +899,7 @@ void prepare(const PrepArgs& a, int64_t mats, hipStream_t s) {
 size_t orth_workspace(int64_t mats, int rows, int cols) {
   const OrthShape o = shape_of(rows, cols);
   if (o.n <= kSmallN && o.m <= kSmallM) return 0;
-  return static_cast<size_t>(mats) * o.bytes;
+  return static_cast<size_t>(mats) * o.bytes + kSlots * sizeof(int32_t) + tail_part_bytes(o, mats);
 }
 
 hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
@@ -862,6 +920,7 @@ hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
   a.m_in = p.m_in;
   a.m_out = p.m_out;
   a.ws = static_cast<char*>(p.ws);
+  a.count = reinterpret_cast<int32_t*>(a.ws + p.mats * o.bytes);
   a.o = o;
   a.rows = p.rows;
   a.cols = p.cols;
@@ -876,6 +935,8 @@ hipError_t launch_orth(const OrthArgs& p, hipStream_t s) {
   st.o = a.o;
   st.out = p.out;
   st.mats = p.mats;
+  st.tail.count = reinterpret_cast<int32_t*>(st.ws + p.mats * o.bytes);
+  st.tail.part = reinterpret_cast<float*>(st.tail.count + kSlots);
   steps(st, p, s);
   return hipGetLastError();
 }
