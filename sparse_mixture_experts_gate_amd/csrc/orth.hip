@@ -107,6 +107,9 @@ template <class T, bool MOM>
 __global__ __launch_bounds__(256) void orth_sum_kernel(PrepArgs a) {
   __shared__ double red[4];
   if (blockIdx.x == 0 && blockIdx.y == 0) a.count[threadIdx.x] = 0;
+  if (blockIdx.x == 0)  // the padding of the diagonal
+    for (int i = a.o.n + threadIdx.x; i < a.o.np; i += 256)
+      reinterpret_cast<float*>(a.ws + blockIdx.y * a.o.bytes + a.o.d)[i] = 0.0f;
   static_assert(kSlots == 256, "one counter per thread");
   const int64_t el = int64_t(a.rows) * a.cols, mat = blockIdx.y;
   const T* g = static_cast<const T*>(a.grad) + mat * el;
@@ -283,6 +286,16 @@ __device__ __forceinline__ OTile orth_tile(const StepArgs& a, int tile) {
   return t;
 }
 
+// Only the Gram product is long enough to share tiles (without the code for it
+// the others run 5% faster).
+template <int KIND>
+__device__ __forceinline__ Unit unit_at(const StepArgs& a, int unit) {
+  if constexpr (KIND == kGram)
+    return unit_of(a.tail, unit);
+  else
+    return {unit, 0, 1};
+}
+
 template <class C, int KIND, bool TALL, bool PHASED>
 __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a, int total) {
   constexpr bool BKM = KIND >= kApply;
@@ -293,7 +306,7 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
   if (first >= total) return;
   const int nk = (KIND == kGram ? a.o.mp : a.o.np) / BK;
   auto next_ops = [&](int unit, Ops16<C>& op) {
-    const Unit u = unit_of(a.tail, unit);
+    const Unit u = unit_at<KIND>(a, unit);
     const KRange kr = split_range(nk, u.s, u.splits);
     const OTile t = orth_tile<C, KIND>(a, u.tile);
     const char* ws = a.ws + t.mat * a.o.bytes;
@@ -323,15 +336,17 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
     int nk;
     int* flag;
     __device__ int k_steps(int unit) const {
-      const Unit u = unit_of(a.tail, unit);
+      const Unit u = unit_at<KIND>(a, unit);
       const KRange r = split_range(nk, u.s, u.splits);
       return r.k1 - r.k0;
     }
     __device__ void operator()(int unit, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
                                float* stage) const {
       using P = RowPasses<C>;
-      const Unit u = unit_of(a.tail, unit);
-      if (!join_splits<C>(acc, a.tail, unit, u, flag)) return;
+      const Unit u = unit_at<KIND>(a, unit);
+      if constexpr (KIND == kGram) {
+        if (!join_splits<C>(acc, a.tail, unit, u, flag)) return;
+      }
       const OTile t = orth_tile<C, KIND>(a, u.tile);
       char* ws = a.ws + t.mat * a.o.bytes;
       const int n = a.o.n, np = a.o.np, mp = a.o.mp, m = a.o.m;
@@ -340,108 +355,145 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
       float* D = reinterpret_cast<float*>(ws + a.o.d);
       float* Q = reinterpret_cast<float*>(ws + a.o.q);
       const _Float16* R = reinterpret_cast<const _Float16*>(ws + a.o.r);
+      if constexpr (KIND == kGram || KIND == kSquare) {
+        _Float16* dst = reinterpret_cast<_Float16*>(ws + (KIND == kGram ? a.o.r : a.o.s));
+        const int cc = min(col, np - 8);
+        f32x4_t dj[2] = {};
+        if constexpr (KIND == kSquare) {
+          dj[0] = *reinterpret_cast<const f32x4_t*>(D + cc);
+          dj[1] = *reinterpret_cast<const f32x4_t*>(D + cc + 4);
+        }
 #pragma unroll
-      for (int mi = 0; mi < C::MI; ++mi) {
-        P::put(stage, lane, acc[mi]);
-        if constexpr (KIND == kGram || KIND == kSquare) {
-          _Float16* dst = reinterpret_cast<_Float16*>(ws + (KIND == kGram ? a.o.r : a.o.s));
-          // eight outputs from the products v: rows `row`, columns `c` (both
-          // below n, or in the padding, where everything is zero)
-          auto finish = [&](float (&v)[8], int row, int c, bool diag) {
-            f16x8_t o;
-            if constexpr (KIND == kGram) {
+        for (int mi = 0; mi < C::MI; ++mi) {
+          f16x8_t r8[P::N];
+          float di[P::N];
+          if constexpr (KIND == kSquare) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float x = v[j] * (1.0f / (kScaleX * kScaleX));
-                if (diag && c + j == row) D[row] = x;
-                o[j] = static_cast<_Float16>(c + j == row ? 0.0f : x * kScaleR);
-              }
-            } else {
-              const f16x8_t r8 = *reinterpret_cast<const f16x8_t*>(R + int64_t(row) * np + c);
-              const float di = D[row];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float rij = static_cast<float>(r8[j]) * (1.0f / kScaleR);
-                const float dj = c + j < n ? D[c + j] : 0.0f;
-                const float rr = v[j] * (1.0f / (kScaleR * kScaleR));
-                if (diag && c + j == row) Q[row] = kB * di + kC * (rr + di * di);
-                const float x = kB * rij + kC * (rr + (di + dj) * rij);
-                o[j] = static_cast<_Float16>(c + j == row ? 0.0f : x * kScaleS);
-              }
+            for (int p = 0; p < P::N; ++p) {
+              const int row = min(row0 + mi * 32 + P::row(p, lane), n - 1);
+              r8[p] = *reinterpret_cast<const f16x8_t*>(R + int64_t(row) * np + cc);
+              di[p] = D[row];
             }
-            *reinterpret_cast<f16x8_t*>(dst + int64_t(row) * np + c) = o;
-          };
+          }
+          P::put(stage, lane, acc[mi]);
+          f16x8_t o[P::N];
 #pragma unroll
           for (int p = 0; p < P::N; ++p) {
+            const int row = row0 + mi * 32 + P::row(p, lane);
             float v[8];
             P::get(stage, lane, p, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bool diag = col + j == row;
+              if constexpr (KIND == kGram) {
+                if (diag && row < n) D[row] = v[j] * (1.0f / (kScaleX * kScaleX));
+                v[j] *= kScaleR / (kScaleX * kScaleX);
+              } else {
+                const float rij = static_cast<float>(r8[p][j]);
+                const float rr = v[j] * (1.0f / (kScaleR * kScaleR));
+                if (diag && row < n) Q[row] = kB * di[p] + kC * (rr + di[p] * di[p]);
+                v[j] = kScaleS * kC * rr +
+                       rij * (kScaleS / kScaleR * (kB + kC * (di[p] + dj[j >> 2][j & 3])));
+              }
+              // rows past n only put zeros into the mirrored tile's padding
+              o[p][j] = static_cast<_Float16>(diag || row >= n ? 0.0f : v[j]);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < P::N; ++p) {
             const int row = row0 + mi * 32 + P::row(p, lane);
-            if (row < n && col < np) finish(v, row, col, t.m == t.n);
+            if (row < n && col < np) *reinterpret_cast<f16x8_t*>(dst + int64_t(row) * np + col) = o[p];
           }
           if (t.m != t.n) {
-            // the mirrored tile: rows are this tile's columns, 32 of its
-            // columns (this pass's rows) at a time, 8 per lane
+            // The mirrored tile: these 32 rows go back to LDS in fp16 (pitch
+            // 144 bytes, so that four rows fall on distinct banks) and return
+            // transposed, 8 of them for one column per lane.
+            constexpr int kPitch = C::WN + 8;
+            static_assert(32 * kPitch * 2 <= P::FLOATS * 4, "fits the wave's stage");
+            _Float16* tile = reinterpret_cast<_Float16*>(stage);
 #pragma unroll
-            for (int p = 0; p < C::WN / 16; ++p) {
-              const int i = p * 16 + (lane & 15), k = (lane >> 4) * 8;
-              float v[8];
+            for (int p = 0; p < P::N; ++p)
+              *reinterpret_cast<f16x8_t*>(tile + P::row(p, lane) * kPitch + P::col(lane)) = o[p];
+            const int gr = lane >> 4, kj = (lane >> 2) & 3, cq = lane & 3;
+#pragma unroll
+            for (int c0 = 0; c0 < C::WN; c0 += 32)
+#pragma unroll
+              for (int k0 = 0; k0 < 32; k0 += 16) {
+                const _Float16* src =
+                    tile + (k0 + 8 * (gr >> 1) + kj) * kPitch + c0 + 16 * (gr & 1) + 4 * cq;
+                const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_i16x4_t*)(uintptr_t)lds_addr(src));
+                const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_i16x4_t*)(uintptr_t)lds_addr(src + 4 * kPitch));
+                typedef short i16x8_t __attribute__((ext_vector_type(8)));
+                const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                const int row = col0 + c0 + (lane & 31), c = row0 + mi * 32 + k0 + 8 * (lane >> 5);
+                if (row < n && c < np) *reinterpret_cast<i16x8_t*>(dst + int64_t(row) * np + c) = v;
+              }
+          }
+        }
+      } else {
+        // A wave's memory operations complete in order, so a load issued after a
+        // store waits for it: rows are loaded kAhead passes ahead, before the
+        // store of the pass in hand.
+        constexpr int kPasses = C::MI * P::N, kAhead = 4;
+        f16x8_t h[kAhead], l[kAhead];
+        const int cc = col < mp ? col : 0;
+        auto fetch = [&](int i) {
+          const int row = min(row0 + i / P::N * 32 + P::row(i % P::N, lane), n - 1);
+          const int64_t at = (int64_t(row) * mp + cc) * 2;
+          h[i % kAhead] = *reinterpret_cast<const f16x8_t*>(ws + a.hi_in + at);
+          l[i % kAhead] = *reinterpret_cast<const f16x8_t*>(ws + a.o.lo + at);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+        uint16_t* out = static_cast<uint16_t*>(a.out) + t.mat * n * int64_t(m);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int mi = i / P::N, p = i % P::N;
+          if (p == 0) P::put(stage, lane, acc[mi]);
+          float x[8];
+          P::get(stage, lane, p, x);
+          const int row = row0 + mi * 32 + P::row(p, lane);
+          const float f = kA + Q[min(row, n - 1)];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            x[j] = f * (static_cast<float>(h[i % kAhead][j]) +
+                        static_cast<float>(l[i % kAhead][j]) * (1.0f / kScaleLo)) +
+                   x[j] * (1.0f / kScaleS);
+          u32x4_t oh, ol;
+          if constexpr (KIND == kApply) {
+            f16x8_t hh, ll;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              _Float16 hi, lo;
+              split_x(x[j], hi, lo);
+              hh[j] = hi;
+              ll[j] = lo;
+            }
+            oh = __builtin_bit_cast(u32x4_t, hh);
+            ol = __builtin_bit_cast(u32x4_t, ll);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              oh[j] = pack_bf16x2(x[2 * j] * (1.0f / kScaleX), x[2 * j + 1] * (1.0f / kScaleX));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (i + kAhead < kPasses) fetch(i + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+          if (row < n && col < mp) {
+            if constexpr (KIND == kApply) {
+              const int64_t at = (int64_t(row) * mp + col) * 2;
+              *reinterpret_cast<u32x4_t*>(ws + a.hi_out + at) = oh;
+              *reinterpret_cast<u32x4_t*>(ws + a.o.lo + at) = ol;
+            } else if (!TALL && m % 8 == 0) {
+              if (col < m) *reinterpret_cast<u32x4_t*>(out + int64_t(row) * m + col) = oh;
+            } else {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                v[j] = stage[(k + j) * C::WN + (((i >> 2) ^ ((k + j) & (P::CPR - 1))) << 2) + (i & 3)];
-              const int row = col0 + i, c = row0 + mi * 32 + k;
-              if (row < n && c < np) finish(v, row, c, false);
-            }
-          }
-        } else {
-          f16x8_t h[P::N], l[P::N];
-#pragma unroll
-          for (int p = 0; p < P::N; ++p) {
-            const int row = row0 + mi * 32 + P::row(p, lane);
-            const int64_t at = (int64_t(row < n ? row : n - 1) * mp + (col < mp ? col : 0)) * 2;
-            h[p] = *reinterpret_cast<const f16x8_t*>(ws + a.hi_in + at);
-            l[p] = *reinterpret_cast<const f16x8_t*>(ws + a.o.lo + at);
-          }
-#pragma unroll
-          for (int p = 0; p < P::N; ++p) {
-            float v[8];
-            P::get(stage, lane, p, v);
-            const int row = row0 + mi * 32 + P::row(p, lane);
-            if (row >= n || col >= mp) continue;
-            const float f = kA + Q[row];
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              x[j] = f * (static_cast<float>(h[p][j]) +
-                          static_cast<float>(l[p][j]) * (1.0f / kScaleLo)) +
-                     v[j] * (1.0f / kScaleS);
-            if constexpr (KIND == kApply) {
-              f16x8_t ho, lo;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                _Float16 hh, ll;
-                split_x(x[j], hh, ll);
-                ho[j] = hh;
-                lo[j] = ll;
-              }
-              const int64_t at = (int64_t(row) * mp + col) * 2;
-              *reinterpret_cast<f16x8_t*>(ws + a.hi_out + at) = ho;
-              *reinterpret_cast<f16x8_t*>(ws + a.o.lo + at) = lo;
-            } else {
-              uint16_t* out = static_cast<uint16_t*>(a.out) + t.mat * n * int64_t(m);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] *= 1.0f / kScaleX;
-              if (!TALL && m % 8 == 0) {
-                if (col < m)
-                  *reinterpret_cast<uint4*>(out + int64_t(row) * m + col) =
-                      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (col + j < m)
-                    out[TALL ? int64_t(col + j) * n + row : int64_t(row) * m + col + j] =
-                        f32_to_bf16(x[j]);
-              }
+                if (col + j < m)
+                  out[TALL ? int64_t(col + j) * n + row : int64_t(row) * m + col + j] =
+                      static_cast<uint16_t>(oh[j >> 1] >> (16 * (j & 1)));
             }
           }
         }
@@ -824,7 +876,7 @@ Plan plan(const OrthShape& o, int64_t mats, int kind) {
     p.tiles = static_cast<int>(mats * (kind < kApply ? tm * (tm + 1) / 2 : tm * tn));
     p.whole = p.tiles / kSlots * kSlots;
     const float busy = big ? 1.4f : 0.65f, kb = b * b / 256;
-    p.splits = tail_splits(p.tiles - p.whole, nk, kSlots, busy, kb);
+    p.splits = kind == kGram ? tail_splits(p.tiles - p.whole, nk, kSlots, busy, kb) : 1;
     if (p.splits == 1) p.whole = p.tiles;
     const double step = p.tiles * p.splits <= kSlots / 2 ? (big ? 1.05 : 0.38) : busy;
     const double fixed = big ? 8.0 : 4.0;
@@ -860,12 +912,7 @@ void product(StepArgs a, hipStream_t s) {
 
 // Partial tiles and counters behind the matrices' workspaces.
 size_t tail_part_bytes(const OrthShape& o, int64_t mats) {
-  size_t most = 0;
-  for (int kind = kGram; kind <= kApply; ++kind) {
-    const size_t b = plan(o, mats, kind).bytes();
-    if (b > most) most = b;
-  }
-  return most;
+  return plan(o, mats, kGram).bytes();
 }
 
 void steps(StepArgs a, const OrthArgs& p, hipStream_t s) {
