@@ -138,9 +138,10 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_desc* desc, const void* dy, 
  * (X^T in place of X where rows > cols), out = X: the singular vectors of u
  * with singular values near 1, the update direction of the Muon optimizer.
  * The products run on fp16 matrix cores with fp32 accumulation; the diagonals
- * of A and of the polynomial and the low part of X are kept apart, which
- * leaves out about 5e-4 (2-norm) from the exact result before its rounding
- * to bf16. The norm is summed in fp64, so grad's scale does not matter.
+ * of A and of the polynomial and the low part of X are kept apart: up to five
+ * steps the result is about 1e-3 (2-norm) or less off the exact one before its
+ * rounding to bf16, rank-deficient updates included; more steps add about 3e-4
+ * each. The norm is summed in fp64, so grad's scale does not matter.
  *   n_mats       >= 0;  rows, cols 1 .. 16384
  *   grad_dtype   MOE_DT_F32 or MOE_DT_BF16
  *   steps        1 .. 16

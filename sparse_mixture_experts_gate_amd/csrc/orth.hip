@@ -15,8 +15,12 @@
 //        A A = R R + D R + R D + D D, of which only R R is a product;
 //   B  = b A + c A A = Q + S the same way: X <- (a + Q) X + S X.
 // Near convergence D and Q dominate their matrices, so their fp16 roundings
-// would be most of the error: on random matrices the result is 5e-4 off (2-norm)
+// would be most of the error: on random matrices the result is 6e-4 off (2-norm)
 // this way, 1.7e-3 with the diagonals inside, 1.1e-2 in bf16 throughout.
+// Only the last two steps multiply all of X by Q. Before them Q multiplies hi
+// alone, as S does: Q + S = B has the null space of X, and applied to two
+// different roundings of X its parts would leave noise there that later steps
+// amplify (64 x 1000 of rank 5: 3.1e-3 off, 7e-4 so).
 //
 // A and A A are symmetric: tiles on and below the diagonal are computed and
 // stored twice. Per step that leaves n^2 m + n^3 + 2 n^2 m operations.
@@ -153,7 +157,15 @@ __global__ __launch_bounds__(256) void orth_sum_kernel(PrepArgs a) {
         ((red[0] + red[1]) + red[2]) + red[3];
 }
 
+// v as a finished fp32 value. Without this the compiler may fold the product
+// behind v into the conversion of one use of hi (one rounding) and not of the
+// other (two), and in one element of some ten thousand the two differ.
+__device__ __forceinline__ float rounded(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
 __device__ __forceinline__ void split_x(float v, _Float16& hi, _Float16& lo) {
+  v = rounded(v);
   hi = static_cast<_Float16>(v);
   lo = static_cast<_Float16>((v - static_cast<float>(hi)) * kScaleLo);
 }
@@ -252,6 +264,7 @@ struct StepArgs {
   void* out;             // last step: bf16 [rows, cols]
   int64_t mats;
   Tail tail;
+  float low_q;           // 1: Q multiplies the low plane too (last two steps), else 0
 };
 
 // Lower-triangular tile p (row by row) of a symmetric product.
@@ -455,12 +468,12 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
           float x[8];
           P::get(stage, lane, p, x);
           const int row = row0 + mi * 32 + P::row(p, lane);
-          const float f = kA + Q[min(row, n - 1)];
+          const float q = Q[min(row, n - 1)];
+          const float fh = kA + q, fl = (kA + a.low_q * q) * (1.0f / kScaleLo);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            x[j] = f * (static_cast<float>(h[i % kAhead][j]) +
-                        static_cast<float>(l[i % kAhead][j]) * (1.0f / kScaleLo)) +
-                   x[j] * (1.0f / kScaleS);
+            x[j] = fh * static_cast<float>(h[i % kAhead][j]) +
+                   fl * static_cast<float>(l[i % kAhead][j]) + x[j] * (1.0f / kScaleS);
           u32x4_t oh, ol;
           if constexpr (KIND == kApply) {
             f16x8_t hh, ll;
@@ -652,7 +665,7 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
           const int c = wn * 64 + nj * 32 + 8 * q + 4 * half;
           f16x4_t h;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = static_cast<_Float16>(x[mi][nj][4 * q + j]);
+          for (int j = 0; j < 4; ++j) h[j] = static_cast<_Float16>(rounded(x[mi][nj][4 * q + j]));
           *reinterpret_cast<f16x4_t*>(X + x_off(r, c)) = h;
         }
   };
@@ -787,14 +800,18 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
     step_y(0, true);
 #pragma unroll 3
     for (int kk = 1; kk < nk; ++kk) step_y(kk, false);
+    const bool low_q = step + 2 >= a.steps;  // Q multiplies all of X, else its fp16 part
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
-      const float f = kA + Q[wm * 64 + mi * 32 + (lane & 31)];
+      const float q = Q[wm * 64 + mi * 32 + (lane & 31)];
 #pragma unroll
       for (int nj = 0; nj < 2; ++nj)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          x[mi][nj][e] = f * x[mi][nj][e] + y[mi][nj][e] * (1.0f / kScaleS);
+        for (int e = 0; e < 16; ++e) {
+          const float v = rounded(x[mi][nj][e]);
+          const float w = low_q ? v : static_cast<float>(static_cast<_Float16>(v));
+          x[mi][nj][e] = kA * v + (q * w + y[mi][nj][e] * (1.0f / kScaleS));
+        }
     }
     __syncthreads();  // every wave has read X and S
     if (step + 1 < a.steps) {
@@ -919,6 +936,7 @@ void steps(StepArgs a, const OrthArgs& p, hipStream_t s) {
   for (int i = 0; i < p.steps; ++i) {
     a.hi_in = i & 1 ? a.o.hi1 : a.o.hi0;
     a.hi_out = i & 1 ? a.o.hi0 : a.o.hi1;
+    a.low_q = i + 2 >= p.steps ? 1.0f : 0.0f;
     product<kGram, false>(a, s);
     product<kSquare, false>(a, s);
     if (i + 1 < p.steps)

@@ -70,15 +70,17 @@ def test_scale_of_the_gradient(scale):
 
 
 @pytest.mark.parametrize("rank", [1, 5, 32])
-def test_rank_deficient_updates(rank):
+@pytest.mark.parametrize("rows,cols", [(200, 330), (64, 1000), (100, 240)])
+@pytest.mark.parametrize("steps", [5, 8])
+def test_rank_deficient_updates(rank, rows, cols, steps):
     """The null space must stay empty: rounding noise there would grow 3.44
     times per step."""
     import sparse_mixture_experts_gate_amd as M
-    g = _rand(1, 2, 200, rank) @ _rand(2, 2, rank, 330)
-    out, _ = M.Muon().direction(g)
-    _check(out, g)
-    out, _ = M.Muon().direction(g.transpose(1, 2).contiguous())
-    _check(out, g.transpose(1, 2))
+    g = _rand(1, 2, rows, rank) @ _rand(2, 2, rank, cols)
+    out, _ = M.Muon(steps=steps).direction(g)
+    _check(out, g, steps=steps)
+    out, _ = M.Muon(steps=steps).direction(g.transpose(1, 2).contiguous())
+    _check(out, g.transpose(1, 2), steps=steps)
 
 
 def test_wide_spectrum_bf16_gradients_and_plain_momentum():
