@@ -174,33 +174,36 @@ __device__ __forceinline__ f32x16_t mma16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
 }
 
 // Output through LDS: the fragments' layout gives a lane 4 adjacent columns of
-// its row, which as stores would be 16-byte pieces of 32 rows. 32 rows of a
-// wave's WN columns at a time pass through its part of LDS (fp32, 16-byte
-// chunks XOR-swizzled with the row, free of bank conflicts both ways), and
-// come back as 8 adjacent columns of one row per lane: whole 128-byte lines
-// for 16-bit outputs.
-template <class C>
+// its row, which as stores would be 16-byte pieces of 32 rows. 32 rows of PJ of
+// a wave's 32-column parts at a time pass through its part of LDS (fp32, 16-byte
+// chunks XOR-swizzled with the row, free of bank conflicts both ways), and come
+// back as 8 adjacent columns of one row per lane: with 64 columns whole 128-byte
+// lines for 16-bit outputs.
+template <class C, int PJ = C::NJ>
 struct RowPasses {
-  static constexpr int CPR = C::WN / 4;            // chunks of a row
-  static constexpr int LPR = C::WN / 8;            // lanes of a row
+  static_assert(C::NJ % PJ == 0, "whole parts");
+  static constexpr int COLS = PJ * 32;
+  static constexpr int CPR = COLS / 4;             // chunks of a row
+  static constexpr int LPR = COLS / 8;             // lanes of a row
   static constexpr int RPP = 64 / LPR;             // rows of a pass
   static constexpr int N = 32 / RPP;               // passes over 32 rows
-  static constexpr int FLOATS = 32 * C::WN;        // LDS floats per wave
+  static constexpr int PARTS = C::NJ / PJ;         // column parts of a wave
+  static constexpr int FLOATS = 32 * COLS;         // LDS floats per wave
 
-  // row (0..31) and first column (within the wave's) of this lane in pass p
+  // row (0..31) and first column (within the part's) of this lane in pass p
   __device__ static int row(int p, int lane) { return p * RPP + lane / LPR; }
   __device__ static int col(int lane) { return (lane % LPR) * 8; }
 
-  __device__ static void put(float* stage, int lane, const f32x16_t (&acc)[C::NJ]) {
+  __device__ static void put(float* stage, int lane, const f32x16_t (&acc)[C::NJ], int part = 0) {
     const int r = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int nj = 0; nj < C::NJ; ++nj)
+    for (int nj = 0; nj < PJ; ++nj)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int c = (nj * 8 + 2 * g + h) ^ (r & (CPR - 1));
-        const f32x4_t v = {acc[nj][4 * g], acc[nj][4 * g + 1], acc[nj][4 * g + 2],
-                           acc[nj][4 * g + 3]};
-        *reinterpret_cast<f32x4_t*>(stage + r * C::WN + c * 4) = v;
+        const f32x16_t& x = acc[part * PJ + nj];
+        const f32x4_t v = {x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+        *reinterpret_cast<f32x4_t*>(stage + r * COLS + c * 4) = v;
       }
   }
   __device__ static void get(const float* stage, int lane, int p, float (&v)[8]) {
@@ -208,12 +211,16 @@ struct RowPasses {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const f32x4_t x =
-          *reinterpret_cast<const f32x4_t*>(stage + r * C::WN + ((c + i) ^ (r & (CPR - 1))) * 4);
+          *reinterpret_cast<const f32x4_t*>(stage + r * COLS + ((c + i) ^ (r & (CPR - 1))) * 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
     }
   }
 };
+// Passes that fit the waves' parts of one ring stage (8 waves).
+template <class C>
+using StagePasses =
+    RowPasses<C, (C::NWAVES * 32 * C::WN * 4 <= C::STAGE * 2 ? C::NJ : C::NJ / 2)>;
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -446,7 +453,7 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
           af[i] = frag_a<C, AKM>(lds, st, wm * C::WM + i * 32, kk, lane);
         if (kk < 2) {
 #pragma unroll
-          for (int i = kk * (NL / 2); i < (kk + 1) * (NL / 2); ++i) ld.load(st ^ 1, i);
+          for (int i = kk * ((NL + 1) / 2); i < (kk ? NL : (NL + 1) / 2); ++i) ld.load(st ^ 1, i);
           if (kk == 1) ld.advance();
         }
         if (kk == 3) vm_wait<0>();
@@ -465,9 +472,9 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
     }
     if (wave < 4) __builtin_amdgcn_s_barrier();
     // the stage just read is free until the next tile's first loads
-    static_assert(8 * RowPasses<C>::FLOATS * 4 <= C::STAGE * 2, "output stages fit");
+    static_assert(8 * StagePasses<C>::FLOATS * 4 <= C::STAGE * 2, "output stages fit");
     epilogue(tc, wm, wn, lane, acc,
-             reinterpret_cast<float*>(lds + (st ^ 1) * C::STAGE) + wave * RowPasses<C>::FLOATS);
+             reinterpret_cast<float*>(lds + (st ^ 1) * C::STAGE) + wave * StagePasses<C>::FLOATS);
     lds_barrier();
   }
   vm_wait<0>();

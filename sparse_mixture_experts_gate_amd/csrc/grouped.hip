@@ -176,7 +176,7 @@ __device__ __forceinline__ void put8(const GArgs& a, int64_t at, int cnt, const 
 // Output of a finished tile. Forward and dgrad hold the transposed tile and
 // store rows through LDS; wgrad holds the tile itself (a lane owns a column, so
 // one register across the wave is two 128-byte row pieces of fp32).
-template <class C, int MODE>
+template <class C, int MODE, class P>
 __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int wm, int wn, int lane,
                                            f32x16_t (&acc)[C::MI][C::NJ], float* stage) {
   if constexpr (MODE == kWgrad) {
@@ -199,21 +199,22 @@ __device__ __forceinline__ void store_tile(const GArgs& a, const GTile& c, int w
         }
     }
   } else {
-    using P = RowPasses<C>;
     const int N = MODE == kForward ? a.n : a.k;
-    const int col = c.n * C::BN + wn * C::WN + P::col(lane);
 #pragma unroll
-    for (int mi = 0; mi < C::MI; ++mi) {
-      P::put(stage, lane, acc[mi]);
+    for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
-      for (int p = 0; p < P::N; ++p) {
-        float v[8];
-        P::get(stage, lane, p, v);
-        const int r = c.m * C::BM + wm * C::WM + mi * 32 + P::row(p, lane);
-        if (r < c.rows && col < N)
-          put8(a, c.s * a.split_stride + (c.row0 + r) * a.ldo + col, N - col, v);
+      for (int part = 0; part < P::PARTS; ++part) {
+        const int col = c.n * C::BN + wn * C::WN + part * P::COLS + P::col(lane);
+        P::put(stage, lane, acc[mi], part);
+#pragma unroll
+        for (int p = 0; p < P::N; ++p) {
+          float v[8];
+          P::get(stage, lane, p, v);
+          const int r = c.m * C::BM + wm * C::WM + mi * 32 + P::row(p, lane);
+          if (r < c.rows && col < N)
+            put8(a, c.s * a.split_stride + (c.row0 + r) * a.ldo + col, N - col, v);
+        }
       }
-    }
   }
 }
 
@@ -382,8 +383,8 @@ grouped_any_kernel(GArgs a) {
       step(ks, 0, s0, s1);
       if (ks + 1 < kr.k1) step(ks + 1, 1, s1, s0);
     }
-    store_tile<C, MODE>(a, c, wm, wn, lane, acc,
-                        reinterpret_cast<float*>(lds) + wave * RowPasses<C>::FLOATS);
+    store_tile<C, MODE, RowPasses<C>>(a, c, wm, wn, lane, acc,
+                                      reinterpret_cast<float*>(lds) + wave * RowPasses<C>::FLOATS);
     __syncthreads();
   }
 }
@@ -408,7 +409,8 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   if (a.tail_part) {
     const int whole = tiles / gridDim.x * gridDim.x;
     const int nk = ((MODE == kForward ? a.k : a.n) + BK - 1) / BK;
-    tail.splits = tail_splits(tiles - whole, nk, gridDim.x, kBigStep, C::BM * C::BN / 256);
+    tail.splits = tail_splits(tiles - whole, nk, gridDim.x, kBigStep * C::BM / 256,
+                              C::BM * C::BN / 256);
     if (tail.splits > 1) tail.whole = whole;
   }
   const int total = tail.whole + (tiles - tail.whole) * tail.splits;
@@ -473,7 +475,8 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
         if (!join_splits<C>(acc, tail, unit, unit_of(tail, unit), flag)) return;
         c.s = 0;
       }
-      store_tile<C, MODE>(a, c, wm, wn, lane, acc, stage);
+      using P = std::conditional_t<PHASED, StagePasses<C>, RowPasses<C>>;
+      store_tile<C, MODE, P>(a, c, wm, wn, lane, acc, stage);
     }
   } ep{a, tail, &flag, locate, range};
   if constexpr (PHASED)
@@ -548,6 +551,7 @@ __global__ __launch_bounds__(256) void grouped_finish_kernel(FinishArgs a) {
 // ---- choice of the kernel -------------------------------------------------------
 
 using TileBig = Tile<256, 256, 128, 64, 2>;          // 8 waves, two-phase loop, 128 KB LDS
+using TileFlat = Tile<192, 256, 96, 64, 2>;          // the same where these fill one round, 112 KB
 using TileMid = Tile<128, 128, 64, 32, 3>;           // 8 waves
 using TileDec = Tile<32, 128, 32, 64, 6, true>;      // 2 waves, weights streamed past L2
 
@@ -559,7 +563,7 @@ int64_t tile_bound(const GArgs& a) {
   return full * tn;
 }
 
-enum Config { kBig = 0, kMid = 1, kDec = 2, kAny = 3, kAnyBig = 4 };
+enum Config { kBig, kFlat, kMid, kDec, kAny, kAnyBig };
 
 struct Choice {
   int config, splits;
@@ -588,6 +592,7 @@ struct TileCost {
 };
 constexpr TileCost kCosts[] = {
     {kBig, 256, 256, 256, 1.7, 1.05, 8.0, 12.0},
+    {kFlat, 192, 256, 256, 1.46, 0.8, 8.0, 0.0},
     {kMid, 128, 128, 256, 0.65, 0.38, 4.0, 4.0},
     {kDec, 32, 128, 256, 0.6, 0.35, 3.0, 0.0},
     {kAny, 128, 128, 256, 0.95, 0.8, 5.0, 5.0},
@@ -602,6 +607,9 @@ constexpr TileCost kCosts[] = {
 //   x [1000, 2048], 8 x 1408                128^2: 21, 32 x 128: 32, 256^2: 43
 //   x [2048, 7168], 32 x 4096               128^2: 335, 256^2: 399, 32 x 128: 563
 //   x [8192, 7168], 32 x 4096               256^2: 610, 128^2: 717
+//   x [5000, 2048], 8 x 2048                192 x 256: 48, 128^2: 53
+//   x [3000, 4096], 1 x 4096                192 x 256: 88, 256^2: 97
+//   x [30000, 2048], 100 x 1408             256^2: 250, 192 x 256: 274
 //   x [8192, 4095], 8 x 2048                128 x 256: 297, 128^2: 326 (any alignment)
 //   x [2311, 613], 9 x 1407                 128^2: 25, 128 x 256: 31 (any alignment)
 //   dw of 8000 rows, 2 x 256 x 256          4 splits: 26, 1: 53 (128^2), 129 (256^2)
@@ -633,17 +641,23 @@ Choice choose(const GroupedArgs& p, bool aligned) {
     for (int splits = 1; splits <= 16 && (splits == 1 || splits * 4 <= nk); splits *= 2) {
       const double units = tiles * splits;
       const double step = units <= t.slots / 2 ? t.idle : t.busy;
-      // a 256 x 256 tile of a long contraction in the last round is shared by the
+      // A tile of a long contraction in the last round is shared by the
       // workgroups that this round leaves idle; that takes a launch to clear the
-      // counters, so it is left out where little can be won
-      const bool tail = t.config == kBig && p.mode != kWgrad && splits == 1 && nk >= 48.0;
-      double rounds = std::ceil(units / t.slots), us = 0.0;
-      if (tail) {
+      // counters, so it is left out where little can be won. With more than one
+      // group the number of tiles is an estimate: half a round stands for what
+      // the last one holds, a quarter where it is shared.
+      const bool tail = t.config <= kFlat && p.mode != kWgrad && splits == 1 && nk >= 48.0;
+      const double share = units / t.slots;
+      double rounds = std::ceil(share), us = 0.0;
+      if (p.mode != kWgrad && p.n_groups > 1) {
+        if (share > 1.0) rounds = share + (tail ? 0.25 : 0.5);
+      } else if (tail) {
+        const float k_us = kBigStep * t.bm / 256, kb = t.bm * t.bn / 256.0f;
         const int rest = static_cast<int>(units) % t.slots, k = static_cast<int>(nk);
-        const int s = tail_splits(rest, k, t.slots, kBigStep, 256.0f);
+        const int s = tail_splits(rest, k, t.slots, k_us, kb);
         if (s > 1) {
-          rounds = std::floor(units / t.slots);
-          us = 5.0 + (k + s - 1) / s * kBigStep + t.fixed + 256.0 / 22.0 + s * 256.0 / 30.0;
+          rounds = std::floor(share);
+          us = 5.0 + (k + s - 1) / s * k_us + t.fixed + kb / 22.0 + s * kb / 30.0;
         }
       }
       us += rounds * (std::ceil(nk / splits) * step +
@@ -682,6 +696,8 @@ void launch_config(const GArgs& a, int config, hipStream_t s) {
     launch_any<TileAny, MODE>(a, s);
   } else if (config == kAnyBig) {
     if constexpr (MODE != kWgrad) launch_any<TileAnyBig, MODE>(a, s);
+  } else if (config == kFlat) {
+    if constexpr (MODE != kWgrad) launch_fast<TileFlat, MODE, true>(a, s);
   } else if (config == kMid) {
     launch_fast<TileMid, MODE, false>(a, s);
   } else if (config == kDec) {

@@ -355,7 +355,8 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
     }
     __device__ void operator()(int unit, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
                                float* stage) const {
-      using P = RowPasses<C>;
+      using P = std::conditional_t<PHASED, StagePasses<C>, RowPasses<C>>;
+      static_assert(P::PARTS == 1, "a wave's columns together");
       const Unit u = unit_at<KIND>(a, unit);
       if constexpr (KIND == kGram) {
         if (!join_splits<C>(acc, a.tail, unit, u, flag)) return;

@@ -95,6 +95,17 @@ def test_products(rows, groups, n, k, skew):
     _check(x, w, dy, off_h, off, f"{rows}x{groups}x{n}x{k}")
 
 
+@pytest.mark.parametrize("n,k,lens", [
+    (2048, 2048, [600, 1, 700, 900, 500, 799, 0, 1500]),
+    # more tiles than expected of so many rows: the last round's are shared
+    (2048, 3208, [577] * 5 + [769] * 3), (3208, 2048, [577] * 5 + [769] * 3),
+])
+def test_tiles_of_192_rows(n, k, lens):
+    off_h, off = _off(lens)
+    x, dy = _rand(1, sum(lens), k), _rand(2, sum(lens), n)
+    _check(x, _rand(3, len(lens), n, k, scale=0.1), dy, off_h, off, f"{n}x{k}")
+
+
 def test_empty_groups_and_rows_outside():
     """Empty groups at both ends and inside; rows before the first and past the
     last group keep what they held; no rows at all."""
