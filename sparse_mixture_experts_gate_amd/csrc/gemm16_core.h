@@ -401,7 +401,10 @@ __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, in
 // multiply (8 MFMAs) while those of the other half read the next sub-step's
 // fragments and issue loads, then they swap, so each SIMD's matrix core has
 // work in every phase. Two stages of 64 KB: the loads of step k + 1 go out in
-// the first two phases of step k and are waited for in its last.
+// the first two memory phases of step k, or the first three where B's
+// transposing reads make these longer (12288 rows, 4096 x 7168, input gradient:
+// 599 us with two, 580 with three; forward: 553 and 568), and are waited for in
+// its last.
 //
 // Rows of a tile past its data are multiplied all the same: leaving out waves
 // whose part of the tile is empty took as long (the loads set the pace there),
@@ -428,6 +431,7 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   constexpr int NL = C::A_LOADS + C::B_LOADS;
+  constexpr int PARTS = BKM && !AKM ? 3 : 2, PER = (NL + PARTS - 1) / PARTS;
   Loader<C, AKM, BKM, std::remove_reference_t<NextOps>> ld(next_ops, lds_addr(lds), first, nb,
                                                             total, wave);
   bf16x8_t af[C::MI], bfr[C::NJ];
@@ -451,10 +455,10 @@ __device__ __forceinline__ void stream_phased(uint16_t* lds, int first, int nb, 
 #pragma unroll
         for (int i = 0; i < C::MI; ++i)
           af[i] = frag_a<C, AKM>(lds, st, wm * C::WM + i * 32, kk, lane);
-        if (kk < 2) {
+        if (kk < PARTS) {
 #pragma unroll
-          for (int i = kk * ((NL + 1) / 2); i < (kk ? NL : (NL + 1) / 2); ++i) ld.load(st ^ 1, i);
-          if (kk == 1) ld.advance();
+          for (int i = kk * PER; i < (kk + 1) * PER && i < NL; ++i) ld.load(st ^ 1, i);
+          if (kk == PARTS - 1) ld.advance();
         }
         if (kk == 3) vm_wait<0>();
         lds_barrier();
