@@ -111,8 +111,9 @@ typedef struct moe_grouped_desc {
 
 enum { MOE_GROUPED_FORWARD = 0, MOE_GROUPED_DGRAD = 1, MOE_GROUPED_WGRAD = 2 };
 
-/* Bytes of workspace for the product `op`: partial sums where the outputs are
- * too few to occupy the GPU, 0 otherwise (ws may then be NULL). Host only. */
+/* Bytes of workspace for the product `op`: partial sums where the outputs (or
+ * the last ones of a long contraction) are too few to occupy the GPU, 0
+ * otherwise (ws may then be NULL). Host only. */
 moe_status moe_grouped_gemm_workspace_size(const moe_grouped_desc* desc, int32_t op,
                                            size_t* bytes);
 

@@ -161,7 +161,8 @@ struct FwdArgs {
 //
 // Mean first, then the squares of what is left, both from registers: merging
 // per-lane moments in one pass is as stable but took ten times the vector
-// operations, and those then bound the kernel (8192 x 7168 bf16: 73 us).
+// operations, and those then bound the kernel. Bound by memory: 8192 x 7168
+// bf16 with a residual takes 98 us, 470 MB at 4.8 TB/s, a large copy's rate.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdArgs a) {
   __shared__ float slot[2][NW];
@@ -316,6 +317,8 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* slot) {
 // each block then writes one partial sum per column. The next row is loaded
 // while the current one is reduced. With NW == 1 the block's four waves add
 // their column sums through LDS, in wave order.
+// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 92 us, 470 MB
+// at 5.1 TB/s.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNormArgs a) {
   constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
@@ -489,26 +492,35 @@ __global__ __launch_bounds__(64) void norm_cols_kernel(BwdNormArgs a) {
   store8(pw + a.d + i0, ab, cnt);
 }
 
-// dweight, dbias = sums of the partial rows [parts][2 d], in order: a block
-// takes 64 columns, its 16 waves a sixteenth of the parts each, then the
-// waves' sums are added in wave order.
+// dweight, dbias = sums of the partial rows [parts][2 d], in a fixed order: a
+// block takes 32 columns, its 32 half-waves a run of the parts each, whose sums
+// are then added in order. Latency-bound: eight loads in flight per
+// lane, half the columns of a wave per block (8192 x 2048 bf16, the whole
+// backward: 31 us with one load and 64 columns, 23 so).
 __global__ __launch_bounds__(1024) void norm_sum_parts_kernel(const float* part, int parts, int d,
                                                               float* dw, float* db) {
-  __shared__ float red[16][64];
-  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t col = int64_t(blockIdx.x) * 64 + lane;
+  __shared__ float red[32][32];
+  const int run = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t width = 2 * int64_t(d), col = int64_t(blockIdx.x) * 32 + lane;
   float s = 0.0f;
-  if (col < 2 * int64_t(d)) {
-    const int per = (parts + 15) / 16;
-    const int p1 = min(parts, (wv + 1) * per);
-    for (int p = wv * per; p < p1; ++p) s += part[int64_t(p) * 2 * d + col];
-  }
-  red[wv][lane] = s;
-  __syncthreads();
-  if (wv || col >= 2 * int64_t(d)) return;
-  s = red[0][lane];
+  if (col < width) {
+    const int per = (parts + 31) / 32, p0 = run * per, p1 = min(parts, p0 + per);
+    const float* at = part + p0 * width + col;
+    int left = p1 - p0;
+    for (; left >= 8; left -= 8, at += 8 * width) {
+      float v[8];
 #pragma unroll
-  for (int w = 1; w < 16; ++w) s += red[w][lane];
+      for (int i = 0; i < 8; ++i) v[i] = at[i * width];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; left > 0; --left, at += width) s += *at;
+  }
+  red[run][lane] = s;
+  __syncthreads();
+  if (run || col >= width) return;
+#pragma unroll
+  for (int w = 1; w < 32; ++w) s += red[w][lane];
   if (col < d) {
     if (dw) dw[col] = s;
   } else if (db) {
@@ -586,8 +598,8 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
 
 // Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
 // More blocks hide more latency but write and add more partial rows (8192 x 7168
-// bf16 with dresidual: 97 us with 256 blocks of 8 waves, 113 with 512; 8192 x
-// 2048: 34 us with 512 of 4 waves, 42 with 256, 38 with 768).
+// bf16 with dresidual: 92 us with 256 blocks of 8 waves, 103 with 512; 8192 x
+// 4096: 54 us with 512 of 4 waves, 59 with 768, 64 with 1024).
 int norm_backward_parts(int64_t n, int d) {
   if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);
   const int nw = row_shape(d).nw;
@@ -627,7 +639,7 @@ hipError_t launch_norm_backward(const NormArgs& p, float* dw, float* db, float* 
       p.r ? bwd_dispatch<float, true>(a, parts, s) : bwd_dispatch<float, false>(a, parts, s);
   }
   if (sums)
-    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((2 * p.d + 63) / 64), dim3(1024), 0, s, part,
+    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, s, part,
                        p.n > 0 ? parts : 0, p.d, dw, db);
   return hipGetLastError();
 }
