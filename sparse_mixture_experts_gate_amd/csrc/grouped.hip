@@ -235,6 +235,7 @@ __device__ __forceinline__ uint4 chunk_any(const uint16_t* p, int cnt, const uin
 }
 
 using TileAny = Tile<128, 128, 64, 32, 2>;   // 8 waves
+using TileAnyLow = Tile<64, 128, 32, 32, 2>;   // 8 waves, for groups of few rows
 using TileAnyBig = Tile<128, 256, 64, 64, 2>;  // a quarter fewer loaded bytes per product
 
 // Odd widths, pitches or base addresses: operands pass through registers
@@ -573,7 +574,7 @@ int64_t tile_bound(const GArgs& a) {
   return full * tn;
 }
 
-enum Config { kBig, kFlat, kMid, kDec, kAny, kAnyBig };
+enum Config { kBig, kFlat, kMid, kDec, kAny, kAnyLow, kAnyBig };
 
 struct Choice {
   int config, splits;
@@ -606,6 +607,7 @@ constexpr TileCost kCosts[] = {
     {kMid, 128, 128, 256, 0.65, 0.38, 4.0, 4.0},
     {kDec, 32, 128, 256, 0.6, 0.35, 3.0, 0.0},
     {kAny, 128, 128, 256, 0.95, 0.8, 5.0, 5.0},
+    {kAnyLow, 64, 128, 256, 0.6, 0.6, 5.0, 0.0},
     {kAnyBig, 128, 256, 256, 1.45, 1.2, 8.0, 0.0},
 };
 
@@ -622,6 +624,7 @@ constexpr TileCost kCosts[] = {
 //   x [30000, 2048], 100 x 1408             256^2: 250, 192 x 256: 274
 //   x [8192, 4095], 8 x 2048                128 x 256: 297, 128^2: 326 (any alignment)
 //   x [2311, 613], 9 x 1407                 128^2: 25, 128 x 256: 31 (any alignment)
+//   dx of [2311, 1407], 9 x 613             64 x 128: 24, 128^2: 30 (any alignment)
 //   dw of 8000 rows, 2 x 256 x 256          4 splits: 26, 1: 53 (128^2), 129 (256^2)
 //   x [8, 4096], 1 x 2048                   4 splits: 22, 1: 26 (32 x 128)
 // Splits add the finishing launch and the partial sums' traffic, so they pay
@@ -704,6 +707,8 @@ template <int MODE>
 void launch_config(const GArgs& a, int config, hipStream_t s) {
   if (config == kAny) {
     launch_any<TileAny, MODE>(a, s);
+  } else if (config == kAnyLow) {
+    if constexpr (MODE != kWgrad) launch_any<TileAnyLow, MODE>(a, s);
   } else if (config == kAnyBig) {
     if constexpr (MODE != kWgrad) launch_any<TileAnyBig, MODE>(a, s);
   } else if (config == kFlat) {
