@@ -396,7 +396,7 @@ grouped_any_kernel(GArgs a) {
 // straight into LDS.
 //
 // What bounds it, measured: 32 x 128 tiles the stream of weights (128 rows over
-// 256 experts of 4096 x 7168: 840 us, 7.0 TB/s); 256 x 256 tiles the matrix
+// 256 experts of 4096 x 7168: 858 us, 6.9 TB/s); 256 x 256 tiles the matrix
 // cores and, per tile, the rows that pad a group to whole tiles and an output
 // of 6 us that nothing overlaps (12288 rows, one group of 4096 x 7168: 1.29
 // PFLOP/s; 24576 rows over 64 groups of 2816 x 2048: 0.81, 42% more rows
