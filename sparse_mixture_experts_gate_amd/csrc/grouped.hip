@@ -450,10 +450,16 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
     const int64_t k0 = int64_t(kr.k0) * BK;
     const int K = static_cast<int>(min(int64_t(depth(c)), int64_t(kr.k1) * BK) - k0);
     if constexpr (MODE == kWgrad) {
+      // A dword that the resource's end cuts reads as zero, so an odd width ends
+      // with the dword of its last value: rows start on 16 bytes, so the other
+      // half of it is in the same aligned dword, and only feeds column n (or k),
+      // which is not stored.
       kmajor_operand<C, C::BM>(op.ra, op.ao, op.base_a, op.left_a, op.step_a,
-                               a.a + (c.row0 + k0) * a.lda, c.m * C::BM, lda, span(K, lda, a.n));
+                               a.a + (c.row0 + k0) * a.lda, c.m * C::BM, lda,
+                               span(K, lda, (a.n + 1) & ~1));
       kmajor_operand<C, C::BN>(op.rb, op.bo, op.base_b, op.left_b, op.step_b,
-                               a.b + (c.row0 + k0) * a.ldb, c.n * C::BN, ldb, span(K, ldb, a.k));
+                               a.b + (c.row0 + k0) * a.ldb, c.n * C::BN, ldb,
+                               span(K, ldb, (a.k + 1) & ~1));
     } else {
       const int left = c.rows - c.m * C::BM;
       kcontig_operand<C>(op.ra, op.ao, op.tail_a, a.a + (c.row0 + int64_t(c.m) * C::BM) * a.lda + k0,
