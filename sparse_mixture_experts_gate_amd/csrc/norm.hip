@@ -545,8 +545,12 @@ RowShape row_shape(int d) {
   return {8, 4};
 }
 
+// Blocks of one launch: its work items, up to 512 a block, are counted in 32
+// bits and wrap around silently. More rows take further launches.
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;
+
 template <class T, bool RES>
-void fwd_dispatch(const FwdArgs& a, hipStream_t s) {
+void fwd_launch(const FwdArgs& a, hipStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.n), quads = static_cast<unsigned>((a.n + 3) / 4);
   if (a.d > kMaxRow) {
     hipLaunchKernelGGL(norm_fwd_long_kernel<T>, dim3(rows), dim3(512), 0, s, a);
@@ -569,13 +573,39 @@ void fwd_dispatch(const FwdArgs& a, hipStream_t s) {
 }
 
 template <class T, bool RES>
+void fwd_dispatch(const FwdArgs& a, hipStream_t s) {
+  const int64_t per = kMaxBlocks * (a.d <= kMaxRow && row_shape(a.d).nw == 1 ? 4 : 1);
+  for (int64_t row = 0; row < a.n; row += per) {
+    FwdArgs b = a;
+    b.n = a.n - row < per ? a.n - row : per;
+    b.x = static_cast<const T*>(a.x) + row * a.ldx;
+    if (RES) b.r = static_cast<const T*>(a.r) + row * a.ldr;
+    b.y = static_cast<T*>(a.y) + row * a.ldy;
+    if (RES) b.sum = static_cast<T*>(a.sum) + row * a.lds;
+    if (a.mean) b.mean = a.mean + row;
+    if (a.mean) b.rstd = a.rstd + row;
+    fwd_launch<T, RES>(b, s);
+  }
+}
+
+template <class T, bool RES>
 void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
   if (a.d > kMaxRow) {
     // the column sums first: dx may take dy's place
     if (a.part)
       hipLaunchKernelGGL(norm_cols_kernel<T>, dim3((a.d + 511) / 512, parts), dim3(64), 0, s, a);
-    hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3(static_cast<unsigned>(a.n)), dim3(512), 0, s,
-                       a);
+    for (int64_t row = 0; row < a.n; row += kMaxBlocks) {
+      BwdNormArgs b = a;
+      b.n = a.n - row < kMaxBlocks ? a.n - row : kMaxBlocks;
+      b.dy = static_cast<const T*>(a.dy) + row * a.ldy;
+      b.x = static_cast<const T*>(a.x) + row * a.ldx;
+      if (a.dr) b.dr = static_cast<const T*>(a.dr) + row * a.ldr;
+      b.dx = static_cast<T*>(a.dx) + row * a.lds;
+      b.mean = a.mean + row;
+      b.rstd = a.rstd + row;
+      hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3(static_cast<unsigned>(b.n)), dim3(512), 0, s,
+                         b);
+    }
     return;
   }
   const RowShape r = row_shape(a.d);
