@@ -4,6 +4,7 @@ allocate outputs and keep the workspace; all arithmetic is the library's."""
 from __future__ import annotations
 
 import contextlib
+import threading
 
 import torch
 
@@ -44,16 +45,30 @@ def _vector(t, name: str, dtype: torch.dtype, n: int) -> None:
 
 
 class _Workspace:
-    """One buffer per stream, grown as calls need it."""
+    """One buffer per stream and host thread, grown as calls need it. Two
+    threads that use one stream have a buffer each: a call's kernels meet in
+    its workspace, and the other thread's may be enqueued between them. A call
+    that is being captured gets a buffer of its own from the graph's memory
+    pool, since replays write to that address whatever eager calls do later."""
 
     def __init__(self):
-        self._bufs = {}
+        self._local = threading.local()
+
+    @property
+    def _bufs(self) -> dict:
+        """The calling thread's buffers."""
+        if not hasattr(self._local, "bufs"):
+            self._local.bufs = {}
+        return self._local.bufs
 
     def get(self, need: int, device, stream) -> torch.Tensor:
-        key = (device, O._stream(stream))
-        buf = self._bufs.get(key)
+        """A buffer of at least `need` bytes; called with `stream` current."""
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        bufs, key = self._bufs, (device, O._stream(stream))
+        buf = bufs.get(key)
         if buf is None or buf.numel() < need:
-            buf = self._bufs[key] = torch.empty(need, dtype=torch.uint8, device=device)
+            buf = bufs[key] = torch.empty(need, dtype=torch.uint8, device=device)
         return buf
 
 
@@ -130,7 +145,8 @@ class GroupedLinear:
                              f"{weight.dtype} {list(weight.shape)}")
         self.weight = weight
 
-    _ws = _Workspace()  # partial sums of small products, shared by all maps of a stream
+    # partial sums of few outputs, shared by all maps of a stream and thread
+    _ws = _Workspace()
 
     @staticmethod
     def _workspace(desc, op, device, stream):
