@@ -66,15 +66,23 @@ def lib() -> ctypes.CDLL:
 
 
 def _p(t) -> int | None:
-    """Device pointer of a tensor (None -> NULL); row matrices may be strided,
-    which their descriptor says."""
+    """Device pointer of a contiguous tensor (None -> NULL)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor or None")
-    if not t.is_contiguous() and t.stride(-1) != 1:
-        raise ValueError("tensors passed to the library must have contiguous columns")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t) -> int | None:
+    """Device pointer of a row matrix. Its rows may be strided, as the
+    descriptor says, and counted by several leading dimensions."""
+    if isinstance(t, torch.Tensor) and t.dim() > 1 and t.stride(-1) == 1 and all(
+            t.stride(i) == t.stride(i + 1) * t.size(i + 1) for i in range(t.dim() - 2)):
+        return t.data_ptr()
+    return _p(t)
 
 
 def _stream(stream) -> int:
@@ -89,9 +97,9 @@ def _nbytes(t) -> int:
 
 
 def moe_layernorm_forward(desc, x, residual, weight, bias, y, sum, mean, rstd, stream=None):
-    L._check(lib().moe_layernorm_forward(ctypes.byref(desc), _p(x), _p(residual), _p(weight),
-                                         _p(bias), _p(y), _p(sum), _p(mean), _p(rstd),
-                                         _stream(stream)), "moe_layernorm_forward")
+    L._check(lib().moe_layernorm_forward(ctypes.byref(desc), _rows(x), _rows(residual),
+                                         _p(weight), _p(bias), _rows(y), _rows(sum), _p(mean),
+                                         _p(rstd), _stream(stream)), "moe_layernorm_forward")
 
 
 def moe_layernorm_backward_workspace_size(desc) -> int:
@@ -103,9 +111,10 @@ def moe_layernorm_backward_workspace_size(desc) -> int:
 
 def moe_layernorm_backward(desc, dy, x, weight, mean, rstd, dresidual, dx, dweight, dbias, ws,
                            stream=None):
-    L._check(lib().moe_layernorm_backward(ctypes.byref(desc), _p(dy), _p(x), _p(weight), _p(mean),
-                                          _p(rstd), _p(dresidual), _p(dx), _p(dweight), _p(dbias),
-                                          _p(ws), _nbytes(ws), _stream(stream)),
+    L._check(lib().moe_layernorm_backward(ctypes.byref(desc), _rows(dy), _rows(x), _p(weight),
+                                          _p(mean), _p(rstd), _rows(dresidual), _rows(dx),
+                                          _p(dweight), _p(dbias), _p(ws), _nbytes(ws),
+                                          _stream(stream)),
              "moe_layernorm_backward")
 
 
@@ -120,19 +129,19 @@ def moe_grouped_gemm_workspace_size(desc, op) -> int:
 
 
 def moe_grouped_gemm(desc, x, w, offsets, y, ws=None, stream=None):
-    L._check(lib().moe_grouped_gemm(ctypes.byref(desc), _p(x), _p(w), _p(offsets), _p(y), _p(ws),
-                                    _nbytes(ws), _stream(stream)), "moe_grouped_gemm")
+    L._check(lib().moe_grouped_gemm(ctypes.byref(desc), _rows(x), _p(w), _p(offsets), _rows(y),
+                                    _p(ws), _nbytes(ws), _stream(stream)), "moe_grouped_gemm")
 
 
 def moe_grouped_gemm_dgrad(desc, dy, w, offsets, dx, ws=None, stream=None):
-    L._check(lib().moe_grouped_gemm_dgrad(ctypes.byref(desc), _p(dy), _p(w), _p(offsets), _p(dx),
-                                          _p(ws), _nbytes(ws), _stream(stream)),
+    L._check(lib().moe_grouped_gemm_dgrad(ctypes.byref(desc), _rows(dy), _p(w), _p(offsets),
+                                          _rows(dx), _p(ws), _nbytes(ws), _stream(stream)),
              "moe_grouped_gemm_dgrad")
 
 
 def moe_grouped_gemm_wgrad(desc, dy, x, offsets, dw, ws=None, stream=None):
-    L._check(lib().moe_grouped_gemm_wgrad(ctypes.byref(desc), _p(dy), _p(x), _p(offsets), _p(dw),
-                                          _p(ws), _nbytes(ws), _stream(stream)),
+    L._check(lib().moe_grouped_gemm_wgrad(ctypes.byref(desc), _rows(dy), _rows(x), _p(offsets),
+                                          _p(dw), _p(ws), _nbytes(ws), _stream(stream)),
              "moe_grouped_gemm_wgrad")
 
 

@@ -45,3 +45,35 @@ def test_captured_calls_do_not_share_or_keep_a_workspace(one_stream, monkeypatch
     assert len({t.data_ptr() for t in (eager, first, second)}) == 3
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     assert ws.get(100, "cpu", None) is eager
+
+
+def test_only_row_matrices_may_be_strided():
+    """Descriptors have row strides for row matrices; weights, dw, vectors and
+    the update's matrices are read as contiguous, so anything else is refused."""
+    z = torch.zeros
+    f, bf = torch.float32, torch.bfloat16
+    norm = _ops.MoeNormDesc(n=2, d=4, dtype=1, eps=1e-5)
+    grp = _ops.MoeGroupedDesc(rows=6, n_groups=2, n=4, k=8, out_dtype=1)
+    orth = _ops.MoeOrthDesc(n_mats=2, rows=4, cols=8, grad_dtype=0, steps=5)
+    x, dy, w, off = z(6, 8, dtype=bf), z(6, 4, dtype=bf), z(2, 4, 8, dtype=bf), z(3, dtype=torch.int32)
+    rows, vec, mat = z(2, 4), z(4), z(2, 4, 8)
+    wide = z(2, 4, 16)[:, :, :8]
+    bad = [
+        lambda: _ops.moe_grouped_gemm(grp, x, wide.to(bf).new_zeros(2, 4, 16)[:, :, :8], off, dy),
+        lambda: _ops.moe_grouped_gemm_dgrad(grp, dy, w.new_zeros(2, 4, 16)[:, :, :8], off, x),
+        lambda: _ops.moe_grouped_gemm_wgrad(grp, dy, x, off, wide),
+        lambda: _ops.moe_grouped_gemm(grp, x, w, z(6, dtype=torch.int32)[::2], dy),
+        lambda: _ops.moe_orthogonalize(orth, wide, None, None, mat.to(bf), None),
+        lambda: _ops.moe_orthogonalize(orth, mat, wide, mat, mat.to(bf), None),
+        lambda: _ops.moe_orthogonalize(orth, mat, mat, wide, mat.to(bf), None),
+        lambda: _ops.moe_orthogonalize(orth, mat, None, None, w.new_zeros(2, 4, 16)[:, :, :8], None),
+        lambda: _ops.moe_layernorm_forward(norm, z(4, 2).t(), None, vec, vec, rows, None, vec, vec),
+        lambda: _ops.moe_layernorm_forward(norm, rows, None, z(8)[::2], vec, rows, None, vec, vec),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    three = z(2, 3, 16)[..., 4:12]  # six rows, 16 values apart
+    assert _ops._rows(z(6, 16)[:, 4:12]) and _ops._rows(three) == three.data_ptr()
+    with pytest.raises(ValueError, match="contiguous"):
+        _ops._rows(z(2, 4, 16)[:, :3, 4:12])  # a gap after every third row
