@@ -79,8 +79,9 @@ def _p(t) -> int | None:
 def _rows(t) -> int | None:
     """Device pointer of a row matrix. Its rows may be strided, as the
     descriptor says, and counted by several leading dimensions."""
-    if isinstance(t, torch.Tensor) and t.dim() > 1 and t.stride(-1) == 1 and all(
-            t.stride(i) == t.stride(i + 1) * t.size(i + 1) for i in range(t.dim() - 2)):
+    if isinstance(t, torch.Tensor) and t.dim() > 1 and 1 in (t.stride(-1), t.size(-1)) and all(
+            t.size(i) == 1 or t.stride(i) == t.stride(i + 1) * t.size(i + 1)
+            for i in range(t.dim() - 2)):
         return t.data_ptr()
     return _p(t)
 

@@ -31,3 +31,15 @@ def test_rows_past_one_launch(n, d):
     x[some] = b.bfloat16()
     for i in range(0, n, 1 << 24):
         assert bool((x[i:i + (1 << 24)] == b.bfloat16()).all())
+
+
+def test_rows_of_one_value_far_apart():
+    """An [n, 1] view has a row stride only; its mean is the value itself."""
+    import sparse_mixture_experts_gate_amd as M
+    buf = torch.randn(2, 300, device="cuda:0")
+    x, buf = buf.t()[::3, :1], buf[0]
+    b = torch.full((1,), 2.5, device="cuda:0")
+    f = M.LayerNorm(None, b).forward(x)
+    assert torch.equal(f["mean"], buf[::3]) and bool((f["y"] == 2.5).all())
+    dx = M.LayerNorm(None, b).backward(x, x, f["mean"], f["rstd"], x)["dx"]
+    assert torch.equal(dx, x)

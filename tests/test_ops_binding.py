@@ -77,3 +77,11 @@ def test_only_row_matrices_may_be_strided():
     assert _ops._rows(z(6, 16)[:, 4:12]) and _ops._rows(three) == three.data_ptr()
     with pytest.raises(ValueError, match="contiguous"):
         _ops._rows(z(2, 4, 16)[:, :3, 4:12])  # a gap after every third row
+
+
+def test_columns_of_one_value_have_no_stride():
+    """[n, 1] row matrices: only the row stride means anything."""
+    t = torch.zeros(2, 12).t()[::3, :1]
+    assert t.shape == (4, 1) and t.stride() == (3, 12)
+    assert blocks._rows(t, "x", torch.float32, 4, 1) == 3
+    assert _ops._rows(t) == t.data_ptr()
