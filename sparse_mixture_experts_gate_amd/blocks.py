@@ -44,6 +44,20 @@ def _vector(t, name: str, dtype: torch.dtype, n: int) -> None:
                          f"{list(t.shape)}")
 
 
+def _on_gpu(stream, *tensors) -> None:
+    """Refuse tensors (None: not given) that are not on the GPU the call runs
+    on: a kernel that reads a host address or another GPU's faults."""
+    at = -2
+    for t in tensors:
+        if t is not None:
+            dev = t.get_device()
+            if dev < 0 or (at >= 0 and dev != at):
+                raise ValueError("expected all tensors on one GPU")
+            at = dev
+    if at >= 0 and at != (torch._C._cuda_getDevice() if stream is None else stream.device_index):
+        raise ValueError(f"expected tensors on the GPU of the stream, got them on GPU {at}")
+
+
 class _Workspace:
     """One buffer per stream and host thread, grown as calls need it. Two
     threads that use one stream have a buffer each: a call's kernels meet in
@@ -102,6 +116,7 @@ class LayerNorm:
         n, d = x.shape
         if residual is not None:
             desc.ld_r = _rows(residual, "residual", x.dtype, n, d)
+        _on_gpu(stream, x, residual, self.weight, self.bias)
         with _on(stream):
             y = x.new_empty(n, d)
             total = x.new_empty(n, d) if residual is not None else None
@@ -122,6 +137,7 @@ class LayerNorm:
             desc.ld_r = _rows(dresidual, "dresidual", x.dtype, n, d)
         _vector(mean, "mean", torch.float32, n)
         _vector(rstd, "rstd", torch.float32, n)
+        _on_gpu(stream, dy, x, self.weight, mean, rstd, dresidual)
         with _on(stream):
             dx = torch.empty(n, d, dtype=x.dtype, device=x.device)
             dw = torch.empty(d, dtype=torch.float32, device=x.device)
@@ -166,6 +182,7 @@ class GroupedLinear:
         G, n, k = self.weight.shape
         desc = self._desc(x.shape[0], G, n, k, offsets, out_dtype)
         desc.ld_k = _rows(x, "x", torch.bfloat16, x.shape[0], k)
+        _on_gpu(stream, x, self.weight, offsets)
         with _on(stream):
             y = torch.empty(x.shape[0], n, dtype=out_dtype, device=x.device)
             ws = self._workspace(desc, O.MOE_GROUPED_FORWARD, x.device, stream)
@@ -178,6 +195,7 @@ class GroupedLinear:
         G, n, k = self.weight.shape
         desc = self._desc(dy.shape[0], G, n, k, offsets, out_dtype)
         desc.ld_n = _rows(dy, "dy", torch.bfloat16, dy.shape[0], n)
+        _on_gpu(stream, dy, self.weight, offsets)
         with _on(stream):
             dx = torch.empty(dy.shape[0], k, dtype=out_dtype, device=dy.device)
             ws = self._workspace(desc, O.MOE_GROUPED_DGRAD, dy.device, stream)
@@ -199,6 +217,7 @@ class GroupedLinear:
                                  or not into.is_contiguous()):
             raise ValueError(f"into: expected contiguous fp32 [{G}, {n}, {k}], got {into.dtype} "
                              f"{list(into.shape)}")
+        _on_gpu(stream, dy, x, offsets, into)
         with _on(stream):
             if into is None:
                 into = torch.empty(G, n, k, dtype=torch.float32, device=dy.device)
@@ -235,6 +254,7 @@ class Muon:
                              cols=cols, grad_dtype=_DT[grad.dtype], steps=self.steps,
                              momentum=self.momentum, nesterov=int(self.nesterov))
         need = O.moe_orthogonalize_workspace_size(desc)
+        _on_gpu(stream, grad, momentum, out_momentum)
         with _on(stream):
             out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
             if momentum is not None and out_momentum is None:

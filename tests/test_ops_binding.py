@@ -85,3 +85,35 @@ def test_columns_of_one_value_have_no_stride():
     assert t.shape == (4, 1) and t.stride() == (3, 12)
     assert blocks._rows(t, "x", torch.float32, 4, 1) == 3
     assert _ops._rows(t) == t.data_ptr()
+
+
+def test_tensors_of_the_host_are_refused():
+    """Every tensor that a kernel would read, by itself on the host."""
+    import sparse_mixture_experts_gate_amd as M
+
+    class OnGpu(torch.Tensor):
+        """A host tensor that says it is on the current GPU."""
+        get_device = lambda self: 0
+
+    def gpu(t):
+        return t.as_subclass(OnGpu)
+
+    bf, f32, z = torch.bfloat16, torch.float32, torch.zeros
+    off = z(3, dtype=torch.int32)
+    calls = {
+        "norm": (lambda w, b, x, r: M.LayerNorm(w, b).forward(x, r),
+                 [z(8), z(8), z(2, 8), z(2, 8)]),
+        "norm backward": (lambda w, dy, x, m, s, r: M.LayerNorm(w).backward(dy, x, m, s, r),
+                          [z(8), z(2, 8), z(2, 8), z(2), z(2), z(2, 8)]),
+        "forward": (lambda w, x, o: M.GroupedLinear(w).forward(x, o),
+                    [z(2, 4, 8, dtype=bf), z(5, 8, dtype=bf), off]),
+        "input gradient": (lambda w, dy, o: M.GroupedLinear(w).input_grad(dy, o),
+                           [z(2, 4, 8, dtype=bf), z(5, 4, dtype=bf), off]),
+        "weight gradient": (M.GroupedLinear.weight_grad,
+                            [z(5, 4, dtype=bf), z(5, 8, dtype=bf), off, z(2, 4, 8)]),
+        "update": (M.Muon().direction, [z(2, 4, 8), z(2, 4, 8), z(2, 4, 8)]),
+    }
+    for name, (call, args) in calls.items():
+        for i in range(len(args)):
+            with pytest.raises(ValueError, match="GPU"):
+                call(*(t if j == i else gpu(t) for j, t in enumerate(args)))
