@@ -44,6 +44,13 @@ def _vector(t, name: str, dtype: torch.dtype, n: int) -> None:
                          f"{list(t.shape)}")
 
 
+def _aligned(t):
+    """t, or a copy of it where it does not start on 16 bytes as the library
+    asks of vectors (a view of a flat parameter buffer, a slice of the rows'
+    statistics)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _on_gpu(stream, *tensors) -> None:
     """Refuse tensors (None: not given) that are not on the GPU the call runs
     on: a kernel that reads a host address or another GPU's faults."""
@@ -122,8 +129,8 @@ class LayerNorm:
             total = x.new_empty(n, d) if residual is not None else None
             mean = x.new_empty(n, dtype=torch.float32)
             rstd = x.new_empty(n, dtype=torch.float32)
-        O.moe_layernorm_forward(desc, x, residual, self.weight, self.bias, y, total, mean, rstd,
-                                stream)
+            weight, bias = _aligned(self.weight), _aligned(self.bias)
+        O.moe_layernorm_forward(desc, x, residual, weight, bias, y, total, mean, rstd, stream)
         return {"y": y, "mean": mean, "rstd": rstd, "sum": x if residual is None else total}
 
     def backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -144,8 +151,8 @@ class LayerNorm:
             db = torch.empty_like(dw)
             need = O.moe_layernorm_backward_workspace_size(desc)
             ws = self._ws.get(need, x.device, stream) if need else None
-        O.moe_layernorm_backward(desc, dy, x, self.weight, mean, rstd, dresidual, dx, dw, db, ws,
-                                 stream)
+            weight, mean, rstd = _aligned(self.weight), _aligned(mean), _aligned(rstd)
+        O.moe_layernorm_backward(desc, dy, x, weight, mean, rstd, dresidual, dx, dw, db, ws, stream)
         return {"dx": dx, "dweight": dw, "dbias": db}
 
 

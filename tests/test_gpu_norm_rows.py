@@ -43,3 +43,30 @@ def test_rows_of_one_value_far_apart():
     assert torch.equal(f["mean"], buf[::3]) and bool((f["y"] == 2.5).all())
     dx = M.LayerNorm(None, b).backward(x, x, f["mean"], f["rstd"], x)["dx"]
     assert torch.equal(dx, x)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_vectors_at_any_element(shift):
+    """Weights that are views of one flat parameter buffer, statistics of a
+    slice of the rows: bit for bit the same as aligned ones."""
+    import sparse_mixture_experts_gate_amd as M
+    n, d = 9, 200
+    x, dy = torch.randn(n, d, device="cuda:0"), torch.randn(n, d, device="cuda:0")
+    flat = torch.randn(2 * d + shift, device="cuda:0")
+    w, b = flat[shift:shift + d], flat[shift + d:]
+    f = M.LayerNorm(w, b).forward(x)
+    want = M.LayerNorm(w.clone(), b.clone()).forward(x)
+    assert torch.equal(f["y"], want["y"])
+    norm = M.LayerNorm(w, b)
+    got = norm.backward(dy[shift:], x[shift:], f["mean"][shift:], f["rstd"][shift:])
+    ref = M.LayerNorm(w.clone()).backward(dy[shift:], x[shift:], f["mean"][shift:].clone(),
+                                          f["rstd"][shift:].clone())
+    for k in ref:
+        assert torch.equal(got[k], ref[k])
+    s = torch.cuda.Stream()  # an aligned copy is made on the stream of the call
+    s.wait_stream(torch.cuda.current_stream())
+    w.mul_(2)
+    s.wait_stream(torch.cuda.current_stream())
+    y = norm.forward(x, stream=s)["y"]
+    s.synchronize()
+    assert torch.equal(y, norm.forward(x)["y"]) and not torch.equal(y, f["y"])
