@@ -417,15 +417,20 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
   const int tiles =
       (MODE == kWgrad ? a.G * ((a.n + C::BM - 1) / C::BM) * tn : gt.total) * a.splits;
   Tail tail{tiles, 1, a.tail_part, a.tail_count};
+  int nb = gridDim.x;
   if (a.tail_part) {
-    const int whole = tiles / gridDim.x * gridDim.x;
+    // all resident workgroups are launched, as the choice of this kernel assumed;
+    // those without a unit end here, and the others are spread over the XCDs
+    const int whole = tiles / nb * nb;
     const int nk = ((MODE == kForward ? a.k : a.n) + BK - 1) / BK;
-    tail.splits = tail_splits(tiles - whole, nk, gridDim.x, kBigStep * C::BM / 256,
-                              C::BM * C::BN / 256);
+    tail.splits =
+        tail_splits(tiles - whole, nk, nb, kBigStep * C::BM / 256, C::BM * C::BN / 256);
     if (tail.splits > 1) tail.whole = whole;
+    nb = min(nb, (tail.whole + (tiles - tail.whole) * tail.splits + 7) / 8 * 8);
+    if (static_cast<int>(blockIdx.x) >= nb) return;
   }
   const int total = tail.whole + (tiles - tail.whole) * tail.splits;
-  const int first = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int first = xcd_logical_block(blockIdx.x, nb);
   if (first >= total) return;
   auto locate = [&](int unit) {
     const Unit u = unit_of(tail, unit);
@@ -497,9 +502,9 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
     }
   } ep{a, tail, &flag, locate, range};
   if constexpr (PHASED)
-    stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
+    stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, nb, total, next_ops, ep);
   else
-    stream_ring<C, TypeBf16, AKM, BKM, SWAP>(lds, first, gridDim.x, total, next_ops, ep);
+    stream_ring<C, TypeBf16, AKM, BKM, SWAP>(lds, first, nb, total, next_ops, ep);
 }
 
 // Workgroups of a persistent launch of kernel K: the resident ones, or no more
@@ -627,6 +632,7 @@ constexpr TileCost kCosts[] = {
 //   x [8192, 7168], 32 x 4096               256^2: 610, 128^2: 717
 //   x [5000, 2048], 8 x 2048                192 x 256: 48, 128^2: 53
 //   x [3000, 4096], 1 x 4096                192 x 256: 88, 256^2: 97
+//   x [1536, 7168], 1 x 1408                192 x 256, tiles shared: 73, whole: 110
 //   x [30000, 2048], 100 x 1408             256^2: 250, 192 x 256: 274
 //   x [8192, 4095], 8 x 2048                128 x 256: 297, 128^2: 326 (any alignment)
 //   x [2311, 613], 9 x 1407                 128^2: 25, 128 x 256: 31 (any alignment)
@@ -695,10 +701,11 @@ Choice choose(const GroupedArgs& p, bool aligned) {
 
 template <class C, int MODE, bool PHASED>
 void launch_fast(const GArgs& a, hipStream_t s) {
+  // shared tiles: every workgroup that its workspace has room for
+  const int64_t units = a.tail_part ? kTailSlots : tile_bound<MODE, C>(a) * a.splits;
   hipLaunchKernelGGL((grouped_kernel<C, MODE, PHASED>),
-                     dim3(grid_of<grouped_kernel<C, MODE, PHASED>>(
-                         C::NT, tile_bound<MODE, C>(a) * a.splits)),
-                     dim3(C::NT), 0, s, a);
+                     dim3(grid_of<grouped_kernel<C, MODE, PHASED>>(C::NT, units)), dim3(C::NT), 0, s,
+                     a);
 }
 
 template <class C, int MODE>
