@@ -9,6 +9,7 @@
 #include "device_common.h"
 #include "gemm16_core.h"
 #include "internal.h"
+#include "resident_grid.h"
 #include "tile_schedule.h"
 
 namespace dsmoe {
@@ -505,21 +506,6 @@ __global__ __launch_bounds__(C::NT, C::MINW) void grouped_kernel(GArgs a) {
     stream_phased<C, TypeBf16, AKM, BKM, SWAP>(lds, first, nb, total, next_ops, ep);
   else
     stream_ring<C, TypeBf16, AKM, BKM, SWAP>(lds, first, nb, total, next_ops, ep);
-}
-
-// Workgroups of a persistent launch of kernel K: the resident ones, or no more
-// than the tiles there can be (whole XCD rounds).
-template <auto K>
-unsigned grid_of(int threads, int64_t tiles) {
-  static int res = 0;
-  if (!res) {
-    int nb = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, K, threads, 0) != hipSuccess || nb < 1)
-      nb = 1;
-    res = (device_cu_count() * nb + 7) / 8 * 8;
-  }
-  const int64_t t = (tiles + 7) / 8 * 8;
-  return static_cast<unsigned>(t < res ? (t < 8 ? 8 : t) : res);
 }
 
 // Sums of the splits' partial outputs, in split order, eight columns of a row

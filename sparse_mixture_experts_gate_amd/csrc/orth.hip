@@ -27,6 +27,7 @@
 #include "device_common.h"
 #include "gemm16_core.h"
 #include "internal.h"
+#include "resident_grid.h"
 
 namespace dsmoe {
 
@@ -863,19 +864,6 @@ void small(const SmallArgs& a, bool tall, int64_t mats, hipStream_t s) {
 }
 
 // ---- launches ------------------------------------------------------------------------
-
-template <auto K>
-unsigned grid_of(int threads, int64_t tiles) {
-  static int res = 0;
-  if (!res) {
-    int nb = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, K, threads, 0) != hipSuccess || nb < 1)
-      nb = 1;
-    res = (device_cu_count() * nb + 7) / 8 * 8;
-  }
-  const int64_t t = (tiles + 7) / 8 * 8;
-  return static_cast<unsigned>(t < res ? t : res);
-}
 
 using TileBig = Tile<256, 256, 128, 64, 2>;  // 8 waves, two-phase loop
 using TileMid = Tile<128, 128, 64, 32, 3>;   // 8 waves, ring

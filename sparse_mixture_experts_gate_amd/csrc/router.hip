@@ -12,6 +12,7 @@
 
 #include "device_common.h"
 #include "internal.h"
+#include "per_device.h"
 #include "route_token.h"
 #include "sigmoid_ieee.h"
 
@@ -305,16 +306,15 @@ hipError_t launch_route(const float* partial, int splits, float* logits_out, con
 }
 
 int device_cu_count() {
-  static int cached[64] = {0};
+  static PerDevice cus;
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  return cus.get(dev, [&] {
     int n = 0;
     if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
       n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
+    return n;
+  });
 }
 
 }  // namespace dsmoe
