@@ -79,18 +79,27 @@ def _p(t) -> int | None:
 def _rows(t) -> int | None:
     """Device pointer of a row matrix. Its rows may be strided, as the
     descriptor says, and counted by several leading dimensions."""
-    if isinstance(t, torch.Tensor) and t.dim() > 1 and 1 in (t.stride(-1), t.size(-1)) and all(
-            t.size(i) == 1 or t.stride(i) == t.stride(i + 1) * t.size(i + 1)
-            for i in range(t.dim() - 2)):
-        return t.data_ptr()
-    return _p(t)
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor or None")
+    if not t.is_contiguous() and not _one_row_stride(t.shape, t.stride()):
+        raise ValueError("row matrices passed to the library must have contiguous columns and "
+                         "one row stride")
+    return t.data_ptr()
+
+
+def _one_row_stride(shape, stride) -> bool:
+    return (len(shape) > 1 and 1 in (shape[-1], stride[-1]) and
+            all(shape[i] == 1 or stride[i] == stride[i + 1] * shape[i + 1]
+                for i in range(len(shape) - 2)))
 
 
 def _stream(stream) -> int:
     """Handle of a torch stream, or of the current one."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _nbytes(t) -> int:

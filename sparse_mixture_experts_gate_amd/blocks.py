@@ -48,21 +48,18 @@ def _aligned(t):
     """t, or a copy of it where it does not start on 16 bytes as the library
     asks of vectors (a view of a flat parameter buffer, a slice of the rows'
     statistics)."""
-    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+    return t if t is None or not t.data_ptr() & 15 else t.clone()
 
 
-def _on_gpu(stream, *tensors) -> None:
+def _on_gpu(stream, first, *others) -> None:
     """Refuse tensors (None: not given) that are not on the GPU the call runs
     on: a kernel that reads a host address or another GPU's faults."""
-    at = -2
-    for t in tensors:
-        if t is not None:
-            dev = t.get_device()
-            if dev < 0 or (at >= 0 and dev != at):
-                raise ValueError("expected all tensors on one GPU")
-            at = dev
-    if at >= 0 and at != (torch._C._cuda_getDevice() if stream is None else stream.device_index):
-        raise ValueError(f"expected tensors on the GPU of the stream, got them on GPU {at}")
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("expected all tensors on one GPU")
+    if at < 0 or at != (torch._C._cuda_getDevice() if stream is None else stream.device_index):
+        raise ValueError("expected tensors on the GPU of the call's stream")
 
 
 class _Workspace:
@@ -78,9 +75,11 @@ class _Workspace:
     @property
     def _bufs(self) -> dict:
         """The calling thread's buffers."""
-        if not hasattr(self._local, "bufs"):
+        try:
+            return self._local.bufs
+        except AttributeError:
             self._local.bufs = {}
-        return self._local.bufs
+            return self._local.bufs
 
     def get(self, need: int, device, stream) -> torch.Tensor:
         """A buffer of at least `need` bytes; called with `stream` current."""
@@ -110,9 +109,10 @@ class LayerNorm:
         if x.dim() != 2 or x.dtype not in _DT:
             raise ValueError(f"x: expected bf16 or fp32 [n, d], got {x.dtype} {list(x.shape)}")
         n, d = x.shape
-        if self.dims - {d}:
-            raise ValueError(f"x: rows of {d} values, weight and bias have {sorted(self.dims)}")
-        return O.MoeNormDesc(n, d, _DT[x.dtype], self.eps, _rows(x, "x", x.dtype, n, d), 0, 0, 0)
+        for v in self.dims:
+            if v != d:
+                raise ValueError(f"x: rows of {d} values, weight and bias have {sorted(self.dims)}")
+        return O.MoeNormDesc(n, d, _DT[x.dtype], self.eps, _rows(x, "x", x.dtype, n, d))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 stream=None) -> dict:
