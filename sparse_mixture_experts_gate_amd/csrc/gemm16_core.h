@@ -403,8 +403,8 @@ __device__ __forceinline__ void stream_ring(uint16_t* lds, int first, int nb, in
 // work in every phase. Two stages of 64 KB: the loads of step k + 1 go out in
 // the first two memory phases of step k, or the first three where B's
 // transposing reads make these longer (12288 rows, 4096 x 7168, input gradient:
-// 599 us with two, 580 with three; forward: 553 and 568), and are waited for in
-// its last.
+// 654 us with two, 647 with three; 24576 rows over 64 groups of 2816 x 2048: 413
+// and 397; forward of the first: 579 and 586), and are waited for in its last.
 //
 // Rows of a tile past its data are multiplied all the same: leaving out waves
 // whose part of the tile is empty took as long (the loads set the pace there),

@@ -243,7 +243,10 @@ using TileAnyBig = Tile<128, 256, 64, 64, 2>;  // a quarter fewer loaded bytes p
 // (unaligned 16-byte loads, element loads at the ends) into the same LDS
 // layouts, loaded two k-steps ahead of the MFMAs and stored to LDS one ahead.
 // (The weight gradient's small tile fits 128 registers, two workgroups per CU:
-// 8192 rows, 2047 x 4095: 297 us, 384 with one. The others would spill.)
+// 8192 rows, 2047 x 4095: 305 us, 384 with one. The others would spill.)
+// Bound by the way through registers: with one workgroup per CU loads, stores to
+// LDS and matrix instructions take turns, 295 us for x [8192, 4095], 8 x 2048,
+// 3.5 times what the operations need at a library product's rate.
 template <class C, int MODE>
 __global__ __launch_bounds__(C::NT, MODE == kWgrad && C::BN == 128 ? 4 : 2) void
 grouped_any_kernel(GArgs a) {
@@ -399,10 +402,10 @@ grouped_any_kernel(GArgs a) {
 // What bounds it, measured: 32 x 128 tiles the stream of weights (128 rows over
 // 256 experts of 4096 x 7168: 858 us, 6.9 TB/s); 256 x 256 tiles the matrix
 // cores and, per tile, the rows that pad a group to whole tiles and an output
-// of 6 us that nothing overlaps (12288 rows, one group of 4096 x 7168: 1.29
-// PFLOP/s; 24576 rows over 64 groups of 2816 x 2048: 0.81, 42% more rows
+// of 6 us that nothing overlaps (12288 rows, one group of 4096 x 7168: 1.27
+// PFLOP/s; 24576 rows over 64 groups of 2816 x 2048: 0.72, 42% more rows
 // multiplied than there are); the weight gradient its fp32 stores, 12 us a tile
-// (8192 rows over 32 groups of 7168 x 2048: 537 us, 1.88 GB). Issuing the next
+// (8192 rows over 32 groups of 7168 x 2048: 541 us, 1.88 GB). Issuing the next
 // tile's loads ahead of those stores gained 3% there and cost up to 9% where
 // groups are short; two workgroups per CU of 128 x 128 tiles took 710 us.
 template <class C, int MODE, bool PHASED>
@@ -612,19 +615,22 @@ constexpr TileCost kCosts[] = {
 // Row counts per group live on the device, so the expected number of row tiles
 // stands in for them: one per group while groups are smaller than a tile, else
 // rows / BM and half a tile per group. What it decides, as measured (us):
-//   x [128, 7168], 256 experts x 4096       32 x 128: 864, 128^2: 998, 256^2: 1258
-//   x [1000, 2048], 8 x 1408                128^2: 21, 32 x 128: 32, 256^2: 43
-//   x [2048, 7168], 32 x 4096               128^2: 335, 256^2: 399, 32 x 128: 563
-//   x [8192, 7168], 32 x 4096               256^2: 610, 128^2: 717
-//   x [5000, 2048], 8 x 2048                192 x 256: 48, 128^2: 53
-//   x [3000, 4096], 1 x 4096                192 x 256: 88, 256^2: 97
-//   x [1536, 7168], 1 x 1408                192 x 256, tiles shared: 73, whole: 110
-//   x [30000, 2048], 100 x 1408             256^2: 250, 192 x 256: 274
-//   x [8192, 4095], 8 x 2048                128 x 256: 297, 128^2: 326 (any alignment)
-//   x [2311, 613], 9 x 1407                 128^2: 25, 128 x 256: 31 (any alignment)
+//   x [128, 7168], 256 experts x 4096       32 x 128: 867, 128^2: 1004, 256^2: 1255
+//   x [1000, 2048], 8 x 1408                128^2: 22, 32 x 128: 33, 256^2: 44
+//   x [2048, 7168], 32 x 4096               128^2: 343, 256^2: 408, 32 x 128: 567
+//   x [8192, 7168], 32 x 4096, Zipf loads   256^2: 621, 192 x 256: 671, 128^2: 729
+//   x [5000, 2048], 8 x 2048                192 x 256: 51, 256^2: 59, 128^2: 68
+//   x [3000, 4096], 1 x 4096                192 x 256: 101, 256^2: 102
+//   x [30000, 2048], 100 x 1408, Zipf       256^2: 256, 192 x 256: 304
+//   x [8192, 4095], 8 x 2048                128 x 256: 295, 128^2: 335 (any alignment)
+//   x [2311, 613], 9 x 1407                 128^2: 26, 64 x 128: 31, 128 x 256: 32 (any)
 //   dx of [2311, 1407], 9 x 613             64 x 128: 24, 128^2: 30 (any alignment)
-//   dw of 8000 rows, 2 x 256 x 256          4 splits: 26, 1: 53 (128^2), 129 (256^2)
-//   x [8, 4096], 1 x 2048                   4 splits: 22, 1: 26 (32 x 128)
+//   dw of 8000 rows, 2 x 256 x 256          4 splits: 24, 1: 42 (128^2), 99 (256^2)
+//   x [8, 4096], 1 x 2048                   4 splits: 18, 1: 26 (32 x 128)
+// and where it is wrong, the tile it takes first:
+//   x [1536, 7168], 1 x 1408                192 x 256, shared: 73, whole: 110; 128^2: 57
+//   x [30000, 2048], 100 x 1408, even loads 256^2: 288, 192 x 256: 273
+//   dx of [24576, 2816], 64 x 2048, Zipf    256^2: 397, 192 x 256: 373
 // Splits add the finishing launch and the partial sums' traffic, so they pay
 // only where few tiles leave most of the GPU idle for many k-steps.
 Choice choose(const GroupedArgs& p, bool aligned) {

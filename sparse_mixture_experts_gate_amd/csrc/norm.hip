@@ -5,6 +5,12 @@
 // once. A row lives in the registers of NW waves (1, 4 or 8 by its length), 8
 // adjacent values per lane and chunk. Rows longer than kMaxRow are read again
 // from memory for every pass instead.
+//
+// The backward of rows past 8192 values holds two rows, the weight and two
+// column sums at 32 values a lane each, which 256 registers do not take: up to
+// 296 bytes a lane go to scratch memory (fp32 with dresidual; 36 without, bf16
+// with it 56). 2048 x 16384: bf16 48 us, with dresidual 74; fp32 104 and 191,
+// 0.4 to 0.9 of a large copy's rate.
 #include "device_common.h"
 #include "internal.h"
 

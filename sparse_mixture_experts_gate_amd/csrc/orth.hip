@@ -15,8 +15,14 @@
 //        A A = R R + D R + R D + D D, of which only R R is a product;
 //   B  = b A + c A A = Q + S the same way: X <- (a + Q) X + S X.
 // Near convergence D and Q dominate their matrices, so their fp16 roundings
-// would be most of the error: on random matrices the result is 6e-4 off (2-norm)
-// this way, 1.7e-3 with the diagonals inside, 1.1e-2 in bf16 throughout.
+// would be most of the error: on random matrices of 512 x 1024 the result is
+// 6e-4 off (2-norm) this way, 1.7e-3 with the diagonals inside, 1.1e-2 in bf16
+// throughout. Roundings average over a row: 4e-4 at 2048 x 7168, 1.2e-3 at 64 x
+// 64, 1.4e-3 at 16 x 16, and with 1 to 8 rows of few values 1.5e-3 to 3.6e-3 (9e-3
+// at worst seen). The polynomial repels at its fixed point (slope -1.58 at
+// 0.868), so further steps grow what is there: 2e-3 after eight from 64 x 64 on.
+// A null space grows too: rank 1 of 2040 x 3000 is 4e-3 off after eight steps,
+// 4e-2 after ten, all of it after 14; in fp32 throughout 1e-2, 1e-1, all.
 // Only the last two steps multiply all of X by Q. Before them Q multiplies hi
 // alone, as S does: Q + S = B has the null space of X, and applied to two
 // different roundings of X its parts would leave noise there that later steps
@@ -259,8 +265,8 @@ __global__ __launch_bounds__(256) void orth_scale_kernel(PrepArgs a) {
 
 // ---- the three products of a step ------------------------------------------------
 //
-// 16 matrices of 2048 x 7168: R 505 us (0.54 TFLOP of lower tiles, 1.07
-// PFLOP/s), S 213 us, X 1110 us (0.96 TFLOP, 0.87 PFLOP/s), the last X 1006 us.
+// 16 matrices of 2048 x 7168: R 528 us (0.54 TFLOP of lower tiles, 1.02
+// PFLOP/s), S 217 us, X 1133 us (0.96 TFLOP, 0.85 PFLOP/s), the last X 1036 us.
 // The matrix cores bound the loops; X's output adds to them, as it reads and
 // writes both planes (256 KB each way per tile of 256 x 256, 16 us at the rates
 // of one CU) and a CU has no second workgroup to multiply meanwhile.
@@ -535,8 +541,10 @@ __global__ __launch_bounds__(C::NT, C::MINW) void orth_product_kernel(StepArgs a
 // One workgroup per matrix of up to 128 x 256, all steps in one launch: X stays
 // in fp32 registers (the master) and as fp16 in LDS (the operand), the n x n
 // matrices share one LDS buffer. Launch-bound otherwise: 17 launches a call
-// took 233 us for 32 matrices of 128 x 256, this kernel 37: 15 dependent
-// products of one workgroup, each bound by its LDS reads and barriers.
+// took 233 us for 32 matrices of 128 x 256, this kernel 40: 15 dependent
+// products of one workgroup, each bound by its LDS reads and barriers. (The
+// tall form without momentum has 36 bytes a lane in scratch memory: 39 us for
+// the same matrices transposed.)
 //
 // X [128][256] serves row reads (16-byte fragments of 16 rows at a time, for X
 // X^T) and transpose reads (4 rows of 32 bytes, for S X), so its 16-byte chunks
@@ -578,7 +586,7 @@ __global__ __launch_bounds__(512, 2) void orth_small_kernel(SmallArgs a) {
   // before the first use: addresses past the matrix are clamped into it and
   // their values dropped, so no load hides behind a branch. (With one branch
   // per element the loads ran one after the other: 71 us for a call of 32
-  // matrices of 128 x 256 that takes 37.)
+  // matrices of 128 x 256 that takes 40.)
   f32x16_t x[2][2];
   const bool runs = !TALL && a.m % 4 == 0;  // whole runs of four, aligned
   auto at = [&](int mi, int nj, int e) {
