@@ -33,7 +33,9 @@ NO_CONTRACT = {"router.hip", "elementwise.hip", "balance.hip", "backward_fp8.hip
 MFMA_VGPR = {"gemm_fp8.hip", "backward_fp8.hip"}
 SOURCES = ["dsmoe_api.cpp", "router.hip", "permute.hip", "gemm_bf16.hip", "gemm_f32.hip",
            "gemm_fp8.hip", "elementwise.hip", "backward.hip", "balance.hip", "backward_fp8.hip",
-           "ops_api.cpp", "norm.hip", "grouped.hip", "orth.hip"]
+           "ops_api.cpp", "norm.hip", "grouped.hip", "orth.hip",
+           "tokens_api.cpp", "rmsnorm.hip", "dispatch.hip", "combine.hip", "mx4.hip",
+           "mx4_gemm.hip"]
 
 
 def _compile(src: str) -> str:

@@ -1,0 +1,199 @@
+// Sorted rows back to their tokens with weights, and the gradients of that
+// (definitions in dsmoe_tokens.h).
+//
+// Memory-bound: a group of LANES lanes owns a token, 8 adjacent values per lane
+// and chunk; its places and weights are wave-uniform, and the rows of up to eight
+// places are in flight together.
+#include "device_common.h"
+#include "internal.h"
+#include "row_io.h"
+
+namespace dsmoe {
+
+namespace {
+
+constexpr int kMaxK = 64;
+
+struct TokArgs {
+  const void* yp;
+  const int32_t* inv;
+  const float* w;
+  const void* base;  // forward: base; backward: dy
+  void* y;           // forward: y; backward: dy_perm
+  float* dw;
+  int64_t t0, T, rows, ldt, ldp;
+  int K, d;
+  bool stream;
+};
+
+// A token's places: lane k holds slot k's place and weight, `mask` the slots that
+// have one.
+struct Places {
+  int32_t at;
+  float w;
+  uint64_t mask;
+};
+__device__ __forceinline__ Places places_of(const TokArgs& a, int64_t t, int lane) {
+  Places p{-1, 0.0f, 0};
+  if (lane < a.K) {
+    p.at = a.inv[t * a.K + lane];
+    p.w = a.w ? a.w[t * a.K + lane] : 1.0f;
+  }
+  p.mask = __ballot(p.at >= 0 && p.at < a.rows);
+  return p;
+}
+__device__ __forceinline__ int next_slot(uint64_t& m) {
+  const int k = __builtin_ctzll(m);
+  m &= m - 1;
+  return k;
+}
+
+// acc += w row over the next N slots, all loads first.
+template <class T, int N>
+__device__ __forceinline__ void add_rows(const TokArgs& a, const Places& p, uint64_t& m, int i0,
+                                         float (&acc)[VEC]) {
+  typename RawOf<T>::type r[N];
+  float w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int k = next_slot(m);
+    const int64_t at = __builtin_amdgcn_readlane(p.at, k);
+    w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k));
+    r[i] = load8(static_cast<const T*>(a.yp) + at * a.ldp + i0, a.d - i0);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float v[VEC];
+    unpack(r[i], v);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] = __builtin_fmaf(w[i], v[j], acc[j]);
+  }
+}
+
+template <class T, int LANES>
+__global__ __launch_bounds__(256) void token_combine_kernel(TokArgs a) {
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t t = a.t0 + int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  if (t >= a.T) return;  // whole waves
+  const Places p = places_of(a, t, threadIdx.x & 63);
+  for (int i0 = lane * VEC; i0 < a.d; i0 += LANES * VEC) {
+    float acc[VEC] = {};
+    if (a.base) unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), acc);
+    uint64_t m = p.mask;
+    int left = __popcll(m);
+    for (; left >= 8; left -= 8) add_rows<T, 8>(a, p, m, i0, acc);
+    if (left & 4) add_rows<T, 4>(a, p, m, i0, acc);
+    if (left & 2) add_rows<T, 2>(a, p, m, i0, acc);
+    if (left & 1) add_rows<T, 1>(a, p, m, i0, acc);
+    store8(static_cast<T*>(a.y) + t * a.ldt + i0, acc, a.d - i0, a.stream);
+  }
+}
+
+// dy's row stays in registers, CH chunks per lane; longer rows take several
+// sweeps over the places. Partial sums of <dy, row> are kept per wave and slot in
+// LDS and added in wave order.
+template <class T, int LANES, int CH>
+__global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
+  constexpr int GROUPS = 256 / LANES, WAVES = LANES / 64;
+  __shared__ float part[GROUPS][WAVES][kMaxK];
+  const int lane = threadIdx.x & (LANES - 1), group = threadIdx.x / LANES;
+  const int wave = lane >> 6;
+  const int64_t t = a.t0 + int64_t(blockIdx.x) * GROUPS + group;
+  const bool real = t < a.T;
+  Places p{-1, 0.0f, 0};
+  if (real) {
+    p = places_of(a, t, threadIdx.x & 63);
+    if ((threadIdx.x & 63) < a.K) part[group][wave][threadIdx.x & 63] = 0.0f;
+    for (int s0 = 0; s0 < a.d; s0 += LANES * VEC * CH) {
+      float g[CH][VEC];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i0 = s0 + (c * LANES + lane) * VEC;
+        unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), g[c]);
+      }
+      uint64_t m = p.mask;
+      while (m) {
+        const int k = next_slot(m);
+        const int64_t at = __builtin_amdgcn_readlane(p.at, k);
+        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k));
+        if (a.dw) {
+          typename RawOf<T>::type r[CH];
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const int i0 = s0 + (c * LANES + lane) * VEC;
+            r[c] = load8(static_cast<const T*>(a.yp) + at * a.ldp + i0, a.d - i0);
+          }
+          float dot = 0.0f;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            float v[VEC];
+            unpack(r[c], v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) dot = __builtin_fmaf(v[j], g[c][j], dot);
+          }
+          dot = wave_sum(dot);
+          if ((threadIdx.x & 63) == 0) part[group][wave][k] += dot;
+        }
+        if (a.y) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const int i0 = s0 + (c * LANES + lane) * VEC;
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o[j] = w * g[c][j];
+            if (i0 < a.d)
+              store8(static_cast<T*>(a.y) + at * a.ldp + i0, o, a.d - i0, a.stream);
+          }
+        }
+      }
+    }
+  }
+  if (!a.dw) return;
+  __syncthreads();
+  if (real && lane < a.K) {
+    float s = part[group][0][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += part[group][w][lane];
+    a.dw[t * a.K + lane] = s;
+  }
+}
+
+template <class T>
+void launch(const CombineArgs& p, bool backward, hipStream_t s) {
+  TokArgs a{p.yp, p.inv, p.w, p.base, p.y, p.dw, 0, p.T, p.rows, p.ldt, p.ldp, p.K, p.d, false};
+  a.stream = (backward ? p.rows : p.T) * p.d * int64_t(sizeof(T)) >= kStreamBytes;
+  const bool narrow = p.d <= 1024;  // a wave per token, at most two chunks a lane
+  const int64_t per = kMaxBlocks * (narrow ? 4 : 1);
+  for (int64_t t = 0; t < p.T; t += per) {
+    const int64_t n = p.T - t < per ? p.T - t : per;
+    a.t0 = t;
+    a.T = t + n;
+    const dim3 grid(static_cast<unsigned>(narrow ? (n + 3) / 4 : n));
+    if (!backward) {
+      if (narrow)
+        hipLaunchKernelGGL((token_combine_kernel<T, 64>), grid, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((token_combine_kernel<T, 256>), grid, dim3(256), 0, s, a);
+    } else if (narrow) {
+      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 64, 2>), grid, dim3(256), 0, s, a);
+    } else if (p.d <= 2048) {
+      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256, 1>), grid, dim3(256), 0, s, a);
+    } else {
+      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256, 4>), grid, dim3(256), 0, s, a);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_token_combine(const CombineArgs& p, hipStream_t s) {
+  p.bf16 ? launch<uint16_t>(p, false, s) : launch<float>(p, false, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_combine_backward(const CombineArgs& p, hipStream_t s) {
+  p.bf16 ? launch<uint16_t>(p, true, s) : launch<float>(p, true, s);
+  return hipGetLastError();
+}
+
+}  // namespace dsmoe

@@ -310,6 +310,92 @@ struct OrthArgs {
 size_t orth_workspace(int64_t mats, int rows, int cols);
 hipError_t launch_orth(const OrthArgs& p, hipStream_t s);
 
+// ---- operators on a token's way (dsmoe_tokens.h) ------------------------------
+// rmsnorm.hip: x (backward: what was normalized), r residual or dresidual (may be
+// NULL), y output or dy, s sum (may be NULL) or dx.
+struct RmsArgs {
+  int64_t n;
+  int d;
+  bool bf16;
+  float eps;
+  const void* x;
+  const void* r;
+  const float* w;
+  void* y;
+  uint8_t* q;
+  float* scale;
+  void* s;
+  float* rstd;
+  int64_t ldx, ldr, ldy, lds, ldq;
+};
+// rows of partial column sums [parts][d] fp32 the backward writes
+int rmsnorm_backward_parts(int64_t n, int d);
+hipError_t launch_rmsnorm_forward(const RmsArgs& p, hipStream_t s);
+hipError_t launch_rmsnorm_backward(const RmsArgs& p, float* dw, float* part, hipStream_t s);
+
+// dispatch.hip: rows are bytes; x2 a second matrix that moves along (tile scales
+// of E4M3 rows), both contiguous. ldt, ldp: bytes between rows of token and of
+// sorted matrices.
+struct DispatchArgs {
+  int64_t T, rows;
+  int E, K;
+  const int32_t* idx;
+  const uint8_t* x;
+  const uint8_t* x2;
+  int32_t* offsets;
+  int32_t* perm;
+  int32_t* inv;
+  uint8_t* xp;
+  uint8_t* xp2;
+  int64_t row_bytes, row2_bytes, ldt, ldp;
+};
+size_t dispatch_workspace(int64_t T, int K, int E);
+hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s);
+
+// combine.hip: strides in elements
+struct CombineArgs {
+  int64_t T, rows;
+  int K, d;
+  bool bf16;
+  const void* yp;   // sorted rows (may be NULL in the backward)
+  const int32_t* inv;
+  const float* w;   // NULL: 1
+  const void* base; // forward: base or NULL; backward: dy
+  void* y;          // forward: y; backward: dy_perm or NULL
+  float* dw;        // backward: dweight or NULL
+  int64_t ldt, ldp;
+};
+hipError_t launch_token_combine(const CombineArgs& p, hipStream_t s);
+hipError_t launch_token_combine_backward(const CombineArgs& p, hipStream_t s);
+
+// mx4.hip
+struct Mx4Args {
+  int64_t mats, rows, ld, n_src;
+  int k;
+  bool bf16, swiglu;
+  const void* src;
+  const int32_t* perm;
+  uint8_t* codes;
+  uint8_t* scales;
+  void* dst;
+};
+hipError_t launch_mx4_quantize(const Mx4Args& p, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4Args& p, hipStream_t s);
+
+// mx4_gemm.hip
+struct Mx4GemmArgs {
+  int64_t rows, ldy;
+  int G, n, k;
+  bool out_f32;
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const uint8_t* wc;
+  const uint8_t* wsc;
+  const int32_t* offsets;
+  void* y;
+};
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& p, hipStream_t s);
+
 // number of compute units of the current device (cached per device)
 int device_cu_count();
 

@@ -1,0 +1,237 @@
+// Microscaled 4-bit values: quantization and dequantization (formats and layouts
+// in dsmoe_tokens.h).
+//
+// Memory-bound: a lane holds 8 adjacent values (one word of codes), four lanes a
+// block, 16 lanes four blocks, whose scale bytes make one word. A workgroup takes
+// ROWS rows of 512 values at a time, so that the scale words of a column of blocks,
+// which lie row by row, leave as one run of ROWS words and not one by one from
+// several XCDs.
+#include "device_common.h"
+#include "internal.h"
+#include "row_io.h"
+
+namespace dsmoe {
+
+namespace {
+
+constexpr int kSpan = 512;  // values of a row that one wave takes
+// Blocks of 32 rows from which on these are taken; fewer leave CUs idle, and 8 rows
+// make four times as many.
+constexpr int64_t kWide = 1024;
+
+struct QArgs {
+  const void* src;
+  const int32_t* perm;
+  uint8_t* codes;
+  uint8_t* scales;
+  void* dst;
+  int64_t rows, ld, n_src, mat;  // mat: values between matrices
+  int64_t row_blocks, blk0;      // blocks of a matrix's rows; this launch's first
+  int k, kb, kg;
+};
+
+// 2^e, e = -127 .. 127 (2^-127 is below the normal numbers).
+__device__ __forceinline__ float power_of_two(int e) {
+  return __int_as_float(e > -127 ? (e + 127) << 23 : 1 << 22);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_get(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true));
+}
+// Largest of four adjacent lanes' values (magnitude bits of floats), in all of them.
+__device__ __forceinline__ uint32_t max4(uint32_t v) {
+  v = max(v, dpp_get<0xb1>(v));  // quad_perm 1 0 3 2
+  return max(v, dpp_get<0x4e>(v));  // quad_perm 2 3 0 1
+}
+
+// Codes (one word) and scale byte of a lane's eight values of a block. Scaling by
+// a power of two is exact, so the conversion's rounding is the only one.
+__device__ __forceinline__ uint32_t mx4_codes(const float (&v)[VEC], uint32_t& byte) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  top = max4(top);
+  if (top >= 0x7f800000u) {
+    byte = 255;
+    return 0;
+  }
+  // floor(log2) is the exponent; of numbers below the normal ones it is below -126,
+  // where e is -127 either way
+  const int e = max(static_cast<int>(top >> 23) - 127 - 2, -127);
+  byte = static_cast<uint32_t>(e + 127);
+  const float inv = power_of_two(-e);
+  float q[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) q[j] = v[j] * inv;
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[0], q[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[4], q[5], 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[6], q[7], 1.0f, 3);
+  return w;
+}
+
+// Block (matrix, rows of ROWS, span of 512 values), four waves of ROWS / 4 rows
+// each.
+template <class T, int ROWS, bool SWIGLU>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
+  __shared__ uint32_t words[4][ROWS];
+  constexpr int PER = ROWS / 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t blk = a.blk0 + blockIdx.x, mat = blk / a.row_blocks;
+  const int64_t r0 = (blk - mat * a.row_blocks) * ROWS;
+  const int i0 = blockIdx.y * kSpan + lane * VEC;
+  const T* src = static_cast<const T*>(a.src) + mat * a.mat;
+  typename RawOf<T>::type raw[PER], raw2[SWIGLU ? PER : 1];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t r = r0 + wave * PER + i;
+    int64_t from = r < a.rows ? r : -1;
+    if (a.perm && from >= 0) {
+      from = a.perm[r];
+      if (from >= a.n_src) from = -1;
+    }
+    const int cnt = from >= 0 ? a.k - i0 : 0;
+    const T* p = src + (from >= 0 ? from : 0) * a.ld + i0;
+    raw[i] = load8(p, cnt);
+    if constexpr (SWIGLU) raw2[i] = load8(p + a.k, cnt);
+  }
+  uint8_t* codes = a.codes + (mat * a.rows + r0) * a.kb * 16;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    float v[VEC];
+    unpack(raw[i], v);
+    if constexpr (SWIGLU) {
+      float up[VEC];
+      unpack(raw2[i], up);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = silu_f32(v[j]) * up[j];
+    }
+    uint32_t byte;
+    const uint32_t w = mx4_codes(v, byte);
+    const int row = wave * PER + i;
+    if (r0 + row < a.rows && i0 < a.kb * 32)
+      *reinterpret_cast<uint32_t*>(codes + int64_t(row) * a.kb * 16 + i0 / 2) = w;
+    // bytes of lanes 0, 4, 8 and 12 of each 16, blocks past the last one 0
+    uint32_t s = (lane & 3) == 0 && i0 < a.kb * 32 ? byte << (8 * ((lane >> 2) & 3)) : 0u;
+    s |= dpp_get<0x124>(s);  // row_ror:4
+    s |= dpp_get<0x128>(s);  // row_ror:8
+    if ((lane & 15) == 0) words[lane >> 4][row] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 4 * ROWS) {
+    const int g = threadIdx.x / ROWS, row = threadIdx.x % ROWS;
+    const int64_t kg = blockIdx.y * 4 + g;
+    if (kg < a.kg && r0 + row < a.rows)
+      reinterpret_cast<uint32_t*>(a.scales)[(mat * a.kg + kg) * a.rows + r0 + row] = words[g][row];
+  }
+}
+
+// The values of eight codes times 2^(byte - 127); byte 255 makes them NaN.
+__device__ __forceinline__ void mx4_values(uint32_t w, uint32_t byte, float (&v)[VEC]) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const float s = byte == 255 ? __int_as_float(0x7fc00000) : power_of_two(static_cast<int>(byte) - 127);
+  const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3)};
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = p[j >> 1][j & 1] * s;
+}
+
+constexpr int kDeqRows = 8;
+template <class T>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(QArgs a, bool stream) {
+  constexpr int PER = kDeqRows / 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t blk = a.blk0 + blockIdx.x, mat = blk / a.row_blocks;
+  const int64_t r0 = (blk - mat * a.row_blocks) * kDeqRows + wave * PER;
+  const int i0 = blockIdx.y * kSpan + lane * VEC;
+  if (i0 >= a.k) return;
+  const int64_t kg = i0 / 128, col = i0 / 2;
+  uint32_t w[PER], b[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t r = min(r0 + i, a.rows - 1);
+    w[i] = *reinterpret_cast<const uint32_t*>(a.codes + (mat * a.rows + r) * a.kb * 16 + col);
+    b[i] = reinterpret_cast<const uint32_t*>(a.scales)[(mat * a.kg + kg) * a.rows + r];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (r0 + i >= a.rows) return;
+    float v[VEC];
+    mx4_values(w[i], (b[i] >> (8 * ((i0 >> 5) & 3))) & 255u, v);
+    store8(static_cast<T*>(a.dst) + mat * a.mat + (r0 + i) * a.ld + i0, v, a.k - i0, stream);
+  }
+}
+
+QArgs q_args(const Mx4Args& p) {
+  QArgs a{};
+  a.src = p.src;
+  a.perm = p.perm;
+  a.codes = p.codes;
+  a.scales = p.scales;
+  a.dst = p.dst;
+  a.rows = p.rows;
+  a.ld = p.ld;
+  a.n_src = p.n_src;
+  a.mat = p.rows * p.ld;
+  a.k = p.k;
+  a.kb = (p.k + 31) / 32;
+  a.kg = (a.kb + 3) / 4;
+  return a;
+}
+
+// Blocks of `per` rows and one span, in launches that count their work items in 32
+// bits.
+template <class Go>
+void in_launches(QArgs a, int64_t mats, int per, Go&& go) {
+  const int64_t spans = (a.k + kSpan - 1) / kSpan, most = (2 * kMaxBlocks) / spans;
+  a.row_blocks = (a.rows + per - 1) / per;
+  const int64_t total = mats * a.row_blocks;
+  for (a.blk0 = 0; a.blk0 < total; a.blk0 += most) {
+    const int64_t n = total - a.blk0 < most ? total - a.blk0 : most;
+    go(a, dim3(static_cast<unsigned>(n), static_cast<unsigned>(spans)));
+  }
+}
+
+template <class T, bool SWIGLU>
+void quantize(const QArgs& a, int64_t mats, hipStream_t s) {
+  const int64_t spans = (a.k + kSpan - 1) / kSpan;
+  if (mats * ((a.rows + 31) / 32) * spans >= kWide)
+    in_launches(a, mats, 32, [&](const QArgs& b, dim3 grid) {
+      hipLaunchKernelGGL((mx4_quantize_kernel<T, 32, SWIGLU>), grid, dim3(256), 0, s, b);
+    });
+  else
+    in_launches(a, mats, 8, [&](const QArgs& b, dim3 grid) {
+      hipLaunchKernelGGL((mx4_quantize_kernel<T, 8, SWIGLU>), grid, dim3(256), 0, s, b);
+    });
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const Mx4Args& p, hipStream_t s) {
+  if (p.mats == 0 || p.rows == 0) return hipSuccess;
+  const QArgs a = q_args(p);
+  if (p.bf16)
+    p.swiglu ? quantize<uint16_t, true>(a, p.mats, s) : quantize<uint16_t, false>(a, p.mats, s);
+  else
+    p.swiglu ? quantize<float, true>(a, p.mats, s) : quantize<float, false>(a, p.mats, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequantize(const Mx4Args& p, hipStream_t s) {
+  if (p.mats == 0 || p.rows == 0) return hipSuccess;
+  const bool stream = p.mats * p.rows * p.k * (p.bf16 ? 2 : 4) >= kStreamBytes;
+  in_launches(q_args(p), p.mats, kDeqRows, [&](const QArgs& b, dim3 grid) {
+    if (p.bf16)
+      hipLaunchKernelGGL(mx4_dequantize_kernel<uint16_t>, grid, dim3(256), 0, s, b, stream);
+    else
+      hipLaunchKernelGGL(mx4_dequantize_kernel<float>, grid, dim3(256), 0, s, b, stream);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace dsmoe

@@ -1,0 +1,522 @@
+// RMS norm, forward and backward (definition in dsmoe_tokens.h).
+//
+// Memory-bound: the forward reads x (and the residual) once and writes what is
+// asked of rows, codes and the sum once; the backward reads dy, x (and
+// dresidual) once and writes dx once. A row lives in the registers of NW waves
+// (1, 4 or 8 by its length), 8 adjacent values per lane and chunk, so that 16
+// lanes hold a 1x128 tile side by side. Rows longer than kMaxRow are read again
+// from memory for every pass instead.
+#include "device_common.h"
+#include "internal.h"
+#include "row_io.h"
+
+namespace dsmoe {
+
+namespace {
+
+constexpr int kTile = 128;  // values that share an E4M3 scale
+
+struct RmsFwdArgs {
+  const void* x;
+  const void* r;
+  const float* w;
+  void* y;        // NULL: no rows
+  uint8_t* q;     // NULL: no codes
+  float* scale;   // [n][tiles]
+  void* sum;
+  float* rstd;
+  int64_t n, ldx, ldr, ldy, lds, ldq;
+  int d, tiles;
+  float eps, inv_d;
+  bool stream;  // row outputs past the caches
+};
+
+// Largest of 16 adjacent lanes' values as unsigned integers, in all of them: for
+// magnitudes of floats this orders NaN above infinity above all numbers.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+                    0, static_cast<int>(v), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = dpp_max<0x128>(v);  // row_ror:8
+  v = dpp_max<0x124>(v);
+  v = dpp_max<0x122>(v);
+  return dpp_max<0x121>(v);
+}
+
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(1)));
+
+// E4M3 codes of a lane's eight values of a tile; its lane 0 stores the scale.
+__device__ __forceinline__ void store_codes(const float (&o)[VEC], int cnt, uint8_t* q,
+                                            float* scale, bool first, bool stream) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    top = max(top, __float_as_uint(o[j]) & 0x7fffffffu);
+  top = max16(top);
+  if (cnt <= 0) return;
+  const float amax = __uint_as_float(top);
+  uint32_t lo, hi;
+  float sc = amax / 448.0f;
+  if (top >= 0x7f800000u) {
+    lo = hi = 0x7f7f7f7fu;
+  } else if (amax < 0x1p-100f) {
+    lo = hi = 0u;
+    sc = 1.0f;
+  } else {
+    const float inv = 448.0f / amax;
+    lo = e4m3_pack4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    hi = e4m3_pack4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+  }
+  if (first) *scale = sc;
+  if (cnt >= VEC) {
+    const u32x2_any_t v = {lo, hi};
+    if (stream)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any_t*>(q));
+    else
+      *reinterpret_cast<u32x2_any_t*>(q) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < cnt) q[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+  }
+}
+
+// A block of max(NW, 4) waves; NW waves own a row, CH chunks of 8 values per
+// lane. One block per row (NW > 1) or per four rows (NW == 1).
+template <class T, int NW, int CH, bool RES>
+__global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_fwd_kernel(RmsFwdArgs a) {
+  __shared__ float slot[NW];
+  constexpr int LANES = NW * 64;
+  const int64_t row = NW == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (NW == 1 && row >= a.n) return;
+  const int lane = threadIdx.x & (LANES - 1);
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  float v[CH][VEC], w[CH][VEC];
+  typename RawOf<T>::type rx[CH], rr[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i0 = (c * LANES + lane) * VEC;
+    rx[c] = load8(x + i0, a.d - i0);
+    if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr + i0, a.d - i0);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i0 = (c * LANES + lane) * VEC;
+    load_vec(a.w ? a.w + i0 : nullptr, w[c], a.d - i0, 1.0f);
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    unpack(rx[c], v[c]);
+    if constexpr (RES) {
+      float r[VEC];
+      unpack(rr[c], r);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[c][j] += r[j];
+    }
+    float q[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) q[j] = v[c][j] * v[c][j];
+    s += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+  }
+  const float rstd = rsqrtf(row_sum<NW>(s, slot) * a.inv_d + a.eps);
+  if (lane == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i0 = (c * LANES + lane) * VEC;
+    const int cnt = a.d - i0;
+    float o[VEC];
+    if constexpr (RES) {
+      if (cnt > 0) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v[c], cnt, a.stream);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = v[c][j] * rstd * w[c][j];
+    if (a.y && cnt > 0) store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
+    if (a.q)
+      store_codes(o, cnt, a.q + row * a.ldq + i0, a.scale + row * a.tiles + i0 / kTile,
+                  (lane & 15) == 0, a.stream);
+  }
+}
+
+// Rows past the register path: 512 threads, the row read twice (the second time
+// from L2).
+template <class T>
+__global__ __launch_bounds__(512) void rms_fwd_long_kernel(RmsFwdArgs a) {
+  __shared__ float slot[8];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
+  auto get = [&](int i0, float (&v)[VEC]) {
+    unpack(load8(x + i0, a.d - i0), v);
+    if (r) {
+      float u[VEC];
+      unpack(load8(r + i0, a.d - i0), u);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] += u[j];
+    }
+  };
+  float s = 0.0f;
+  for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
+    float v[VEC];
+    get(i0, v);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] *= v[j];
+    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  }
+  const float rstd = rsqrtf(row_sum<8>(s, slot) * a.inv_d + a.eps);
+  if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+  // whole tiles of lanes stay in the loop: the scales are met across 16 lanes
+  for (int i0 = threadIdx.x * VEC; i0 < a.tiles * kTile; i0 += 512 * VEC) {
+    float v[VEC], w[VEC], o[VEC];
+    const int cnt = a.d - i0;
+    get(i0, v);
+    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
+    if (r && cnt > 0) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v, cnt, a.stream);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = v[j] * rstd * w[j];
+    if (a.y && cnt > 0) store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
+    if (a.q)
+      store_codes(o, cnt, a.q + row * a.ldq + i0, a.scale + row * a.tiles + i0 / kTile,
+                  (threadIdx.x & 15) == 0, a.stream);
+  }
+}
+
+// ---- backward ---------------------------------------------------------------
+
+struct RmsBwdArgs {
+  const void* dy;
+  const void* x;
+  const float* w;
+  const float* rstd;
+  const void* dr;
+  void* dx;
+  float* part;  // [gridDim.x][d] partial dweight; NULL: not wanted
+  int64_t n, ldx, ldr, ldy, lds;
+  int d;
+  bool stream;  // row outputs past the caches
+};
+
+// A row group (NW waves) takes rows slot, slot + slots, ... and keeps the column
+// sums of dy z for its columns in registers over all of them; each block then
+// writes one partial sum per column. The next row is loaded while the current one
+// is reduced. With NW == 1 the block's four waves add their column sums through
+// LDS, in wave order.
+template <class T, int NW, int CH, bool RES>
+__global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwdArgs a) {
+  constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
+  __shared__ float slot[2][NW];
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t first = int64_t(blockIdx.x) * GROUPS + (NW == 1 ? threadIdx.x >> 6 : 0);
+  const int64_t stride = int64_t(gridDim.x) * GROUPS;
+  float aw[CH][VEC], w[CH][VEC];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i0 = (c * LANES + lane) * VEC;
+    load_vec(a.w ? a.w + i0 : nullptr, w[c], a.d - i0, 1.0f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) aw[c][j] = 0.0f;
+  }
+  typename RawOf<T>::type rx[CH], rg[CH], rr[CH];
+  float rs = 0.0f;
+  auto fetch = [&](int64_t row) {
+    rs = a.rstd[row];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i0 = (c * LANES + lane) * VEC;
+      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx + i0, a.d - i0);
+      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, a.d - i0);
+      if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0);
+    }
+  };
+  if (first < a.n) fetch(first);
+  int par = 0;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  for (int64_t row = first; row < a.n; row += stride) {
+    float z[CH][VEC], g[CH][VEC];
+    typename RawOf<T>::type kr[CH];
+    float s = 0.0f;
+    const float r = rs;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      unpack(rx[c], z[c]);
+      unpack(rg[c], g[c]);
+      if constexpr (RES) kr[c] = rr[c];
+      const int cnt = a.d - (c * LANES + lane) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        z[c][j] = j < cnt ? z[c][j] * r : 0.0f;
+        aw[c][j] += g[c][j] * z[c][j];
+        g[c][j] *= w[c][j];
+        s += g[c][j] * z[c][j];
+      }
+    }
+    if (row + stride < a.n) fetch(row + stride);
+    const float c2 = row_sum<NW>(s, slot[par]) * inv_d;
+    par ^= 1;  // the next row's sums go to the other slots: one barrier per row
+    T* dx = static_cast<T*>(a.dx) + row * a.lds;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i0 = (c * LANES + lane) * VEC;
+      if (i0 >= a.d) continue;
+      float o[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = r * (g[c][j] - z[c][j] * c2);
+      if constexpr (RES) {
+        float e[VEC];
+        unpack(kr[c], e);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] += e[j];
+      }
+      store8(dx + i0, o, a.d - i0, a.stream);
+    }
+  }
+  if (!a.part) return;
+  float* pw = a.part + int64_t(blockIdx.x) * a.d;
+  if constexpr (NW == 1) {
+    __shared__ float red[4][CH * 64 * VEC];
+    const int wv = threadIdx.x >> 6;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) red[wv][(c * 64 + lane) * VEC + j] = aw[c][j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d; i += 256)
+      pw[i] = ((red[0][i] + red[1][i]) + red[2][i]) + red[3][i];
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i0 = (c * LANES + lane) * VEC;
+      if (i0 < a.d) store8(pw + i0, aw[c], a.d - i0);
+    }
+  }
+}
+
+// Rows past the register path: dx in two passes over the row; the column sums
+// come from rms_cols_kernel.
+template <class T>
+__global__ __launch_bounds__(512) void rms_bwd_long_kernel(RmsBwdArgs a) {
+  __shared__ float slot[8];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.ldy;
+  const float r = a.rstd[row];
+  auto get = [&](int i0, float (&z)[VEC], float (&g)[VEC]) {
+    float w[VEC];
+    const int cnt = a.d - i0;
+    unpack(load8(x + i0, cnt), z);
+    unpack(load8(dy + i0, cnt), g);
+    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      z[j] = j < cnt ? z[j] * r : 0.0f;
+      g[j] *= w[j];
+    }
+  };
+  float s = 0.0f;
+  for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
+    float z[VEC], g[VEC];
+    get(i0, z, g);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s += g[j] * z[j];
+  }
+  const float c2 = row_sum<8>(s, slot) / static_cast<float>(a.d);
+  for (int i0 = threadIdx.x * VEC; i0 < a.d; i0 += 512 * VEC) {
+    float z[VEC], g[VEC], o[VEC];
+    get(i0, z, g);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = r * (g[j] - z[j] * c2);
+    if (a.dr) {
+      float e[VEC];
+      unpack(load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0), e);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] += e[j];
+    }
+    store8(static_cast<T*>(a.dx) + row * a.lds + i0, o, a.d - i0, a.stream);
+  }
+}
+
+// Partial column sums of dy z: block (x, y) takes 512 columns and rows y, y +
+// gridDim.y, ...
+template <class T>
+__global__ __launch_bounds__(64) void rms_cols_kernel(RmsBwdArgs a) {
+  const int i0 = (blockIdx.x * 64 + threadIdx.x) * VEC;
+  if (i0 >= a.d) return;
+  const int cnt = a.d - i0;
+  float aw[VEC] = {};
+  for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
+    float z[VEC], g[VEC];
+    unpack(load8(static_cast<const T*>(a.x) + row * a.ldx + i0, cnt), z);
+    unpack(load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, cnt), g);
+    const float r = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) aw[j] += g[j] * (z[j] * r);
+  }
+  store8(a.part + int64_t(blockIdx.y) * a.d + i0, aw, cnt);
+}
+
+// dweight = sum of the partial rows [parts][d], in a fixed order: a block takes
+// 32 columns, its 32 half-waves a run of the parts each, whose sums are then
+// added in order; eight loads in flight per lane.
+__global__ __launch_bounds__(1024) void rms_sum_parts_kernel(const float* part, int parts, int d,
+                                                             float* dw) {
+  __shared__ float red[32][32];
+  const int run = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t width = d, col = int64_t(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (col < width) {
+    const int per = (parts + 31) / 32, p0 = run * per, p1 = min(parts, p0 + per);
+    const float* at = part + p0 * width + col;
+    int left = p1 - p0;
+    for (; left >= 8; left -= 8, at += 8 * width) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = at[i * width];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; left > 0; --left, at += width) s += *at;
+  }
+  red[run][lane] = s;
+  __syncthreads();
+  if (run || col >= width) return;
+#pragma unroll
+  for (int w = 1; w < 32; ++w) s += red[w][lane];
+  dw[col] = s;
+}
+
+// ---- shapes ------------------------------------------------------------------
+
+constexpr int kMaxRow = 16384;  // 8 waves x 64 lanes x 4 chunks x 8 values
+
+// Waves and chunks of a row of d values.
+struct RowShape {
+  int nw, ch;
+};
+RowShape row_shape(int d) {
+  if (d <= 512) return {1, 1};
+  if (d <= 1024) return {1, 2};
+  if (d <= 2048) return {4, 1};
+  if (d <= 4096) return {4, 2};
+  if (d <= 8192) return {8, 2};
+  return {8, 4};
+}
+
+template <class T, bool RES>
+void fwd_launch(const RmsFwdArgs& a, hipStream_t s) {
+  const unsigned rows = static_cast<unsigned>(a.n), quads = static_cast<unsigned>((a.n + 3) / 4);
+  if (a.d > kMaxRow) {
+    hipLaunchKernelGGL(rms_fwd_long_kernel<T>, dim3(rows), dim3(512), 0, s, a);
+    return;
+  }
+  const RowShape r = row_shape(a.d);
+#define RMS_CASE(NW, CH)                                                                 \
+  if (r.nw == NW && r.ch == CH) {                                                        \
+    hipLaunchKernelGGL((rms_fwd_kernel<T, NW, CH, RES>), dim3(NW == 1 ? quads : rows),   \
+                       dim3(NW == 1 ? 256 : NW * 64), 0, s, a);                          \
+    return;                                                                              \
+  }
+  RMS_CASE(1, 1)
+  RMS_CASE(1, 2)
+  RMS_CASE(4, 1)
+  RMS_CASE(4, 2)
+  RMS_CASE(8, 2)
+  RMS_CASE(8, 4)
+#undef RMS_CASE
+}
+
+template <class T, bool RES>
+void fwd_dispatch(const RmsFwdArgs& a, hipStream_t s) {
+  const int64_t per = kMaxBlocks * (a.d <= kMaxRow && row_shape(a.d).nw == 1 ? 4 : 1);
+  for (int64_t row = 0; row < a.n; row += per) {
+    RmsFwdArgs b = a;
+    b.n = a.n - row < per ? a.n - row : per;
+    b.x = static_cast<const T*>(a.x) + row * a.ldx;
+    if (RES) b.r = static_cast<const T*>(a.r) + row * a.ldr;
+    if (a.y) b.y = static_cast<T*>(a.y) + row * a.ldy;
+    if (a.q) b.q = a.q + row * a.ldq;
+    if (a.q) b.scale = a.scale + row * a.tiles;
+    if (RES) b.sum = static_cast<T*>(a.sum) + row * a.lds;
+    if (a.rstd) b.rstd = a.rstd + row;
+    fwd_launch<T, RES>(b, s);
+  }
+}
+
+template <class T, bool RES>
+void bwd_dispatch(const RmsBwdArgs& a, int parts, hipStream_t s) {
+  if (a.d > kMaxRow) {
+    // the column sums first: dx may take dy's place
+    if (a.part)
+      hipLaunchKernelGGL(rms_cols_kernel<T>, dim3((a.d + 511) / 512, parts), dim3(64), 0, s, a);
+    for (int64_t row = 0; row < a.n; row += kMaxBlocks) {
+      RmsBwdArgs b = a;
+      b.n = a.n - row < kMaxBlocks ? a.n - row : kMaxBlocks;
+      b.dy = static_cast<const T*>(a.dy) + row * a.ldy;
+      b.x = static_cast<const T*>(a.x) + row * a.ldx;
+      if (a.dr) b.dr = static_cast<const T*>(a.dr) + row * a.ldr;
+      b.dx = static_cast<T*>(a.dx) + row * a.lds;
+      b.rstd = a.rstd + row;
+      hipLaunchKernelGGL(rms_bwd_long_kernel<T>, dim3(static_cast<unsigned>(b.n)), dim3(512), 0, s,
+                         b);
+    }
+    return;
+  }
+  const RowShape r = row_shape(a.d);
+#define RMS_CASE(NW, CH)                                                          \
+  if (r.nw == NW && r.ch == CH) {                                                 \
+    hipLaunchKernelGGL((rms_bwd_kernel<T, NW, CH, RES>), dim3(parts),             \
+                       dim3(NW == 1 ? 256 : NW * 64), 0, s, a);                   \
+    return;                                                                       \
+  }
+  RMS_CASE(1, 1)
+  RMS_CASE(1, 2)
+  RMS_CASE(4, 1)
+  RMS_CASE(4, 2)
+  RMS_CASE(8, 2)
+  RMS_CASE(8, 4)
+#undef RMS_CASE
+}
+
+}  // namespace
+
+// Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
+int rmsnorm_backward_parts(int64_t n, int d) {
+  if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);
+  const int nw = row_shape(d).nw;
+  const int64_t groups = nw == 1 ? (n + 3) / 4 : n, most = nw == 8 ? 256 : 512;
+  return static_cast<int>(groups < 1 ? 1 : groups < most ? groups : most);
+}
+
+namespace {
+bool streamed(const RmsArgs& p) { return p.n * p.d * (p.bf16 ? 2 : 4) >= kStreamBytes; }
+}  // namespace
+
+hipError_t launch_rmsnorm_forward(const RmsArgs& p, hipStream_t s) {
+  if (p.n == 0) return hipSuccess;
+  const RmsFwdArgs a{p.x, p.r, p.w, p.y, p.q, p.scale, p.s, p.rstd, p.n, p.ldx, p.ldr, p.ldy,
+                     p.lds, p.ldq, p.d, (p.d + kTile - 1) / kTile, p.eps, 1.0f / p.d, streamed(p)};
+  if (p.bf16)
+    p.r ? fwd_dispatch<uint16_t, true>(a, s) : fwd_dispatch<uint16_t, false>(a, s);
+  else
+    p.r ? fwd_dispatch<float, true>(a, s) : fwd_dispatch<float, false>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_backward(const RmsArgs& p, float* dw, float* part, hipStream_t s) {
+  const int parts = rmsnorm_backward_parts(p.n, p.d);
+  if (p.n > 0) {
+    const RmsBwdArgs a{p.y, p.x, p.w, p.rstd, p.r, p.s, dw ? part : nullptr,
+                       p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, streamed(p)};
+    if (p.bf16)
+      p.r ? bwd_dispatch<uint16_t, true>(a, parts, s) : bwd_dispatch<uint16_t, false>(a, parts, s);
+    else
+      p.r ? bwd_dispatch<float, true>(a, parts, s) : bwd_dispatch<float, false>(a, parts, s);
+  }
+  if (dw)
+    hipLaunchKernelGGL(rms_sum_parts_kernel, dim3((p.d + 31) / 32), dim3(1024), 0, s, part,
+                       p.n > 0 ? parts : 0, p.d, dw);
+  return hipGetLastError();
+}
+
+}  // namespace dsmoe
