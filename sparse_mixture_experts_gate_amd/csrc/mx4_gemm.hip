@@ -15,6 +15,7 @@
 #include "group_tables.h"
 #include "internal.h"
 #include "resident_grid.h"
+#include "row_io.h"
 #include "tile_schedule.h"
 
 namespace dsmoe {
@@ -195,57 +196,79 @@ __device__ __forceinline__ f32x16_t mma4(i32x4_t a, i32x4_t b, f32x16_t c, int s
 }
 
 // Stores eight adjacent values of a row, of which `cnt` exist.
-__device__ __forceinline__ void put8(const MArgs& a, int64_t at, int cnt, const float (&v)[8]) {
-  if (a.out_f32) {
-    float* p = static_cast<float*>(a.y) + at;
-    if (a.vec && cnt >= 8) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cnt) p[j] = v[j];
-    }
+__device__ __forceinline__ void put8(const MArgs& a, int64_t at, int cnt, const uint32_t (&w)[4]) {
+  uint16_t* p = static_cast<uint16_t*>(a.y) + at;
+  if (a.vec && cnt >= 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    uint16_t* p = static_cast<uint16_t*>(a.y) + at;
-    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    if (a.vec && cnt >= 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+    for (int j = 0; j < 8; ++j)
+      if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+  }
+}
+__device__ __forceinline__ void put4(const MArgs& a, int64_t at, int cnt, const float (&v)[4]) {
+  float* p = static_cast<float*>(a.y) + at;
+  if (a.vec && cnt >= 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 4; ++j)
+      if (j < cnt) p[j] = v[j];
+  }
+}
+
+// Output of a finished tile, straight from registers, so that no barrier holds the
+// other waves: a lane has columns 8 g + 4 h .. + 3 (g = 0 .. 3, h its half) of row l %
+// 32. For bf16 the halves swap words, which leaves each lane 8 adjacent columns of
+// its row, 16 bytes.
+template <class C>
+__device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int wm, int wn, int lane,
+                                           const f32x16_t (&acc)[C::MI][C::NJ]) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) {
+    const int r = c.m * C::BM + wm * C::WM + mi * 32 + (lane & 31);
+    const int64_t row = (c.row0 + r) * a.ldy;
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj) {
+      const int col0 = c.n * C::BN + wn * C::WN + nj * 32;
+      const f32x16_t& x = acc[mi][nj];
+      if (a.out_f32) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = col0 + 8 * g + 4 * h;
+          const float v[4] = {x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+          if (r < c.rows && col < a.n) put4(a, row + col, a.n - col, v);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const auto s = __builtin_amdgcn_permlane32_swap(
+                bf16_pair(x[8 * q + 2 * j], x[8 * q + 2 * j + 1]),
+                bf16_pair(x[8 * q + 4 + 2 * j], x[8 * q + 4 + 2 * j + 1]), false, false);
+            w[j] = s[0];
+            w[2 + j] = s[1];
+          }
+          const int col = col0 + 16 * q + 8 * h;
+          if (r < c.rows && col < a.n) put8(a, row + col, a.n - col, w);
+        }
+      }
     }
   }
 }
 
-template <class C, class P>
-__device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int wm, int wn, int lane,
-                                           f32x16_t (&acc)[C::MI][C::NJ], float* stage) {
-#pragma unroll
-  for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-    for (int part = 0; part < P::PARTS; ++part) {
-      const int col = c.n * C::BN + wn * C::WN + part * P::COLS + P::col(lane);
-      P::put(stage, lane, acc[mi], part);
-#pragma unroll
-      for (int p = 0; p < P::N; ++p) {
-        float v[8];
-        P::get(stage, lane, p, v);
-        const int r = c.m * C::BM + wm * C::WM + mi * 32 + P::row(p, lane);
-        if (r < c.rows && col < a.n) put8(a, (c.row0 + r) * a.ldy + col, a.n - col, v);
-      }
-    }
-}
-
-// Ring loop for small tiles: NST stages, loads NST - 1 k-steps ahead, the blocks of
-// sub-step kk + 1 read between the matrix instructions of sub-step kk, one barrier
-// per k-step (before its last sub-step, whose blocks are already in registers).
+// The k-loop: NST stages; the blocks of sub-step kk + 1 are read between the matrix
+// instructions of sub-step kk. One barrier per k-step, before its last sub-step,
+// whose blocks are already in registers: behind it the step's stage is free and is
+// loaded with step k + NST at once, and step k + 1's loads, NST - 1 steps old, have
+// landed. Waves are in step only there, so the two waves of a SIMD fill each
+// other's gaps, and a wave that stores its tile holds no other up.
 template <class C, class NextOps, class Epilogue>
-__device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, float* out, int first, int nb,
-                                         int total, NextOps&& next_ops, Epilogue&& epilogue) {
+__device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first, int nb, int total,
+                                         NextOps&& next_ops, Epilogue&& epilogue) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -275,17 +298,20 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, float* out
 #pragma unroll
     for (int i = 0; i < C::NJ; ++i) sb[i] = nbs[i];
   };
-  auto sub = [&](auto kk_c, int buf, int st_rd, int kk_rd, bool dma, int st_dma) {
-    constexpr int KK = decltype(kk_c)::value;
+  auto sub = [&](auto kk_c, int st_rd, int st_dma) {
+    constexpr int KK = decltype(kk_c)::value, buf = KK & 1;
     constexpr int RPS = (NR + NM - 1) / NM, LPS = (NL + NM - 1) / NM;
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
       const int mi = i / C::NJ, nj = i % C::NJ;
       acc[mi][nj] = mma4<KK>(af[buf][mi], bf[buf][nj], acc[mi][nj], sa[mi], sb[nj]);
+      // holds the instruction here (no code): selected out of this order, all blocks
+      // of a k-step are live at once and spill
+      asm volatile("" : "+v"(acc[mi][nj]));
 #pragma unroll
       for (int q = 0; q < RPS; ++q)
-        if (i * RPS + q < NR) rd(st_rd, kk_rd, buf ^ 1, i * RPS + q);
-      if (dma) {
+        if (i * RPS + q < NR) rd(st_rd, (KK + 1) & 3, buf ^ 1, i * RPS + q);
+      if constexpr (KK == 3) {
 #pragma unroll
         for (int q = 0; q < LPS; ++q)
           if (i * LPS + q < NL) ld.load(st_dma, i * LPS + q);
@@ -294,14 +320,14 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, float* out
     }
   };
 #pragma unroll
-  for (int j = 0; j < NST - 1; ++j) {
+  for (int j = 0; j < NST; ++j) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) ld.load(j, i);
     ld.advance();
   }
-  vm_wait<INFLIGHT>();
+  vm_wait<(INFLIGHT + NL < 63 ? INFLIGHT + NL : 63)>();
   lds_barrier();
-  int st = 0, sti = NST - 1;
+  int st = 0;
 #pragma unroll
   for (int i = 0; i < NR; ++i) rd(st, 0, 0, i);
   rd_scales(st);
@@ -309,102 +335,27 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, float* out
     zero_acc<C>(acc);
     const int nkc = epilogue.k_steps();
     for (int kc = 0; kc < nkc; ++kc) {
+      const int next = st == NST - 1 ? 0 : st + 1;
       use_scales();
-      sub(std::integral_constant<int, 0>{}, 0, st, 1, true, sti);
-      ld.advance();
-      sub(std::integral_constant<int, 1>{}, 1, st, 2, false, 0);
-      sub(std::integral_constant<int, 2>{}, 0, st, 3, false, 0);
+      sub(std::integral_constant<int, 0>{}, st, 0);
+      sub(std::integral_constant<int, 1>{}, st, 0);
+      sub(std::integral_constant<int, 2>{}, st, 0);
       vm_wait<INFLIGHT>();
       lds_barrier();
-      st = st == NST - 1 ? 0 : st + 1;
-      sti = sti == NST - 1 ? 0 : sti + 1;
-      rd_scales(st);
-      sub(std::integral_constant<int, 3>{}, 1, st, 0, false, 0);
+      rd_scales(next);
+      sub(std::integral_constant<int, 3>{}, next, st);
+      ld.advance();
+      st = next;
     }
-    epilogue(tc, wm, wn, lane, acc, out + wave * RowPasses<C>::FLOATS);
+    epilogue(tc, wm, wn, lane, acc);
   }
   vm_wait<0>();
 }
 
-// Two-phase loop for 256-wide tiles in 8 waves, as the 16-bit products' (its
-// comment shows why the stages are safe): four waves multiply while the other four
-// read the next sub-step's blocks and issue loads, then they swap.
-template <class C, class NextOps, class Epilogue>
-__device__ __forceinline__ void mx4_phased(uint16_t* lds, uint32_t* sc, int first, int nb, int total,
-                                           NextOps&& next_ops, Epilogue&& epilogue) {
-  static_assert(C::NWAVES == 8 && C::NST == 2, "two halves of four waves, two stages");
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  using L = MLoader<C, std::remove_reference_t<NextOps>>;
-  constexpr int NL = L::NL, PARTS = 2, PER = (NL + PARTS - 1) / PARTS;
-  L ld(next_ops, lds_addr(lds), lds_addr(sc), first, nb, total, wave);
-  i32x4_t af[C::MI], bf[C::NJ];
-  int sa[C::MI], sb[C::NJ];
-  f32x16_t acc[C::MI][C::NJ];
-#pragma unroll
-  for (int i = 0; i < NL; ++i) ld.load(0, i);
-  ld.advance();
-  vm_wait<0>();
-  lds_barrier();
-  int st = 0;
-  auto phase = [&](auto kk_c) {
-    constexpr int KK = decltype(kk_c)::value;
-    if constexpr (KK == 0) {
-#pragma unroll
-      for (int i = 0; i < C::NJ; ++i) sb[i] = word_of<C>(sc, st, true, wn * C::WN + i * 32, lane);
-#pragma unroll
-      for (int i = 0; i < C::MI; ++i) sa[i] = word_of<C>(sc, st, false, wm * C::WM + i * 32, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < C::NJ; ++i) bf[i] = block_of<C>(lds, st, true, wn * C::WN + i * 32, KK, lane);
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i)
-      af[i] = block_of<C>(lds, st, false, wm * C::WM + i * 32, KK, lane);
-    if constexpr (KK < PARTS) {
-#pragma unroll
-      for (int i = KK * PER; i < (KK + 1) * PER && i < NL; ++i) ld.load(st ^ 1, i);
-      if constexpr (KK == PARTS - 1) ld.advance();
-    }
-    if constexpr (KK == 3) vm_wait<0>();
-    lds_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-      for (int nj = 0; nj < C::NJ; ++nj)
-        acc[mi][nj] = mma4<KK>(af[mi], bf[nj], acc[mi][nj], sa[mi], sb[nj]);
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  for (int tc = first; tc < total; tc += nb) {
-    zero_acc<C>(acc);
-    const int nkc = epilogue.k_steps();
-    if (wave >= 4) __builtin_amdgcn_s_barrier();
-    for (int kc = 0; kc < nkc; ++kc) {
-      phase(std::integral_constant<int, 0>{});
-      phase(std::integral_constant<int, 1>{});
-      phase(std::integral_constant<int, 2>{});
-      phase(std::integral_constant<int, 3>{});
-      st ^= 1;
-    }
-    if (wave < 4) __builtin_amdgcn_s_barrier();
-    // the stage just read is free until the next tile's first loads
-    static_assert(8 * StagePasses<C>::FLOATS * 4 <= C::STAGE * 2, "output stages fit");
-    epilogue(tc, wm, wn, lane, acc,
-             reinterpret_cast<float*>(lds + (st ^ 1) * C::STAGE) + wave * StagePasses<C>::FLOATS);
-    lds_barrier();
-  }
-  vm_wait<0>();
-}
-
-template <class C, bool PHASED>
+template <class C>
 __global__ __launch_bounds__(C::NT, C::MINW) void mx4_gemm_kernel(MArgs a) {
-  constexpr int kOut = PHASED ? 0 : C::NWAVES * RowPasses<C>::FLOATS;
   __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
   __shared__ uint32_t sc[C::NST * Scales<C>::STAGE];
-  __shared__ __attribute__((aligned(16))) float out[kOut ? kOut : 1];
   __shared__ GroupTables gt;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, (a.n + C::BN - 1) / C::BN);
   const int total = gt.total, nb = gridDim.x;
@@ -416,21 +367,17 @@ __global__ __launch_bounds__(C::NT, C::MINW) void mx4_gemm_kernel(MArgs a) {
     const MArgs& a;
     const GroupTables& t;
     __device__ int k_steps() const { return (a.kb + kStepBlocks - 1) / kStepBlocks; }
-    __device__ void operator()(int tile, int wm, int wn, int lane, f32x16_t (&acc)[C::MI][C::NJ],
-                               float* stage) const {
-      using P = std::conditional_t<PHASED, StagePasses<C>, RowPasses<C>>;
-      store_tile<C, P>(a, tile_of<C>(a, t, tile), wm, wn, lane, acc, stage);
+    __device__ void operator()(int tile, int wm, int wn, int lane,
+                               const f32x16_t (&acc)[C::MI][C::NJ]) const {
+      store_tile<C>(a, tile_of<C>(a, t, tile), wm, wn, lane, acc);
     }
   } ep{a, gt};
-  if constexpr (PHASED)
-    mx4_phased<C>(lds, sc, first, nb, total, next_ops, ep);
-  else
-    mx4_ring<C>(lds, sc, out, first, nb, total, next_ops, ep);
+  mx4_ring<C>(lds, sc, first, nb, total, next_ops, ep);
 }
 
 // ---- choice of the kernel -------------------------------------------------------
 
-using TileBig = Tile<256, 256, 128, 64, 2>;      // 8 waves, two-phase loop
+using TileBig = Tile<256, 256, 128, 64, 2>;      // 8 waves
 using TileMid = Tile<128, 128, 64, 32, 3>;       // 8 waves
 using TileDec = Tile<32, 128, 32, 64, 6, true>;  // 2 waves, weights streamed past L2
 
@@ -440,10 +387,9 @@ int64_t tile_bound(const MArgs& a) {
   return (a.rows / C::BM + (a.rows < a.G ? a.rows : a.G)) * tn;
 }
 
-template <class C, bool PHASED>
+template <class C>
 void launch(const MArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx4_gemm_kernel<C, PHASED>),
-                     dim3(grid_of<mx4_gemm_kernel<C, PHASED>>(C::NT, tile_bound<C>(a))),
+  hipLaunchKernelGGL((mx4_gemm_kernel<C>), dim3(grid_of<mx4_gemm_kernel<C>>(C::NT, tile_bound<C>(a))),
                      dim3(C::NT), 0, s, a);
 }
 
@@ -499,11 +445,11 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& p, hipStream_t s) {
   a.vec = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
   const int c = choose(a);
   if (c == 0)
-    launch<TileBig, true>(a, s);
+    launch<TileBig>(a, s);
   else if (c == 1)
-    launch<TileMid, false>(a, s);
+    launch<TileMid>(a, s);
   else
-    launch<TileDec, false>(a, s);
+    launch<TileDec>(a, s);
   return hipGetLastError();
 }
 
