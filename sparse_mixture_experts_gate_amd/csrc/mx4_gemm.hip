@@ -1,13 +1,23 @@
 // Products grouped by expert on microscaled 4-bit operands (definition in
 // dsmoe_tokens.h): y = x W_g^T over ragged row groups.
 //
-// A block of 32 codes is 16 bytes, the 16-byte chunk of the 16-bit products'
-// tiles: operands go straight into LDS in 128-byte rows (a k-step: 256 values),
-// with the same swizzle, loaders and loops. A matrix instruction of 32 x 32 x 64
-// takes one block per lane and its scale byte from a register's byte chosen by the
-// instruction. The k order inside a step is ours to choose: lane half h takes
-// chunks 4 h .. 4 h + 3, so the scale word [k / 128][row] of its half holds the
-// bytes of its four sub-steps, and one 4-byte LDS read per 32 rows serves a k-step.
+// A block of 32 codes is 16 bytes: operands go straight into LDS by 16-byte loads,
+// rows of 8 blocks (a k-step of 256 values) in XOR-swizzled chunks. A matrix
+// instruction of 32 x 32 x 64 takes one block per lane and its scale byte from a
+// register's byte chosen by the instruction. The k order inside a step is ours to
+// choose: lane half h takes chunks 4 h .. 4 h + 3, so the scale word [k / 128][row] of
+// its half holds the bytes of its four sub-steps, and one 4-byte LDS read per 32 rows
+// serves a k-step.
+//
+// What bounds it, measured. Large products the power limit: one group of 8192 rows,
+// 4096 x 7168, 119 us, 4.0 PFLOP/s with random codes and a third more with zeros; the
+// matrix instructions alone, operands held in registers, reach 6.4 at 1.5 GHz, and
+// with the loads into LDS switched off the same loop takes 52% of the time. Few rows:
+// the stream of weights (128 rows over 256 experts of 4096 x 7168: 227 us, 6.9 TB/s).
+// Measured equal or slower: waves in step per sub-step as in the 16-bit products'
+// large tiles (123 us; four barriers more a step), k-steps of 128 values in four
+// stages (127), loads of the lines three steps ahead into L2 (131), waves without rows
+// leaving out their matrix instructions (the same).
 #include <cmath>
 
 #include "device_common.h"
@@ -22,8 +32,35 @@ namespace dsmoe {
 
 namespace {
 
-constexpr int kStepBlocks = 8;  // blocks of a row per k-step
-constexpr int kFp4 = 4;         // operand format of the scaled matrix instructions
+constexpr int kFp4 = 4;  // operand format of the scaled matrix instructions
+
+constexpr int kChunks = 8;          // blocks of a row per k-step, 16 bytes each
+constexpr int kRow = kChunks * 16;  // bytes of a row of a stage
+constexpr int kSubs = kChunks / 2;  // matrix instructions along a k-step
+
+// BM x BN tile in waves of WM x WN, NST LDS stages in the load ring.
+template <int BM_, int BN_, int WM_, int WN_, int NST_, bool B_NT_ = false>
+struct MxTile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+  static constexpr bool B_NT = B_NT_;  // weights streamed past L2
+  static constexpr int WAVES_N = BN / WN, NWAVES = BM / WM * WAVES_N, NT = NWAVES * 64;
+  static constexpr int MI = WM / 32, NJ = WN / 32;
+  static constexpr int RPP = NT / kChunks;  // rows covered by one pass of 16-byte loads
+  static constexpr int A_LOADS = BM / RPP, B_LOADS = BN / RPP;
+  // scale words of a stage: [A half-steps][BM], then [B half-steps][BN]
+  static constexpr int A_WORDS = 2 * BM, B_WORDS = 2 * BN;
+  // waves that load A's words; the others B's, or all of them both
+  static constexpr bool SHARED = BM == BN;
+  static constexpr int S_LOADS = SHARED ? 1 : 2;
+  static constexpr int A_LANES = A_WORDS / 4 / (SHARED ? NWAVES / 2 : NWAVES);
+  static constexpr int B_LANES = B_WORDS / 4 / (SHARED ? NWAVES / 2 : NWAVES);
+  static constexpr int CODES = (BM + BN) * kRow;
+  static constexpr int STAGE = CODES + (A_WORDS + B_WORDS) * 4;  // bytes
+  static constexpr int NL = A_LOADS + B_LOADS + S_LOADS;         // loads of a wave and step
+  static_assert(BM % RPP == 0 && BN % RPP == 0 && RPP % 16 == 0, "whole passes, one swizzle");
+  static_assert(A_LANES <= 64 && B_LANES <= 64 && STAGE % 16 == 0, "one load of a wave's words");
+  static_assert(NST >= 2 && NL * (NST - 2) <= 63, "ring depth within the vmcnt range");
+};
 
 struct MArgs {
   const uint8_t* xc;
@@ -39,24 +76,18 @@ struct MArgs {
   int out_f32, vec;
 };
 
-// Scale words of a stage: [A half 0 | A half 1 | B half 0 | B half 1], rows adjacent,
-// in pieces of 64 words, dealt over the waves.
-template <class C>
-struct Scales {
-  static constexpr int WORDS = 2 * (C::BM + C::BN);
-  static constexpr int PIECES = WORDS / 64;
-  static constexpr int LOADS = (PIECES + C::NWAVES - 1) / C::NWAVES;
-  static constexpr int STAGE = LOADS * C::NWAVES * 64;  // words, the last pieces unused
-  static_assert(WORDS % 64 == 0 && (2 * C::BM) % 64 == 0, "a piece belongs to one operand");
-};
+// Swizzled position of a row's chunk: 16 lanes that one 128-bit LDS access serves
+// together read one chunk of 16 adjacent rows, which this spreads over all banks.
+__device__ __forceinline__ int position(int row, int chunk) {
+  return chunk ^ ((row >> 1) & 7);
+}
 
 template <class C>
 struct MOps {
-  i32x4_t ra, rb;
-  i32x4_t rs[Scales<C>::LOADS];
-  uint32_t ao[C::A_LOADS], bo[C::B_LOADS], so[Scales<C>::LOADS];
-  uint32_t sstep[Scales<C>::LOADS];  // bytes between k-steps
-  uint32_t tail_a, tail_b;
+  i32x4_t ra, rb, rs[C::S_LOADS];
+  uint32_t ao[C::A_LOADS], bo[C::B_LOADS], so[C::S_LOADS];
+  uint32_t sstep[C::S_LOADS];  // bytes between k-steps
+  uint32_t tail;               // sends chunks past a row's end out of range in the last step
   int nk;
 };
 
@@ -78,42 +109,54 @@ __device__ __forceinline__ MTile tile_of(const MArgs& a, const GroupTables& t, i
   return c;
 }
 
-__device__ __forceinline__ int64_t row_span(int rows, uint32_t ld) {
-  return rows > 0 ? int64_t(rows) * ld : 0;
-}
-
 template <class C>
 __device__ __forceinline__ void tile_ops(const MArgs& a, const MTile& c, int wave, MOps<C>& op) {
-  using S = Scales<C>;
   const uint32_t ld = static_cast<uint32_t>(a.kb) * 16u;  // bytes of a row, of both operands
-  const int left = c.rows - c.m * C::BM, nleft = a.n - c.n * C::BN;
+  const int left = min(c.rows - c.m * C::BM, C::BM), nleft = min(a.n - c.n * C::BN, C::BN);
   const int64_t row = c.row0 + int64_t(c.m) * C::BM;
   const int64_t col = int64_t(c.g) * a.n + int64_t(c.n) * C::BN;
-  op.nk = (a.kb + kStepBlocks - 1) / kStepBlocks;
-  // in units of 16 bits, 8 to a chunk
-  kcontig_operand<C>(op.ra, op.ao, op.tail_a, a.xc + row * ld, left, ld,
-                     row_span(min(left, C::BM), ld), a.kb * 8);
-  kcontig_operand<C>(op.rb, op.bo, op.tail_b, a.wc + col * ld, nleft, ld,
-                     row_span(min(nleft, C::BN), ld), a.kb * 8);
+  op.nk = (a.kb + kChunks - 1) / kChunks;
+  op.ra = rsrc4(a.xc + row * ld, static_cast<uint32_t>(left) * ld);
+  op.rb = rsrc4(a.wc + col * ld, static_cast<uint32_t>(nleft) * ld);
+  const int r0 = threadIdx.x / kChunks, chunk = position(r0, threadIdx.x % kChunks);
+#pragma unroll
+  for (int p = 0; p < C::A_LOADS; ++p) {
+    const int r = r0 + p * C::RPP;
+    op.ao[p] = (r < left ? static_cast<uint32_t>(r) * ld : kInvalidRow) + chunk * 16u;
+  }
+#pragma unroll
+  for (int p = 0; p < C::B_LOADS; ++p) {
+    const int r = r0 + p * C::RPP;
+    op.bo[p] = (r < nleft ? static_cast<uint32_t>(r) * ld : kInvalidRow) + chunk * 16u;
+  }
+  op.tail = (op.nk - 1) * kChunks + chunk < a.kb ? 0u : kInvalidRow;
   // Scales past the last word of a row read as zeros: a group's own words end the
   // resource, so that no other group's bytes (a NaN) meet the zero codes there.
   // Rows past the operand's read other rows' words; their outputs are not stored.
-  const i32x4_t rsa = rsrc4(a.xs, static_cast<uint32_t>(a.kg) * static_cast<uint32_t>(a.rows) * 4u);
-  const i32x4_t rsb = rsrc4(a.ws + int64_t(c.g) * a.kg * a.n * 4,
-                            static_cast<uint32_t>(a.kg) * static_cast<uint32_t>(a.n) * 4u);
+  const uint32_t pa = static_cast<uint32_t>(a.rows) * 4u, pb = static_cast<uint32_t>(a.n) * 4u;
+  const i32x4_t rsa = rsrc4(a.xs, static_cast<uint32_t>(a.kg) * pa);
+  const i32x4_t rsb = rsrc4(a.ws + int64_t(c.g) * a.kg * a.n * 4, static_cast<uint32_t>(a.kg) * pb);
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int j = 0; j < S::LOADS; ++j) {
-    const int piece = j * C::NWAVES + wave;
-    const bool is_a = piece * 64 < 2 * C::BM;
-    const int i = piece * 64 + lane - (is_a ? 0 : 2 * C::BM);
-    const int width = is_a ? C::BM : C::BN;
-    const uint32_t half = static_cast<uint32_t>(i / width), r = static_cast<uint32_t>(i % width);
-    const uint32_t plane = static_cast<uint32_t>(is_a ? a.rows : a.n) * 4u;
-    const uint32_t r0 = static_cast<uint32_t>(is_a ? row : int64_t(c.n) * C::BN);
-    op.rs[j] = is_a ? rsa : rsb;
-    op.so[j] = piece < S::PIECES ? half * plane + (r0 + r) * 4u : kInvalidRow;
-    op.sstep[j] = 2u * plane;
+  // first word of this lane's four of an operand's, `w` waves with `lanes` of them
+  auto word = [&](int w, int lanes, int width, uint32_t plane, uint32_t first) {
+    const int i = (w * lanes + min(lane, lanes - 1)) * 4;
+    return static_cast<uint32_t>(i / width) * plane +
+           (first + static_cast<uint32_t>(i % width)) * 4u;
+  };
+  const uint32_t fa = static_cast<uint32_t>(row), fb = static_cast<uint32_t>(c.n) * C::BN;
+  if constexpr (C::SHARED) {
+    const bool is_a = wave < C::NWAVES / 2;
+    op.rs[0] = is_a ? rsa : rsb;
+    op.so[0] = is_a ? word(wave, C::A_LANES, C::BM, pa, fa)
+                    : word(wave - C::NWAVES / 2, C::B_LANES, C::BN, pb, fb);
+    op.sstep[0] = 2u * (is_a ? pa : pb);
+  } else {
+    op.rs[0] = rsa;
+    op.so[0] = word(wave, C::A_LANES, C::BM, pa, fa);
+    op.sstep[0] = 2u * pa;
+    op.rs[C::S_LOADS - 1] = rsb;
+    op.so[C::S_LOADS - 1] = word(wave, C::B_LANES, C::BN, pb, fb);
+    op.sstep[C::S_LOADS - 1] = 2u * pb;
   }
 }
 
@@ -122,41 +165,38 @@ __device__ __forceinline__ void tile_ops(const MArgs& a, const MTile& c, int wav
 // loads that step again into stages nobody reads.
 template <class C, class NextOps>
 struct MLoader {
-  using S = Scales<C>;
   MOps<C> op;
   NextOps& next_ops;
-  uint32_t lds0, sc0;
+  uint32_t lds0;
   int ti, nb, total, ki, wave;
   bool more;
-  static constexpr int NL = C::A_LOADS + C::B_LOADS + S::LOADS;
 
-  __device__ MLoader(NextOps& n, uint32_t l0, uint32_t s0, int first, int nb_, int total_,
-                     int wave_)
-      : next_ops(n), lds0(l0), sc0(s0), ti(first), nb(nb_), total(total_), ki(0), wave(wave_),
-        more(true) {
+  __device__ MLoader(NextOps& n, uint32_t l0, int first, int nb_, int total_, int wave_)
+      : next_ops(n), lds0(l0), ti(first), nb(nb_), total(total_), ki(0), wave(wave_), more(true) {
     next_ops(ti, op);
   }
   // load i of NL of the current k-step into stage st
   __device__ __forceinline__ void load(int st, int i) {
-    const uint32_t base =
-        __builtin_amdgcn_readfirstlane(lds0 + (st * C::STAGE + wave * 8 * BK) * 2);
-    const uint32_t kn = static_cast<uint32_t>(ki) * (BK * 2);
-    const bool last = ki == op.nk - 1;
+    const uint32_t stage = lds0 + st * C::STAGE;
+    const uint32_t base = __builtin_amdgcn_readfirstlane(stage + wave * 1024);
+    const uint32_t kn = static_cast<uint32_t>(ki) * kRow;
+    const uint32_t tail = ki == op.nk - 1 ? op.tail : 0u;
     if (i < C::A_LOADS) {
-      dma16(op.ra, (op.ao[i] + kn) | (last ? op.tail_a : 0u), base + i * C::RPP * BK * 2);
+      dma16(op.ra, (op.ao[i] + kn) | tail, base + i * C::RPP * kRow);
     } else if (i < C::A_LOADS + C::B_LOADS) {
       const int j = i - C::A_LOADS;
-      const uint32_t v = (op.bo[j] + kn) | (last ? op.tail_b : 0u);
-      const uint32_t at = base + C::BM * BK * 2 + j * C::RPP * BK * 2;
+      const uint32_t at = base + (C::BM + j * C::RPP) * kRow;
       if constexpr (C::B_NT)
-        dma16_nt(op.rb, v, at);
+        dma16_nt(op.rb, (op.bo[j] + kn) | tail, at);
       else
-        dma16(op.rb, v, at);
+        dma16(op.rb, (op.bo[j] + kn) | tail, at);
     } else {
       const int j = i - C::A_LOADS - C::B_LOADS;
-      const uint32_t at = __builtin_amdgcn_readfirstlane(
-          sc0 + (st * S::STAGE + (j * C::NWAVES + wave) * 64) * 4);
-      dma4(op.rs[j], op.so[j] + static_cast<uint32_t>(ki) * op.sstep[j], at);
+      const uint32_t v = op.so[j] + static_cast<uint32_t>(ki) * op.sstep[j];
+      const int lanes = j == 0 ? C::A_LANES : C::B_LANES;
+      const uint32_t at = stage + C::CODES + wave * lanes * 16 + (j == 0 ? 0 : C::A_WORDS * 4);
+      if (static_cast<int>(threadIdx.x & 63) < lanes)
+        dma16(op.rs[j], v, __builtin_amdgcn_readfirstlane(at));
     }
   }
   __device__ __forceinline__ void advance() {
@@ -172,18 +212,21 @@ struct MLoader {
   }
 };
 
-// 16 bytes (one block) of row l % 32 for sub-step kk: chunk 4 (l / 32) + kk.
+// 16 bytes (one block) of row l % 32 for sub-step kk: chunk SUBS (l / 32) + kk.
 template <class C>
-__device__ __forceinline__ i32x4_t block_of(const uint16_t* lds, int st, bool b, int row, int kk,
+__device__ __forceinline__ i32x4_t block_of(const uint8_t* stage, bool b, int row, int kk,
                                             int lane) {
-  const uint16_t* s = lds + st * C::STAGE + (b ? C::BM * BK : 0);
-  return *reinterpret_cast<const i32x4_t*>(s + lds_off(row + (lane & 31), 4 * (lane >> 5) + kk));
+  const int r = row + (lane & 31), chunk = kSubs * (lane >> 5) + kk;
+  return *reinterpret_cast<const i32x4_t*>(stage + (b ? C::BM * kRow : 0) + r * kRow +
+                                           position(r, chunk) * 16);
 }
-// Scale word of row l % 32 for the lane's half of the step.
+// Scale bytes of row l % 32 for the lane's half of the step, sub-step kk's in byte kk.
 template <class C>
-__device__ __forceinline__ int word_of(const uint32_t* sc, int st, bool b, int row, int lane) {
-  const uint32_t* s = sc + st * Scales<C>::STAGE + (b ? 2 * C::BM : 0);
-  return static_cast<int>(s[(lane >> 5) * (b ? C::BN : C::BM) + row + (lane & 31)]);
+__device__ __forceinline__ int word_of(const uint8_t* stage, bool b, int row, int lane) {
+  const uint32_t* s =
+      reinterpret_cast<const uint32_t*>(stage + C::CODES) + (b ? C::A_WORDS : 0);
+  const int r = row + (lane & 31), h = lane >> 5;
+  return static_cast<int>(s[h * (b ? C::BN : C::BM) + r]);
 }
 
 // c + b a with sub-step KK's bytes of the scale words; the W operand goes first,
@@ -195,10 +238,11 @@ __device__ __forceinline__ f32x16_t mma4(i32x4_t a, i32x4_t b, f32x16_t c, int s
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(B, A, c, kFp4, kFp4, KK, sb, KK, sa);
 }
 
-// Stores eight adjacent values of a row, of which `cnt` exist.
-__device__ __forceinline__ void put8(const MArgs& a, int64_t at, int cnt, const uint32_t (&w)[4]) {
-  uint16_t* p = static_cast<uint16_t*>(a.y) + at;
-  if (a.vec && cnt >= 8) {
+// Stores eight adjacent values of a row, of which `cnt` exist; all of them, in whole
+// 16-byte accesses, where FULL.
+template <bool FULL>
+__device__ __forceinline__ void put8(uint16_t* p, bool vec, int cnt, const uint32_t (&w)[4]) {
+  if (FULL || (vec && cnt >= 8)) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
@@ -206,9 +250,9 @@ __device__ __forceinline__ void put8(const MArgs& a, int64_t at, int cnt, const 
       if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
   }
 }
-__device__ __forceinline__ void put4(const MArgs& a, int64_t at, int cnt, const float (&v)[4]) {
-  float* p = static_cast<float*>(a.y) + at;
-  if (a.vec && cnt >= 4) {
+template <bool FULL>
+__device__ __forceinline__ void put4(float* p, bool vec, int cnt, const float (&v)[4]) {
+  if (FULL || (vec && cnt >= 4)) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
@@ -217,12 +261,11 @@ __device__ __forceinline__ void put4(const MArgs& a, int64_t at, int cnt, const 
   }
 }
 
-// Output of a finished tile, straight from registers, so that no barrier holds the
-// other waves: a lane has columns 8 g + 4 h .. + 3 (g = 0 .. 3, h its half) of row l %
-// 32. For bf16 the halves swap words, which leaves each lane 8 adjacent columns of
-// its row, 16 bytes.
-template <class C>
-__device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int wm, int wn, int lane,
+// A lane has columns 8 g + 4 h .. + 3 (g = 0 .. 3, h its half) of row l % 32. For bf16
+// the halves swap words, which leaves each lane 8 adjacent columns of its row, 16
+// bytes. FULL: every row and column exists.
+template <class C, bool FULL>
+__device__ __forceinline__ void store_part(const MArgs& a, const MTile& c, int wm, int wn, int lane,
                                            const f32x16_t (&acc)[C::MI][C::NJ]) {
   const int h = lane >> 5;
 #pragma unroll
@@ -238,7 +281,8 @@ __device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int w
         for (int g = 0; g < 4; ++g) {
           const int col = col0 + 8 * g + 4 * h;
           const float v[4] = {x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
-          if (r < c.rows && col < a.n) put4(a, row + col, a.n - col, v);
+          if (FULL || (r < c.rows && col < a.n))
+            put4<FULL>(static_cast<float*>(a.y) + row + col, a.vec, a.n - col, v);
         }
       } else {
 #pragma unroll
@@ -253,44 +297,59 @@ __device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int w
             w[2 + j] = s[1];
           }
           const int col = col0 + 16 * q + 8 * h;
-          if (r < c.rows && col < a.n) put8(a, row + col, a.n - col, w);
+          if (FULL || (r < c.rows && col < a.n))
+            put8<FULL>(static_cast<uint16_t*>(a.y) + row + col, a.vec, a.n - col, w);
         }
       }
     }
   }
 }
+// Output of a finished tile, straight from registers, so that no barrier holds the
+// other waves.
+template <class C>
+__device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int wm, int wn, int lane,
+                                           const f32x16_t (&acc)[C::MI][C::NJ]) {
+  if (a.vec && c.m * C::BM + (wm + 1) * C::WM <= c.rows && c.n * C::BN + (wn + 1) * C::WN <= a.n)
+    store_part<C, true>(a, c, wm, wn, lane, acc);
+  else
+    store_part<C, false>(a, c, wm, wn, lane, acc);
+}
 
 // The k-loop: NST stages; the blocks of sub-step kk + 1 are read between the matrix
 // instructions of sub-step kk. One barrier per k-step, before its last sub-step,
-// whose blocks are already in registers: behind it the step's stage is free and is
-// loaded with step k + NST at once, and step k + 1's loads, NST - 1 steps old, have
-// landed. Waves are in step only there, so the two waves of a SIMD fill each
+// whose blocks are already in registers: behind it the step's stage is free for step
+// k + NST, whose loads go out over the next four sub-steps (with two stages all in
+// the first of them, since they are waited for after four), and step k + 1's loads
+// have landed. Waves are in step only there, so the two waves of a SIMD fill each
 // other's gaps, and a wave that stores its tile holds no other up.
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
 template <class C, class NextOps, class Epilogue>
-__device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first, int nb, int total,
+__device__ __forceinline__ void mx4_ring(uint8_t* lds, int first, int nb, int total,
                                          NextOps&& next_ops, Epilogue&& epilogue) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  using L = MLoader<C, std::remove_reference_t<NextOps>>;
-  constexpr int NST = C::NST, NL = L::NL, INFLIGHT = NL * (NST - 2);
+  constexpr int NST = C::NST, NL = C::NL, INFLIGHT = NL * (NST - 2), LAST = kSubs - 1;
+  // sub-steps over which a step's loads are spread
+  constexpr int SLOTS = NST > 2 ? kSubs : 1;
   constexpr int NR = C::MI + C::NJ, NM = C::MI * C::NJ;
-  static_assert(INFLIGHT <= 63, "vmcnt range");
-  L ld(next_ops, lds_addr(lds), lds_addr(sc), first, nb, total, wave);
+  MLoader<C, std::remove_reference_t<NextOps>> ld(next_ops, lds_addr(lds), first, nb, total, wave);
   i32x4_t af[2][C::MI], bf[2][C::NJ];
   int sa[C::MI], sb[C::NJ], na[C::MI], nbs[C::NJ];
   f32x16_t acc[C::MI][C::NJ];
   auto rd = [&](int st, int kk, int buf, int i) {
+    const uint8_t* s = lds + st * C::STAGE;
     if (i < C::NJ)
-      bf[buf][i] = block_of<C>(lds, st, true, wn * C::WN + i * 32, kk, lane);
+      bf[buf][i] = block_of<C>(s, true, wn * C::WN + i * 32, kk, lane);
     else
-      af[buf][i - C::NJ] = block_of<C>(lds, st, false, wm * C::WM + (i - C::NJ) * 32, kk, lane);
+      af[buf][i - C::NJ] = block_of<C>(s, false, wm * C::WM + (i - C::NJ) * 32, kk, lane);
   };
   auto rd_scales = [&](int st) {
+    const uint8_t* s = lds + st * C::STAGE;
 #pragma unroll
-    for (int i = 0; i < C::MI; ++i) na[i] = word_of<C>(sc, st, false, wm * C::WM + i * 32, lane);
+    for (int i = 0; i < C::MI; ++i) na[i] = word_of<C>(s, false, wm * C::WM + i * 32, lane);
 #pragma unroll
-    for (int i = 0; i < C::NJ; ++i) nbs[i] = word_of<C>(sc, st, true, wn * C::WN + i * 32, lane);
+    for (int i = 0; i < C::NJ; ++i) nbs[i] = word_of<C>(s, true, wn * C::WN + i * 32, lane);
   };
   auto use_scales = [&] {
 #pragma unroll
@@ -299,8 +358,10 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first,
     for (int i = 0; i < C::NJ; ++i) sb[i] = nbs[i];
   };
   auto sub = [&](auto kk_c, int st_rd, int st_dma) {
-    constexpr int KK = decltype(kk_c)::value, buf = KK & 1;
-    constexpr int RPS = (NR + NM - 1) / NM, LPS = (NL + NM - 1) / NM;
+    constexpr int KK = decltype(kk_c)::value, buf = KK & 1, next = KK == LAST ? 0 : KK + 1;
+    constexpr int RPS = (NR + NM - 1) / NM;
+    constexpr int SLOT = KK == LAST ? 0 : KK + 1, L0 = min_of(NL * SLOT / SLOTS, NL),
+                  L1 = min_of(NL * (SLOT + 1) / SLOTS, NL);
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
       const int mi = i / C::NJ, nj = i % C::NJ;
@@ -310,22 +371,20 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first,
       asm volatile("" : "+v"(acc[mi][nj]));
 #pragma unroll
       for (int q = 0; q < RPS; ++q)
-        if (i * RPS + q < NR) rd(st_rd, (KK + 1) & 3, buf ^ 1, i * RPS + q);
-      if constexpr (KK == 3) {
+        if (i * RPS + q < NR) rd(st_rd, next, buf ^ 1, i * RPS + q);
 #pragma unroll
-        for (int q = 0; q < LPS; ++q)
-          if (i * LPS + q < NL) ld.load(st_dma, i * LPS + q);
-      }
+      for (int l = L0; l < L1; ++l)
+        if ((l - L0) * NM / (L1 - L0) == i) ld.load(st_dma, l);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 #pragma unroll
   for (int j = 0; j < NST; ++j) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) ld.load(j, i);
-    ld.advance();
+    for (int i = 0; i < (j < NST - 1 ? NL : NL / SLOTS); ++i) ld.load(j, i);
+    if (j < NST - 1) ld.advance();
   }
-  vm_wait<(INFLIGHT + NL < 63 ? INFLIGHT + NL : 63)>();
+  vm_wait<INFLIGHT>();
   lds_barrier();
   int st = 0;
 #pragma unroll
@@ -335,16 +394,16 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first,
     zero_acc<C>(acc);
     const int nkc = epilogue.k_steps();
     for (int kc = 0; kc < nkc; ++kc) {
-      const int next = st == NST - 1 ? 0 : st + 1;
+      const int next = st == NST - 1 ? 0 : st + 1, last = st == 0 ? NST - 1 : st - 1;
       use_scales();
-      sub(std::integral_constant<int, 0>{}, st, 0);
-      sub(std::integral_constant<int, 1>{}, st, 0);
-      sub(std::integral_constant<int, 2>{}, st, 0);
+      sub(std::integral_constant<int, 0>{}, st, last);
+      sub(std::integral_constant<int, 1>{}, st, last);
+      sub(std::integral_constant<int, 2>{}, st, last);
+      ld.advance();
       vm_wait<INFLIGHT>();
       lds_barrier();
       rd_scales(next);
-      sub(std::integral_constant<int, 3>{}, next, st);
-      ld.advance();
+      sub(std::integral_constant<int, LAST>{}, next, st);
       st = next;
     }
     epilogue(tc, wm, wn, lane, acc);
@@ -352,10 +411,13 @@ __device__ __forceinline__ void mx4_ring(uint16_t* lds, uint32_t* sc, int first,
   vm_wait<0>();
 }
 
+// waves per SIMD the register budget is sized for
 template <class C>
-__global__ __launch_bounds__(C::NT, C::MINW) void mx4_gemm_kernel(MArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[C::LDS_ELEMS];
-  __shared__ uint32_t sc[C::NST * Scales<C>::STAGE];
+constexpr int kMinWaves = C::NWAVES >= 8 ? 2 : 1;
+
+template <class C>
+__global__ __launch_bounds__(C::NT, kMinWaves<C>) void mx4_gemm_kernel(MArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::NST * C::STAGE];
   __shared__ GroupTables gt;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, (a.n + C::BN - 1) / C::BN);
   const int total = gt.total, nb = gridDim.x;
@@ -366,20 +428,21 @@ __global__ __launch_bounds__(C::NT, C::MINW) void mx4_gemm_kernel(MArgs a) {
   struct Epilogue {
     const MArgs& a;
     const GroupTables& t;
-    __device__ int k_steps() const { return (a.kb + kStepBlocks - 1) / kStepBlocks; }
+    __device__ int k_steps() const { return (a.kb + kChunks - 1) / kChunks; }
     __device__ void operator()(int tile, int wm, int wn, int lane,
                                const f32x16_t (&acc)[C::MI][C::NJ]) const {
       store_tile<C>(a, tile_of<C>(a, t, tile), wm, wn, lane, acc);
     }
   } ep{a, gt};
-  mx4_ring<C>(lds, sc, first, nb, total, next_ops, ep);
+  mx4_ring<C>(lds, first, nb, total, next_ops, ep);
 }
 
 // ---- choice of the kernel -------------------------------------------------------
 
-using TileBig = Tile<256, 256, 128, 64, 2>;      // 8 waves
-using TileMid = Tile<128, 128, 64, 32, 3>;       // 8 waves
-using TileDec = Tile<32, 128, 32, 64, 6, true>;  // 2 waves, weights streamed past L2
+using TileBig = MxTile<256, 256, 128, 64, 2>;      // 8 waves
+using TileWide = MxTile<128, 256, 64, 64, 3>;      // 8 waves
+using TileFlat = MxTile<64, 256, 32, 64, 3>;       // 8 waves
+using TileLow = MxTile<32, 128, 32, 32, 6, true>;  // 4 waves, weights streamed past L2
 
 template <class C>
 int64_t tile_bound(const MArgs& a) {
@@ -401,14 +464,15 @@ struct TileCost {
   double busy, idle, fixed;
 };
 constexpr TileCost kCosts[] = {
-    {256, 256, 1.7, 1.05, 8.0}, {128, 128, 0.65, 0.38, 4.0}, {32, 128, 0.6, 0.35, 3.0}};
+    {256, 256, 1.76, 1.22, 7.0}, {128, 256, 1.0, 0.6, 3.5}, {64, 256, 0.85, 0.36, 1.5},
+    {32, 128, 0.34, 0.21, 0.8}};
 
 int choose(const MArgs& a) {
   const double touched = static_cast<double>(a.rows < a.G ? a.rows : a.G);
-  const double nk = (a.kb + kStepBlocks - 1) / kStepBlocks;
+  const double nk = (a.kb + 7) / 8;
   int best = 0;
   double least = 0.0;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const TileCost& t = kCosts[i];
     const double mt = a.G == 1 ? std::ceil(a.rows / static_cast<double>(t.bm))
                                : a.rows / static_cast<double>(t.bm) + 0.5 * touched;
@@ -447,9 +511,11 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& p, hipStream_t s) {
   if (c == 0)
     launch<TileBig>(a, s);
   else if (c == 1)
-    launch<TileMid>(a, s);
+    launch<TileWide>(a, s);
+  else if (c == 2)
+    launch<TileFlat>(a, s);
   else
-    launch<TileDec>(a, s);
+    launch<TileLow>(a, s);
   return hipGetLastError();
 }
 
