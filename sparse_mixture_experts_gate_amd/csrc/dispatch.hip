@@ -203,38 +203,54 @@ __global__ __launch_bounds__(kChunk) void rank_kernel(const int32_t* idx, int64_
 }
 
 // Second launch, one block: the chunks' counts become the places of their first
-// pairs. Threads of a column (expert) take a run of the chunks each.
+// pairs. Threads of a column (expert) take a run of PER chunks each, whose counts stay
+// in registers (PER 0: runs of any length, read twice).
+template <int PER>
 __global__ __launch_bounds__(1024) void scan_kernel(int32_t* count, int chunks, int E, int cols,
                                                     int64_t rows, int32_t* offsets) {
   __shared__ int32_t part[1024];
-  __shared__ int32_t first[kMaxExperts + 1];
+  __shared__ __attribute__((aligned(16))) int32_t first[kMaxExperts + 4];
   const int tid = threadIdx.x, runs = 1024 / cols;  // cols: a power of two, at least E
   const int e = tid & (cols - 1), run = tid / cols;
-  const int per = (chunks + runs - 1) / runs, c0 = min(run * per, chunks),
-            c1 = min(c0 + per, chunks);
-  // eight loads in flight: a chunk of a run waits for no store of an earlier one
-  auto walk = [&](auto&& visit) {
-    for (int c = c0; c < c1; c += 8) {
-      int32_t n[8];
+  const int per = PER ? PER : (chunks + runs - 1) / runs, c0 = min(run * per, chunks),
+            c1 = e < E ? min(c0 + per, chunks) : 0;
+  int32_t* col = count + e;
+  constexpr int N = PER ? PER : 8;  // loads in flight
+  int32_t n[N];
+  auto read = [&](int c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = c + i < c1 ? count[int64_t(c + i) * E + e] : 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < c1) visit(c + i, n[i]);
-    }
+    for (int i = 0; i < N; ++i) n[i] = c + i < c1 ? col[int64_t(c + i) * E] : 0;
   };
   int sum = 0;
-  if (e < E) walk([&](int, int n) { sum += n; });
+  for (int c = c0; c < (PER ? c0 + 1 : c1); c += N) {
+    read(c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += n[i];
+  }
   part[tid] = sum;
+  if (tid < kMaxExperts) first[tid] = 0;
   __syncthreads();
-  if (tid < 64) {  // experts' totals and their scan, eight experts per lane
-    int c[8], all = 0;
+  int at = 0;  // pairs of this expert in the runs before this thread's
+  if (e < E) {
+    int all = 0;
+#pragma unroll 4
+    for (int r = 0; r < runs; ++r) {
+      const int v = part[r * cols + e];
+      at += r < run ? v : 0;
+      all += v;
+    }
+    if (run == 0) first[e] = all;
+  }
+  __syncthreads();
+  if (tid < 64) {  // scan of the experts' pairs, eight experts per lane
+    int4 lo = reinterpret_cast<const int4*>(first)[2 * tid];
+    int4 hi = reinterpret_cast<const int4*>(first)[2 * tid + 1];
+    const int v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    int all = 0, c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int x = 8 * tid + j;
       c[j] = all;
-      if (x < E)
-        for (int r = 0; r < runs; ++r) all += part[r * cols + x];
+      all += v[j];
     }
     int p = all;
 #pragma unroll
@@ -242,23 +258,25 @@ __global__ __launch_bounds__(1024) void scan_kernel(int32_t* count, int chunks, 
       const int o = __shfl_up(p, s, 64);
       if (tid >= s) p += o;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (8 * tid + j <= E) first[8 * tid + j] = p - all + c[j];
-    if (tid == 63 && E == kMaxExperts) first[E] = p;
+    p -= all;
+    reinterpret_cast<int4*>(first)[2 * tid] = make_int4(p + c[0], p + c[1], p + c[2], p + c[3]);
+    reinterpret_cast<int4*>(first)[2 * tid + 1] = make_int4(p + c[4], p + c[5], p + c[6], p + c[7]);
+    if (tid == 63) first[kMaxExperts] = p + all;
   }
   __syncthreads();
-  if (run == 0 && e < E) {
-    offsets[e] = static_cast<int32_t>(min(int64_t(first[e]), rows));
-    if (e == E - 1) offsets[E] = static_cast<int32_t>(min(int64_t(first[E]), rows));
-  }
+  for (int i = tid; i <= E; i += 1024)
+    offsets[i] = static_cast<int32_t>(min(int64_t(first[i]), rows));
   if (e >= E) return;
-  int at = first[e];
-  for (int r = 0; r < run; ++r) at += part[r * cols + e];
-  walk([&](int c, int n) {
-    count[int64_t(c) * E + e] = at;
-    at += n;
-  });
+  at += first[e];
+  for (int c = c0; c < (PER ? c0 + 1 : c1); c += N) {
+    if (!PER) read(c);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < c1) {
+        col[int64_t(c + i) * E] = at;
+        at += n[i];
+      }
+  }
 }
 
 // Third launch: a group of LANES lanes per token.
@@ -361,8 +379,17 @@ hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s) {
   while (cols < p.E) cols *= 2;
   hipLaunchKernelGGL(rank_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kChunk), 0, s, p.idx,
                      pairs, p.E, count, rank);
-  hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(1024), 0, s, count, static_cast<int>(chunks), p.E,
-                     cols, p.rows, p.offsets);
+  const int runs = 1024 / cols;
+  auto scan = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, s, count, static_cast<int>(chunks), p.E, cols,
+                       p.rows, p.offsets);
+  };
+  if (chunks <= 4 * runs)
+    scan(scan_kernel<4>);
+  else if (chunks <= 16 * runs)
+    scan(scan_kernel<16>);
+  else
+    scan(scan_kernel<0>);
   if (!p.x) {
     hipLaunchKernelGGL(place_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0,
                        s, a);
