@@ -456,20 +456,39 @@ void launch(const MArgs& a, hipStream_t s) {
                      dim3(C::NT), 0, s, a);
 }
 
-// Time model of a tile (microseconds): `busy` and `idle` per k-step with the GPU
-// full or at most half full of tiles, `fixed` for a tile's first loads and its
-// output.
+// Time model of a tile (microseconds), fitted to measured products: `busy` and `idle`
+// per k-step with the GPU full or at most half full of tiles, `fixed` for a tile's
+// first loads and its output.
 struct TileCost {
   int bm, bn;
   double busy, idle, fixed;
 };
-constexpr TileCost kCosts[] = {
-    {256, 256, 1.76, 1.22, 7.0}, {128, 256, 1.0, 0.6, 3.5}, {64, 256, 0.85, 0.36, 1.5},
-    {32, 128, 0.34, 0.21, 0.8}};
+constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.22, 7.0},
+                               {128, 256, 1.0, 0.7, 3.5},
+                               {64, 256, 0.74, 0.36, 1.8},
+                               {32, 128, 0.34, 0.21, 1.0}};
 
+// The rule: the tile with the least modelled time. Row counts per group live on the
+// device, so the expected number of row tiles stands in for them: at least one per
+// group with rows, else rows / BM and half a tile per group; with more than one group
+// half a round more than the tiles fill. Measured (us, 256 / 128 / 64 / 32 rows):
+//   x [16, 4096], 1 x 4096                    25 / 15 / 13 / 10
+//   x [512, 2048], 8 x 1408                   17 / 12 / 10 / 8
+//   x [1024, 7168], 1 x 4096                  47 / 30 / 26 / 48
+//   x [2048, 4096], 1 x 4096                  35 / 26 / 31 / 58
+//   x [1024, 4096], 16 x 4096                 34 / 39 / 36 / 42
+//   x [2048, 2048], 64 x 2816                 59 / 41 / 37 / 41
+//   x [4096, 7168], 32 x 4096                174 / 125 / 168 / 221
+//   x [8192, 7168], 1 x 4096                 119 / 129 / 173 / 361
+//   x [8192, 7168], 32 x 4096, Zipf loads    195 / 199 / 245 / 424
+//   x [128, 7168], 128 of 256 groups x 4096   32 rows: 276 (weights through the caches
+//                                            325), 64: 328
+// and where it is wrong, the tile it takes first:
+//   x [700, 256], 100 x 4096                  32 rows: 24, 64: 20
+//   x [24576, 2048], 64 x 2816                128 rows: 122, 256: 119
 int choose(const MArgs& a) {
   const double touched = static_cast<double>(a.rows < a.G ? a.rows : a.G);
-  const double nk = (a.kb + 7) / 8;
+  const double nk = (a.kb + kChunks - 1) / kChunks;
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < 4; ++i) {
@@ -477,8 +496,7 @@ int choose(const MArgs& a) {
     const double mt = a.G == 1 ? std::ceil(a.rows / static_cast<double>(t.bm))
                                : a.rows / static_cast<double>(t.bm) + 0.5 * touched;
     const double share = (a.n + t.bn - 1) / t.bn * (mt > touched ? mt : touched) / 256;
-    double rounds = std::ceil(share);
-    if (a.G > 1 && share > 1.0) rounds = share + 0.5;
+    const double rounds = a.G == 1 ? std::ceil(share) : share > 0.5 ? share + 0.5 : 1.0;
     const double us = rounds * (nk * (share <= 0.5 ? t.idle : t.busy) + t.fixed);
     if (i == 0 || us < least) {
       least = us;
