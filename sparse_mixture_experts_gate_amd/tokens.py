@@ -284,7 +284,9 @@ class MX4Linear:
         cs, ss = _mx4_bytes(*codes.shape[:2], k)
         _matrix(codes, "codes", torch.uint8, *cs)
         _matrix(scales, "scales", torch.uint8, *ss)
-        self.codes, self.scales, self.k = _aligned(codes), _aligned(scales), k
+        if (codes.data_ptr() | scales.data_ptr()) & 15:
+            raise ValueError("codes and scales must start on 16 bytes")
+        self.codes, self.scales, self.k = codes, scales, k
 
     @classmethod
     def from_weight(cls, weight: torch.Tensor, stream=None) -> "MX4Linear":

@@ -155,6 +155,19 @@ def test_same_expert_twice_in_a_token():
     _check_return(5, 4, 100, "f32", idx, 2, None, True, True)
 
 
+@pytest.mark.parametrize("T", [5, 3000])
+def test_selections_of_any_value(T):
+    """Everything outside 0 .. E - 1 is no expert, the type's ends among it."""
+    import sparse_mixture_experts_gate_amd as M
+    bad = np.array([-2 ** 31, 2 ** 31 - 1, -1, 4, 513, 1 << 9], np.int32)
+    idx = np.random.default_rng(T).integers(0, 4, (T, 4)).astype(np.int32)
+    idx[1::2, 1:3] = bad[np.arange(T // 2 * 2).reshape(-1, 2) % 6]
+    off, perm, inv = _place(idx, 4)
+    o = M.TokenDispatch(4).forward(None, torch.from_numpy(idx).to(DEV))
+    for k, v in (("offsets", off), ("perm", perm), ("inv", inv)):
+        assert np.array_equal(host(o[k]), v), k
+
+
 def test_bad_places_are_left_out():
     """inv outside the sorted rows reads and writes nothing."""
     import sparse_mixture_experts_gate_amd as M

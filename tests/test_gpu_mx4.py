@@ -254,3 +254,25 @@ def test_from_blocks_and_values():
     off = torch.tensor([0, 5, 5, 30], dtype=torch.int32, device=DEV)
     dx = M.GroupedLinear(ref.values()).input_grad(_rand(2, 30, 40, dt="bf16"), off)
     assert dx.shape == (30, 200) and bool(dx.isfinite().all())
+
+
+def test_no_rows():
+    import sparse_mixture_experts_gate_amd as M
+    codes, scales = M.mx4_quantize(torch.empty(0, 100, device=DEV))
+    assert codes.shape == (0, 64) and scales.shape == (1, 0, 4)
+    assert M.mx4_dequantize(codes, scales, 100).shape == (0, 100)
+    lin = M.MX4Linear.from_weight(_rand(1, 2, 30, 100))
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert lin.forward(torch.empty(0, 100, device=DEV), off).shape == (0, 30)
+    assert lin.forward(_rand(1, 5, 100), off).shape == (5, 30)  # rows of no group
+
+
+@pytest.mark.parametrize("rows,n,k", [(33, 300, 4096), (200, 130, 1408), (64, 4096, 96)])
+def test_one_row_more_or_less_changes_no_other(rows, n, k):
+    """A row's product does not depend on the rows beside it, nor on the tile."""
+    import sparse_mixture_experts_gate_amd as M
+    x, lin = _rand(1, 9000, k, dt="bf16"), M.MX4Linear.from_weight(_rand(2, 1, n, k))
+    off = lambda m: torch.tensor([0, m], dtype=torch.int32, device=DEV)
+    want = lin.forward(x, off(9000), out_dtype=torch.float32)
+    for m in (1, rows, rows + 1, 1000):
+        assert torch.equal(lin.forward(x[:m], off(m), out_dtype=torch.float32), want[:m])

@@ -218,6 +218,7 @@ def test_objects_check_shapes_and_types():
         lambda: M.mx4_dequantize(z(4, 32, dt=u8), z(1, 4, 4, dt=u8), 64, torch.float16),
         lambda: M.MX4Linear(z(2, 4, 32, dt=u8), z(2, 1, 4, 4, dt=u8), 65),
         lambda: M.MX4Linear(z(2, 4, 32), z(2, 1, 4, 4, dt=u8), 64),
+        lambda: M.MX4Linear(z(260, dt=u8)[4:].reshape(2, 4, 32), z(2, 1, 4, 4, dt=u8), 64),
         lambda: M.MX4Linear.from_blocks(z(2, 4, 32, dt=u8), z(2, 4, 3, dt=u8)),
         lambda: M.MX4Linear.from_weight(z(4, 64)),
         lambda: lin.forward(z(5, 39), off), lambda: lin.forward(z(5, 40), off.long()),
