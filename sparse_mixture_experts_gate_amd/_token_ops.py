@@ -74,9 +74,17 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def call(name: str, desc, *args) -> None:
+    """The entry point `name` with addresses and plain values, for callers that
+    have checked their tensors."""
+    status = getattr(_lib or lib(), name)(ctypes.byref(desc), *args)
+    if status:
+        L._check(status, name)
+
+
 def _size(name: str, desc) -> int:
     n = ctypes.c_size_t(0)
-    L._check(getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n)), name)
+    call(name, desc, ctypes.byref(n))
     return n.value
 
 

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
 template <class T>
 void launch(const CombineArgs& p, bool backward, hipStream_t s) {
   TokArgs a{p.yp, p.inv, p.w, p.base, p.y, p.dw, 0, p.T, p.rows, p.ldt, p.ldp, p.K, p.d, false};
-  a.stream = (backward ? p.rows : p.T) * p.d * int64_t(sizeof(T)) >= kStreamBytes;
+  a.stream = (backward ? p.rows : p.T) * p.d * int64_t(sizeof(T)) >= kFarBytes;
   const bool narrow = p.d <= 1024;  // a wave per token, at most two chunks a lane
   const int64_t per = kMaxBlocks * (narrow ? 4 : 1);
   for (int64_t t = 0; t < p.T; t += per) {

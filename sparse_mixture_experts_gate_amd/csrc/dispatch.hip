@@ -58,10 +58,13 @@ __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64
       for (int i = 0; i < CH; ++i)
         if (c0 + i * LANES < whole) {
           auto* q = reinterpret_cast<u32x4_any1_t*>(d + (c0 + i * LANES) * 16);
-          if (stream)
+          if (stream) {  // (the empty statements keep the two stores apart)
+            asm volatile("" ::: "memory");
             __builtin_nontemporal_store(v[i], q);
-          else
+            asm volatile("" ::: "memory");
+          } else {
             *q = v[i];
+          }
         }
     }
   }
@@ -363,7 +366,7 @@ hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s) {
   a.ldp = p.ldp;
   a.E = p.E;
   a.K = p.K;
-  a.stream = p.rows * p.row_bytes >= kStreamBytes;
+  a.stream = p.rows * p.row_bytes >= kFarBytes;
   if (few(p.T, p.K)) {
     hipLaunchKernelGGL(dispatch_few_kernel, dim3(static_cast<unsigned>(p.T + 1)), dim3(kFewThreads),
                        0, s, a);

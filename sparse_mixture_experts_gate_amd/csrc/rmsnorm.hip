@@ -49,7 +49,7 @@ typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(1)));
 
 // E4M3 codes of a lane's eight values of a tile; its lane 0 stores the scale.
 __device__ __forceinline__ void store_codes(const float (&o)[VEC], int cnt, uint8_t* q,
-                                            float* scale, bool first, bool stream) {
+                                            float* scale, bool first) {
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < VEC; ++j)
@@ -71,11 +71,7 @@ __device__ __forceinline__ void store_codes(const float (&o)[VEC], int cnt, uint
   }
   if (first) *scale = sc;
   if (cnt >= VEC) {
-    const u32x2_any_t v = {lo, hi};
-    if (stream)
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any_t*>(q));
-    else
-      *reinterpret_cast<u32x2_any_t*>(q) = v;
+    *reinterpret_cast<u32x2_any_t*>(q) = u32x2_any_t{lo, hi};
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
@@ -136,7 +132,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_fwd_kernel(RmsFwd
     if (a.y && cnt > 0) store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
     if (a.q)
       store_codes(o, cnt, a.q + row * a.ldq + i0, a.scale + row * a.tiles + i0 / kTile,
-                  (lane & 15) == 0, a.stream);
+                  (lane & 15) == 0);
   }
 }
 
@@ -179,7 +175,7 @@ __global__ __launch_bounds__(512) void rms_fwd_long_kernel(RmsFwdArgs a) {
     if (a.y && cnt > 0) store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
     if (a.q)
       store_codes(o, cnt, a.q + row * a.ldq + i0, a.scale + row * a.tiles + i0 / kTile,
-                  (threadIdx.x & 15) == 0, a.stream);
+                  (threadIdx.x & 15) == 0);
   }
 }
 

@@ -62,36 +62,35 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
 // The first `cnt` of eight values. `stream`: past the caches, for outputs larger
-// than the L2s together, which no reader would find there.
+// than the L2s together, which no reader would find there. The empty statements keep
+// the compiler from merging the two stores into one without the hint.
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int cnt,
                                        bool stream = false) {
   if (cnt >= VEC) {
     u32x4_any_t r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
-    if (stream)
+    if (stream) {
+      asm volatile("" ::: "memory");
       __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any_t*>(p));
-    else
+      asm volatile("" ::: "memory");
+    } else {
       *reinterpret_cast<u32x4_any_t*>(p) = r;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
       if (j < cnt) p[j] = static_cast<uint16_t>(bf16_pair(v[j], 0.0f));
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[VEC], int cnt,
-                                       bool stream = false) {
+// fp32 values leave in two stores per lane, 16 bytes of every 32 each, which the
+// caches have to join: never past them.
+__device__ __forceinline__ void store8(float* p, const float (&v)[VEC], int cnt, bool = false) {
   if (cnt >= VEC) {
     typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
     f32x4_any_t* q = reinterpret_cast<f32x4_any_t*>(p);
-    const f32x4_any_t lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-    if (stream) {
-      __builtin_nontemporal_store(lo, q);
-      __builtin_nontemporal_store(hi, q + 1);
-    } else {
-      q[0] = lo;
-      q[1] = hi;
-    }
+    q[0] = f32x4_any_t{v[0], v[1], v[2], v[3]};
+    q[1] = f32x4_any_t{v[4], v[5], v[6], v[7]};
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
@@ -137,9 +136,16 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
   return v;
 }
 
-// Row outputs of this many bytes or more are stored past the caches: eight L2s
-// of 4 MB (8192 x 7168 fp32: 122 -> 110 us; bf16 equal).
+// bf16 row outputs of this many bytes or more are stored past the caches: eight L2s
+// of 4 MB (layer norm of 8192 x 7168 with a residual 98 -> 95 us, its backward 92 ->
+// 89, 4096 x 4096 19 -> 17; fp32 rows of 8192 x 7168, in both stores, 137 -> 155).
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
+// The same for rows moved between tokens and experts, whose reader comes next and
+// finds smaller outputs in the 256 MB that the L2s share: E4M3 rows of 8192 tokens to 8
+// experts each (485 MB) 125 -> 102 us, the gradient of 4096 x 6 rows of 2048 (100 MB)
+// with the return itself 69 -> 60; a return of 58 MB 32 -> 35, a dispatch of 69 MB 22
+// -> 27.
+constexpr int64_t kFarBytes = int64_t(96) << 20;
 
 // Blocks of one launch: its work items, up to 512 a block, are counted in 32
 // bits and wrap around silently. More rows take further launches.

@@ -7,9 +7,14 @@ import torch
 
 from . import _lib as L
 from . import _token_ops as T
+from ._ops import _stream
 from .blocks import _DT, _aligned, _on, _on_gpu, _rows, _vector, _Workspace
 
 _ACT = {None: T.MOE_MX4_PLAIN, "swiglu": T.MOE_MX4_SWIGLU}
+
+
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _matrix(t, name: str, dtype, *shape) -> None:
@@ -34,8 +39,7 @@ class RMSNorm:
         n, d = x.shape
         if self.weight is not None and self.weight.numel() != d:
             raise ValueError(f"x: rows of {d} values, weight has {self.weight.numel()}")
-        return T.MoeRmsNormDesc(n=n, d=d, dtype=_DT[x.dtype], eps=self.eps,
-                                ld_x=_rows(x, "x", x.dtype, n, d))
+        return T.MoeRmsNormDesc(n, d, _DT[x.dtype], self.eps, _rows(x, "x", x.dtype, n, d))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, rows: bool = True,
                 codes: bool = False, stream=None) -> dict:
@@ -56,7 +60,8 @@ class RMSNorm:
             total = x.new_empty(n, d) if residual is not None else None
             rstd = x.new_empty(n, dtype=torch.float32)
             weight = _aligned(self.weight)
-        T.moe_rmsnorm_forward(desc, x, residual, weight, y, q, scale, total, rstd, stream)
+        T.call("moe_rmsnorm_forward", desc, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(y),
+               _ptr(q), _ptr(scale), _ptr(total), rstd.data_ptr(), _stream(stream))
         return {"y": y, "codes": q, "scale": scale, "rstd": rstd,
                 "sum": x if residual is None else total}
 
@@ -77,7 +82,9 @@ class RMSNorm:
             need = T.moe_rmsnorm_backward_workspace_size(desc)
             ws = self._ws.get(need, x.device, stream) if need else None
             weight, rstd = _aligned(self.weight), _aligned(rstd)
-        T.moe_rmsnorm_backward(desc, dy, x, weight, rstd, dresidual, dx, dw, ws, stream)
+        T.call("moe_rmsnorm_backward", desc, dy.data_ptr(), x.data_ptr(), _ptr(weight),
+               rstd.data_ptr(), _ptr(dresidual), dx.data_ptr(), dw.data_ptr(), _ptr(ws), need,
+               _stream(stream))
         return {"dx": dx, "dweight": dw}
 
 
@@ -141,8 +148,9 @@ class TokenDispatch:
                 scale_into = scale.new_empty(places, tiles)
             need = T.moe_token_dispatch_workspace_size(desc)
             ws = self._ws.get(need, topk_idx.device, stream) if need else None
-        T.moe_token_dispatch(desc, topk_idx, x, scale, offsets, perm, inv, into, scale_into, ws,
-                             stream)
+        T.call("moe_token_dispatch", desc, topk_idx.data_ptr(), _ptr(x), _ptr(scale),
+               offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), _ptr(into), _ptr(scale_into),
+               _ptr(ws), need, _stream(stream))
         return {"rows": into, "scale": scale_into, "offsets": offsets, "perm": perm, "inv": inv}
 
     @staticmethod
@@ -173,7 +181,8 @@ class TokenDispatch:
         _on_gpu(stream, rows, inv, weight, base)
         with _on(stream):
             y = torch.empty(n, d, dtype=rows.dtype, device=rows.device)
-        T.moe_token_combine(desc, rows, inv, weight, base, y, stream)
+        T.call("moe_token_combine", desc, rows.data_ptr(), inv.data_ptr(), _ptr(weight),
+               _ptr(base), y.data_ptr(), _stream(stream))
         return y
 
     @staticmethod
@@ -195,8 +204,9 @@ class TokenDispatch:
                 into = torch.empty(rows.shape[0], d, dtype=dy.dtype, device=dy.device)
             dw = None if weight is None else torch.empty(inv.shape, dtype=torch.float32,
                                                          device=dy.device)
-        T.moe_token_combine_backward(desc, dy, rows if dw is not None else None, inv, weight, into,
-                                     dw, stream)
+        T.call("moe_token_combine_backward", desc, dy.data_ptr(),
+               None if dw is None else rows.data_ptr(), inv.data_ptr(), _ptr(weight),
+               into.data_ptr(), _ptr(dw), _stream(stream))
         return {"drows": into, "dweight": dw}
 
 
@@ -244,7 +254,8 @@ def mx4_quantize(x: torch.Tensor, perm: torch.Tensor | None = None, act: str | N
         codes = torch.empty(cs[-x.dim():] if x.dim() == 3 else cs[1:], dtype=torch.uint8,
                             device=x.device)
         scales = torch.empty(ss if x.dim() == 3 else ss[1:], dtype=torch.uint8, device=x.device)
-    T.moe_mx4_quantize(desc, x, perm, codes, scales, stream)
+    T.call("moe_mx4_quantize", desc, x.data_ptr(), _ptr(perm), codes.data_ptr(),
+           scales.data_ptr(), _stream(stream))
     return codes, scales
 
 
@@ -265,7 +276,8 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int, dtype=torc
     with _on(stream):
         codes, scales = _aligned(codes), _aligned(scales)
         out = torch.empty(*codes.shape[:-1], k, dtype=dtype, device=codes.device)
-    T.moe_mx4_dequantize(desc, codes, scales, out, stream)
+    T.call("moe_mx4_dequantize", desc, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+           _stream(stream))
     return out
 
 
@@ -328,7 +340,8 @@ class MX4Linear:
             y = torch.empty(rows, n, dtype=out_dtype, device=x.device)
             ws = self._ws.get(first + -(-kb // 4) * rows * 4, x.device, stream) if rows else None
         if rows:
-            codes, scales = ws[:first], ws[first:]
-            T.moe_mx4_quantize(desc, x, perm, codes, scales, stream)
-            T.moe_mx4_gemm(g, codes, scales, self.codes, self.scales, offsets, y, stream)
+            codes, at = ws.data_ptr(), _stream(stream)
+            T.call("moe_mx4_quantize", desc, x.data_ptr(), _ptr(perm), codes, codes + first, at)
+            T.call("moe_mx4_gemm", g, codes, codes + first, self.codes.data_ptr(),
+                   self.scales.data_ptr(), offsets.data_ptr(), y.data_ptr(), at)
         return y
