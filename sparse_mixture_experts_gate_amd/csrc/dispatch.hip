@@ -59,9 +59,9 @@ __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64
         if (c0 + i * LANES < whole) {
           auto* q = reinterpret_cast<u32x4_any1_t*>(d + (c0 + i * LANES) * 16);
           if (stream) {  // (the empty statements keep the two stores apart)
-            asm volatile("" ::: "memory");
+            asm volatile("");
             __builtin_nontemporal_store(v[i], q);
-            asm volatile("" ::: "memory");
+            asm volatile("");
           } else {
             *q = v[i];
           }

@@ -27,8 +27,9 @@ struct QArgs {
   uint8_t* scales;
   void* dst;
   int64_t rows, ld, n_src, mat;  // mat: values between matrices
-  int64_t row_blocks, blk0;      // blocks of a matrix's rows; this launch's first
-  int k, kb, kg, spans;
+  // blocks of a matrix's rows; this launch's first (rows < 2^31: both in 32 bits); spans
+  uint32_t row_blocks, rb0, spans;
+  int k, kb, kg;
   bool stream;  // the output past the caches
 };
 
@@ -40,10 +41,10 @@ struct Block {
   int64_t mat, rows;
   int span;
   __device__ __forceinline__ explicit Block(const QArgs& a) {
-    const int64_t blk = a.blk0 + blockIdx.x, rb = blk / a.spans;
-    span = static_cast<int>(blk - rb * a.spans);
-    mat = rb / a.row_blocks;
-    rows = rb - mat * a.row_blocks;
+    const uint32_t q = blockIdx.x / a.spans, rb = a.rb0 + q, m = rb / a.row_blocks;
+    span = static_cast<int>(blockIdx.x - q * a.spans);
+    mat = m;
+    rows = rb - m * a.row_blocks;
   }
 };
 
@@ -132,9 +133,9 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
     if (r0 + row < a.rows && i0 < a.kb * 32) {
       uint32_t* to = reinterpret_cast<uint32_t*>(codes + int64_t(row) * a.kb * 16 + i0 / 2);
       if (a.stream) {  // (the empty statements keep the two stores apart)
-        asm volatile("" ::: "memory");
+        asm volatile("");
         __builtin_nontemporal_store(w, to);
-        asm volatile("" ::: "memory");
+        asm volatile("");
       } else {
         *to = w;
       }
@@ -214,15 +215,17 @@ QArgs q_args(const Mx4Args& p) {
   return a;
 }
 
-// Blocks of `per` rows and one span, in launches that count their work items in 32
-// bits.
+// Blocks of `per` rows and one span, in launches of whole row blocks that count their
+// work items in 32 bits.
 template <class Go>
 void in_launches(QArgs a, int64_t mats, int per, Go&& go) {
-  constexpr int64_t kMost = 2 * kMaxBlocks;
-  a.row_blocks = (a.rows + per - 1) / per;
-  const int64_t total = mats * a.row_blocks * a.spans;
-  for (a.blk0 = 0; a.blk0 < total; a.blk0 += kMost)
-    go(a, dim3(static_cast<unsigned>(total - a.blk0 < kMost ? total - a.blk0 : kMost)));
+  const int64_t most = 2 * kMaxBlocks / a.spans;
+  a.row_blocks = static_cast<uint32_t>((a.rows + per - 1) / per);
+  const int64_t total = mats * a.row_blocks;
+  for (int64_t rb = 0; rb < total; rb += most) {
+    a.rb0 = static_cast<uint32_t>(rb);
+    go(a, dim3(static_cast<unsigned>((total - rb < most ? total - rb : most) * a.spans)));
+  }
 }
 
 template <class T, bool SWIGLU>

@@ -71,9 +71,9 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int c
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
     if (stream) {
-      asm volatile("" ::: "memory");
+      asm volatile("");
       __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any_t*>(p));
-      asm volatile("" ::: "memory");
+      asm volatile("");
     } else {
       *reinterpret_cast<u32x4_any_t*>(p) = r;
     }
