@@ -17,7 +17,9 @@
 // Measured equal or slower: waves in step per sub-step as in the 16-bit products'
 // large tiles (123 us; four barriers more a step), k-steps of 128 values in four
 // stages (127), loads of the lines three steps ahead into L2 (131), waves without rows
-// leaving out their matrix instructions (the same).
+// leaving out their matrix instructions (the same), the last round's tiles cut into
+// quarters (the same), operands through registers three steps ahead into two stages
+// (128 rows a tile, Zipf loads over 32 groups: 226 against 199).
 #include <cmath>
 
 #include "device_common.h"
@@ -456,17 +458,18 @@ void launch(const MArgs& a, hipStream_t s) {
                      dim3(C::NT), 0, s, a);
 }
 
-// Time model of a tile (microseconds), fitted to measured products: `busy` and `idle`
-// per k-step with the GPU full or at most half full of tiles, `fixed` for a tile's
-// first loads and its output.
+// Time model of a tile (microseconds), fitted to measured products, per k-step: `one`
+// and `many` with the GPU full of tiles of one group, or of more, whose weights come
+// from memory; `idle` with it at most half full; `fixed` for a tile's first loads and
+// its output.
 struct TileCost {
   int bm, bn;
-  double busy, idle, fixed;
+  double one, many, idle, fixed;
 };
-constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.22, 7.0},
-                               {128, 256, 1.0, 0.7, 3.5},
-                               {64, 256, 0.74, 0.36, 1.8},
-                               {32, 128, 0.34, 0.21, 1.0}};
+constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.76, 1.22, 7.0},
+                               {128, 256, 0.97, 1.15, 0.7, 3.5},
+                               {64, 256, 0.7, 0.95, 0.36, 1.8},
+                               {32, 128, 0.34, 0.38, 0.21, 1.1}};
 
 // The rule: the tile with the least modelled time. Row counts per group live on the
 // device, so the expected number of row tiles stands in for them: at least one per
@@ -481,11 +484,11 @@ constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.22, 7.0},
 //   x [4096, 7168], 32 x 4096                174 / 125 / 168 / 221
 //   x [8192, 7168], 1 x 4096                 119 / 129 / 173 / 361
 //   x [8192, 7168], 32 x 4096, Zipf loads    195 / 199 / 245 / 424
+//   x [24576, 2048], 64 x 2816               119 / 122 / 158 / 271
 //   x [128, 7168], 128 of 256 groups x 4096   32 rows: 276 (weights through the caches
 //                                            325), 64: 328
 // and where it is wrong, the tile it takes first:
-//   x [700, 256], 100 x 4096                  32 rows: 24, 64: 20
-//   x [24576, 2048], 64 x 2816                128 rows: 122, 256: 119
+//   x [2048, 7168], 32 x 4096                 128 rows: 124, 64: 109
 int choose(const MArgs& a) {
   const double touched = static_cast<double>(a.rows < a.G ? a.rows : a.G);
   const double nk = (a.kb + kChunks - 1) / kChunks;
@@ -497,7 +500,8 @@ int choose(const MArgs& a) {
                                : a.rows / static_cast<double>(t.bm) + 0.5 * touched;
     const double share = (a.n + t.bn - 1) / t.bn * (mt > touched ? mt : touched) / 256;
     const double rounds = a.G == 1 ? std::ceil(share) : share > 0.5 ? share + 0.5 : 1.0;
-    const double us = rounds * (nk * (share <= 0.5 ? t.idle : t.busy) + t.fixed);
+    const double step = share <= 0.5 ? t.idle : a.G == 1 ? t.one : t.many;
+    const double us = rounds * (nk * step + t.fixed);
     if (i == 0 || us < least) {
       least = us;
       best = i;
