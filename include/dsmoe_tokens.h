@@ -184,11 +184,13 @@ typedef struct moe_mx4_desc {
 
 /* src [n_mats, rows, k] (gate | up: 2 k); perm NULL, or [rows] int32 with n_mats
  * == 1: row r is src[perm[r]], zeros for perm outside 0 .. n_src - 1 (the sorted
- * rows of moe_token_dispatch, quantized without writing them first). */
+ * rows of moe_token_dispatch, quantized without writing them first); src may be NULL
+ * with n_src == 0. */
 moe_status moe_mx4_quantize(const moe_mx4_desc* desc, const void* src, const int32_t* perm,
                             uint8_t* codes, uint8_t* scales, hipStream_t stream);
 
-/* dst [n_mats, rows, k]: the values of codes and scales, exact in bf16 and fp32. */
+/* dst [n_mats, rows, k]: the values of codes and scales, exact in bf16 and fp32
+ * (infinity past their range: magnitudes of 2^128 and more). */
 moe_status moe_mx4_dequantize(const moe_mx4_desc* desc, const uint8_t* codes,
                               const uint8_t* scales, void* dst, hipStream_t stream);
 

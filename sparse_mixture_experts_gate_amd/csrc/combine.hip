@@ -89,10 +89,48 @@ __global__ __launch_bounds__(256) void token_combine_kernel(TokArgs a) {
   }
 }
 
-// dy's row stays in registers, CH chunks per lane; longer rows take several
-// sweeps over the places. Partial sums of <dy, row> are kept per wave and slot in
+// The gradients of the next N slots for the chunk of dy that a lane holds, all loads
+// first; lane 0 of each wave adds the wave's part of <dy, row> to the slot's.
+template <class T, int N>
+__device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uint64_t& m, int i0,
+                                          const float (&g)[VEC], float* part) {
+  typename RawOf<T>::type r[N];
+  int64_t at[N];
+  float w[N];
+  int k[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    k[i] = next_slot(m);
+    at[i] = __builtin_amdgcn_readlane(p.at, k[i]) * a.ldp + i0;
+    w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k[i]));
+    if (a.dw) r[i] = load8(static_cast<const T*>(a.yp) + at[i], a.d - i0);
+  }
+  if (a.dw) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[VEC], dot = 0.0f;
+      unpack(r[i], v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dot = __builtin_fmaf(v[j], g[j], dot);
+      dot = wave_sum(dot);
+      if ((threadIdx.x & 63) == 0) part[k[i]] += dot;
+    }
+  }
+  if (a.y && i0 < a.d) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float o[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = w[i] * g[j];
+      store8(static_cast<T*>(a.y) + at[i], o, a.d - i0, a.stream);
+    }
+  }
+}
+
+// A chunk of dy's row stays in a lane's registers for all places; longer rows take
+// several sweeps over them. Partial sums of <dy, row> are kept per wave and slot in
 // LDS and added in wave order.
-template <class T, int LANES, int CH>
+template <class T, int LANES>
 __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
   constexpr int GROUPS = 256 / LANES, WAVES = LANES / 64;
   __shared__ float part[GROUPS][WAVES][kMaxK];
@@ -100,52 +138,20 @@ __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
   const int wave = lane >> 6;
   const int64_t t = a.t0 + int64_t(blockIdx.x) * GROUPS + group;
   const bool real = t < a.T;
-  Places p{-1, 0.0f, 0};
   if (real) {
-    p = places_of(a, t, threadIdx.x & 63);
-    if ((threadIdx.x & 63) < a.K) part[group][wave][threadIdx.x & 63] = 0.0f;
-    for (int s0 = 0; s0 < a.d; s0 += LANES * VEC * CH) {
-      float g[CH][VEC];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int i0 = s0 + (c * LANES + lane) * VEC;
-        unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), g[c]);
-      }
+    const Places p = places_of(a, t, threadIdx.x & 63);
+    float* sums = part[group][wave];
+    if ((threadIdx.x & 63) < a.K) sums[threadIdx.x & 63] = 0.0f;
+    for (int s0 = 0; s0 < a.d; s0 += LANES * VEC) {
+      const int i0 = s0 + lane * VEC;
+      float g[VEC];
+      unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), g);
       uint64_t m = p.mask;
-      while (m) {
-        const int k = next_slot(m);
-        const int64_t at = __builtin_amdgcn_readlane(p.at, k);
-        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k));
-        if (a.dw) {
-          typename RawOf<T>::type r[CH];
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const int i0 = s0 + (c * LANES + lane) * VEC;
-            r[c] = load8(static_cast<const T*>(a.yp) + at * a.ldp + i0, a.d - i0);
-          }
-          float dot = 0.0f;
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            float v[VEC];
-            unpack(r[c], v);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) dot = __builtin_fmaf(v[j], g[c][j], dot);
-          }
-          dot = wave_sum(dot);
-          if ((threadIdx.x & 63) == 0) part[group][wave][k] += dot;
-        }
-        if (a.y) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const int i0 = s0 + (c * LANES + lane) * VEC;
-            float o[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] = w * g[c][j];
-            if (i0 < a.d)
-              store8(static_cast<T*>(a.y) + at * a.ldp + i0, o, a.d - i0, a.stream);
-          }
-        }
-      }
+      int left = __popcll(m);
+      for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, g, sums);
+      for (; left >= 4; left -= 4) grad_rows<T, 4>(a, p, m, i0, g, sums);
+      for (; left >= 2; left -= 2) grad_rows<T, 2>(a, p, m, i0, g, sums);
+      for (; left >= 1; --left) grad_rows<T, 1>(a, p, m, i0, g, sums);
     }
   }
   if (!a.dw) return;
@@ -162,7 +168,11 @@ template <class T>
 void launch(const CombineArgs& p, bool backward, hipStream_t s) {
   TokArgs a{p.yp, p.inv, p.w, p.base, p.y, p.dw, 0, p.T, p.rows, p.ldt, p.ldp, p.K, p.d, false};
   a.stream = (backward ? p.rows : p.T) * p.d * int64_t(sizeof(T)) >= kFarBytes;
-  const bool narrow = p.d <= 1024;  // a wave per token, at most two chunks a lane
+  // a wave takes rows that its lanes hold in one chunk each: 4096 tokens of 8 places,
+  // rows of 256 bf16 values 5.0 us and 10.3 backward (a block per token 6.1 and 19.1), of
+  // 512 6.6 and 13.0 (7.5, 17.4), of 1024 13.9 and 24.4 (13.9, 24.9); 64 tokens of 1024
+  // 4.7 and 8.0 (3.6, 5.6)
+  const bool narrow = p.d <= 512;
   const int64_t per = kMaxBlocks * (narrow ? 4 : 1);
   for (int64_t t = 0; t < p.T; t += per) {
     const int64_t n = p.T - t < per ? p.T - t : per;
@@ -174,12 +184,11 @@ void launch(const CombineArgs& p, bool backward, hipStream_t s) {
         hipLaunchKernelGGL((token_combine_kernel<T, 64>), grid, dim3(256), 0, s, a);
       else
         hipLaunchKernelGGL((token_combine_kernel<T, 256>), grid, dim3(256), 0, s, a);
-    } else if (narrow) {
-      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 64, 2>), grid, dim3(256), 0, s, a);
-    } else if (p.d <= 2048) {
-      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256, 1>), grid, dim3(256), 0, s, a);
     } else {
-      hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256, 4>), grid, dim3(256), 0, s, a);
+      if (narrow)
+        hipLaunchKernelGGL((token_combine_bwd_kernel<T, 64>), grid, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256>), grid, dim3(256), 0, s, a);
     }
   }
 }

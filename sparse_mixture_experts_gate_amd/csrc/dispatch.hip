@@ -37,11 +37,11 @@ struct MoveArgs {
   const uint16_t* rank;  // [pairs] place of a pair among its chunk's of its expert
 };
 
-// Copies one row to the places pos[0 .. K) that exist, by LANES lanes.
+// Copies one row to the places that exist, by LANES lanes; lane k of a wave holds slot
+// k's in `at`.
 template <int LANES>
 __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64_t bytes,
-                                         int64_t ldp, const int32_t* pos, int K, int lane,
-                                         bool stream) {
+                                         int64_t ldp, int32_t at, int K, int lane, bool stream) {
   constexpr int CH = 4;  // 16-byte pieces of a lane in flight
   const int64_t whole = bytes / 16;
   for (int64_t c0 = lane; c0 < whole; c0 += CH * LANES) {
@@ -51,7 +51,7 @@ __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64
       if (c0 + i * LANES < whole)
         v[i] = *reinterpret_cast<const u32x4_any1_t*>(src + (c0 + i * LANES) * 16);
     for (int k = 0; k < K; ++k) {
-      const int p = __builtin_amdgcn_readfirstlane(pos[k]);
+      const int p = __builtin_amdgcn_readlane(at, k);
       if (p < 0) continue;
       uint8_t* d = dst + p * ldp;
 #pragma unroll
@@ -69,12 +69,11 @@ __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64
     }
   }
   const int tail = static_cast<int>(bytes - whole * 16);
-  if (lane < tail) {
-    const uint8_t v = src[whole * 16 + lane];
-    for (int k = 0; k < K; ++k) {
-      const int p = pos[k];
-      if (p >= 0) dst[p * ldp + whole * 16 + lane] = v;
-    }
+  if (tail == 0) return;
+  const uint8_t v = lane < tail ? src[whole * 16 + lane] : 0;
+  for (int k = 0; k < K; ++k) {
+    const int p = __builtin_amdgcn_readlane(at, k);
+    if (p >= 0 && lane < tail) dst[p * ldp + whole * 16 + lane] = v;
   }
 }
 
@@ -82,9 +81,10 @@ template <int LANES>
 __device__ __forceinline__ void move_token(const MoveArgs& a, int64_t t, const int32_t* pos,
                                            int lane) {
   if (!a.x) return;
-  move_row<LANES>(a.x + t * a.ldt, a.xp, a.row_bytes, a.ldp, pos, a.K, lane, a.stream);
+  const int32_t at = (lane & 63) < a.K ? pos[lane & 63] : -1;
+  move_row<LANES>(a.x + t * a.ldt, a.xp, a.row_bytes, a.ldp, at, a.K, lane, a.stream);
   if (a.x2)
-    move_row<LANES>(a.x2 + t * a.row2_bytes, a.xp2, a.row2_bytes, a.row2_bytes, pos, a.K, lane,
+    move_row<LANES>(a.x2 + t * a.row2_bytes, a.xp2, a.row2_bytes, a.row2_bytes, at, a.K, lane,
                     false);
 }
 
@@ -97,7 +97,8 @@ __device__ __forceinline__ int wave_sum_int(int v) {
 
 // Few pairs: block t < T places and moves token t's row; block T writes offsets
 // and the end of perm.
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 256, kFewK = 8;
+constexpr int kFewLoads = 4;  // selections of a thread in flight
 __global__ __launch_bounds__(kFewThreads) void dispatch_few_kernel(MoveArgs a) {
   const int tid = threadIdx.x;
   const int n = static_cast<int>(a.pairs), E = a.E, K = a.K;
@@ -129,42 +130,49 @@ __global__ __launch_bounds__(kFewThreads) void dispatch_few_kernel(MoveArgs a) {
     for (int r = count[E - 1] + tid; r < rows; r += kFewThreads) a.perm[r] = -1;
     return;
   }
-  __shared__ int32_t pos[kMaxK];
-  __shared__ int32_t part[kFewThreads / 64][8];
+  __shared__ int32_t pos[kFewK];
+  __shared__ int32_t part[kFewThreads / 64][kFewK];
   const int t = blockIdx.x;
-  for (int k0 = 0; k0 < K; k0 += 8) {
-    int ex[8], before[8] = {};
+  int ex[kFewK], before[kFewK] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = k0 + j < K ? a.idx[t * K + k0 + j] : -1;
-      ex[j] = static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
+  for (int j = 0; j < kFewK; ++j) {
+    const int e = j < K ? a.idx[t * K + j] : -1;
+    ex[j] = static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
+  }
+  for (int q0 = tid; q0 < n; q0 += kFewLoads * kFewThreads) {
+    int e[kFewLoads];
+#pragma unroll
+    for (int i = 0; i < kFewLoads; ++i) {
+      const int q = q0 + i * kFewThreads;
+      e[i] = q < n ? a.idx[q] : -1;
     }
-    for (int q = tid; q < n; q += kFewThreads) {
-      const int e = a.idx[q];
-      if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          before[j] += e < ex[j] || (e == ex[j] && q < t * K + k0 + j);
+    for (int i = 0; i < kFewLoads; ++i) {
+      const int q = q0 + i * kFewThreads;
+      if (static_cast<uint32_t>(e[i]) < static_cast<uint32_t>(E)) {
+#pragma unroll
+        for (int j = 0; j < kFewK; ++j)
+          before[j] += e[i] < ex[j] || (e[i] == ex[j] && q < t * K + j);
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int s = wave_sum_int(before[j]);
-      if ((tid & 63) == 0) part[tid >> 6][j] = s;
-    }
-    __syncthreads();
-    if (tid < 8 && k0 + tid < K) {
-      int p = part[0][tid];
-#pragma unroll
-      for (int w = 1; w < kFewThreads / 64; ++w) p += part[w][tid];
-      const int e = a.idx[t * K + k0 + tid];
-      if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E) || p >= a.rows) p = -1;
-      pos[k0 + tid] = p;
-      a.inv[t * K + k0 + tid] = p;
-      if (p >= 0) a.perm[p] = t;
-    }
-    __syncthreads();
   }
+#pragma unroll
+  for (int j = 0; j < kFewK; ++j) {
+    const int s = wave_sum_int(before[j]);
+    if ((tid & 63) == 0) part[tid >> 6][j] = s;
+  }
+  __syncthreads();
+  if (tid < K) {
+    int p = part[0][tid];
+#pragma unroll
+    for (int w = 1; w < kFewThreads / 64; ++w) p += part[w][tid];
+    const int e = a.idx[t * K + tid];
+    if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E) || p >= a.rows) p = -1;
+    pos[tid] = p;
+    a.inv[t * K + tid] = p;
+    if (p >= 0) a.perm[p] = t;
+  }
+  __syncthreads();
   move_token<kFewThreads>(a, t, pos, tid);
 }
 
@@ -328,9 +336,13 @@ __global__ __launch_bounds__(256) void no_pairs_kernel(int32_t* offsets, int E) 
   for (int e = threadIdx.x; e <= E; e += 256) offsets[e] = 0;
 }
 
-// Whether the pairs are few: every token's group reads all selections, so that
-// many bytes come from L2.
-bool few(int64_t T, int K) { return T * K <= 8192 && T * T * K <= (int64_t(1) << 21); }
+// Whether the pairs are few: every token's group reads all selections. Measured with
+// rows of 2048 bf16 values over 256 experts, one launch / three (us, replayed graphs):
+//   T x K  64 x 8    6.8 /  9.3     256 x 8   9.7 / 10.2     512 x 8  13.9 / 11.5
+//                                   512 x 4   9.3 /  9.8    1024 x 4  14.7 / 11.6
+//                                  1024 x 1   7.9 /  9.1    2048 x 1  13.5 / 10.2
+// More than eight slots would read them again for every eight (64 x 16: 12.2 / 10.6).
+bool few(int64_t T, int K) { return K <= kFewK && T <= 1024 && T * K <= 2048; }
 
 int64_t chunks_of(int64_t pairs) { return (pairs + kChunk - 1) / kChunk; }
 
@@ -387,6 +399,8 @@ hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s) {
     hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, s, count, static_cast<int>(chunks), p.E, cols,
                        p.rows, p.offsets);
   };
+  // (the whole sort in us, scan_kernel<4> / <16> / <0>: 4096 x 8 pairs over 64 experts
+  // 8.7 / 9.5 / 9.3; 8192 x 8 over 256 - / 10.2 / 11.3)
   if (chunks <= 4 * runs)
     scan(scan_kernel<4>);
   else if (chunks <= 16 * runs)
@@ -398,7 +412,10 @@ hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s) {
                        s, a);
     return hipGetLastError();
   }
-  const bool narrow = p.row_bytes <= 2048;  // a wave's 64 lanes take it in two pieces each
+  // a wave takes rows that its lanes hold in one piece each: 8192 tokens to 8 experts,
+  // rows of 256 bytes 14 us (a block per token 18), of 1 KB 21 (22), of 2 KB 33 (33),
+  // of 8 KB, 4096 tokens, 67 (61)
+  const bool narrow = p.row_bytes <= 1024;
   const int64_t per = kMaxBlocks * (narrow ? 4 : 1);
   for (int64_t t = 0; t < p.T; t += per) {
     a.t0 = t;

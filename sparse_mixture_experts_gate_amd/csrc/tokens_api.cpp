@@ -355,8 +355,9 @@ moe_status moe_mx4_quantize(const moe_mx4_desc* desc, const void* src, const int
   moe_status st = validate(desc, true);
   if (st) return st;
   if (desc->n_mats == 0 || desc->rows == 0) return MOE_OK;
-  st = check({{src, "src", size_of(desc->dtype), true}, {perm, "perm", 4, false},
-              {codes, "codes", 16, true}, {scales, "scales", 16, true}});
+  // no row of an empty src is read, whatever perm holds
+  st = check({{src, "src", size_of(desc->dtype), !perm || desc->n_src > 0},
+              {perm, "perm", 4, false}, {codes, "codes", 16, true}, {scales, "scales", 16, true}});
   if (st) return st;
   if (perm && desc->n_mats != 1)
     return fail(MOE_ERR_INVALID_ARGUMENT, "perm with n_mats = %lld: one matrix",

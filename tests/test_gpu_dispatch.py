@@ -234,3 +234,19 @@ def test_gradients_against_differences():
     for i in [(0, 0), (1, 1), (2, 1)]:
         e = torch.zeros_like(w); e[i] = 1.0
         assert abs(loss(x, w + e) - loss(x, w - e) - 2 * float(g["dweight"][i])) < 1e-4
+
+
+@pytest.mark.parametrize("T,K", [(256, 8), (257, 8), (1024, 2), (1025, 1), (1024, 1), (30, 9), (3, 33)])
+def test_both_sides_of_one_launch(T, K):
+    """Pairs that one launch places and the next size up, rows of a wave and of a block."""
+    import sparse_mixture_experts_gate_amd as M
+    idx = _idx(T, T, K, 40, 0.1)
+    off, perm, inv = _place(idx, 40)
+    for d in (512, 520):
+        x = _rows(2, T, d, "bf16")
+        o = M.TokenDispatch(40).forward(x, torch.from_numpy(idx).to(DEV))
+        assert np.array_equal(host(o["offsets"]), off) and np.array_equal(host(o["perm"]), perm)
+        assert np.array_equal(host(o["inv"]), inv)
+        n = int(off[-1])
+        assert torch.equal(o["rows"][:n], x[torch.from_numpy(perm[:n].astype(np.int64)).to(DEV)])
+        _check_return(T, K, d, "f32", idx, 40, None, True, False)

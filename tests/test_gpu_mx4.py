@@ -276,3 +276,28 @@ def test_one_row_more_or_less_changes_no_other(rows, n, k):
     want = lin.forward(x, off(9000), out_dtype=torch.float32)
     for m in (1, rows, rows + 1, 1000):
         assert torch.equal(lin.forward(x[:m], off(m), out_dtype=torch.float32), want[:m])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_permutation_of_no_rows(dt):
+    """A rank without tokens: every entry of perm is outside."""
+    import sparse_mixture_experts_gate_amd as M
+    x = torch.empty(0, 96, dtype=DT[dt], device=DEV)
+    perm = torch.tensor([-1, 0, 5], dtype=torch.int32, device=DEV)
+    codes, scales = M.mx4_quantize(x, perm)
+    assert codes.shape == (3, 48) and not codes.any() and not scales.any()
+    lin = M.MX4Linear.from_weight(_rand(1, 1, 40, 96))
+    y = lin.forward(x, torch.tensor([0, 3], dtype=torch.int32, device=DEV), perm=perm)
+    assert y.shape == (3, 40) and not y.any()
+
+
+@pytest.mark.parametrize("a,b", [(-100, -40), (-126, -3), (-60, -84), (-120, -120), (120, 20)])
+def test_products_at_the_ends_of_the_range(a, b):
+    """Sums below the normal numbers keep their bits, past the range they are infinite:
+    32 equal products of powers of two are one power."""
+    import sparse_mixture_experts_gate_amd as M
+    lin = M.MX4Linear.from_weight(torch.full((1, 40, 32), 2.0 ** b, device=DEV))
+    off = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    y = host(lin.forward(torch.full((5, 32), 2.0 ** a, device=DEV), off, out_dtype=torch.float32))
+    with np.errstate(over="ignore"):
+        assert (y == np.float32(2.0 ** (a + b + 5))).all()
