@@ -40,7 +40,7 @@ struct FwdArgs {
 // Mean first, then the squares of what is left, both from registers: merging
 // per-lane moments in one pass is as stable but took ten times the vector
 // operations, and those then bound the kernel. Bound by memory: 8192 x 7168
-// bf16 with a residual takes 98 us, 470 MB at 4.8 TB/s, a large copy's rate.
+// bf16 with a residual takes 95 us, 470 MB at 4.9 TB/s, a large copy's rate.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdArgs a) {
   __shared__ float slot[2][NW];
@@ -195,8 +195,8 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* slot) {
 // each block then writes one partial sum per column. The next row is loaded
 // while the current one is reduced. With NW == 1 the block's four waves add
 // their column sums through LDS, in wave order.
-// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 92 us, 470 MB
-// at 5.1 TB/s.
+// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 90 us, 470 MB
+// at 5.2 TB/s.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNormArgs a) {
   constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
@@ -502,8 +502,8 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
 
 // Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
 // More blocks hide more latency but write and add more partial rows (8192 x 7168
-// bf16 with dresidual: 92 us with 256 blocks of 8 waves, 103 with 512; 8192 x
-// 4096: 54 us with 512 of 4 waves, 59 with 768, 64 with 1024).
+// bf16 with dresidual: 90 us with 256 blocks of 8 waves, 98 with 512; 8192 x 4096:
+// 53 us with 256 of 4 waves, 56 with 512, 63 with 1024; 8192 x 2048: 36, 29, 33).
 int norm_backward_parts(int64_t n, int d) {
   if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);
   const int nw = row_shape(d).nw;
