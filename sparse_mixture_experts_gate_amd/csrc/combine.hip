@@ -61,12 +61,12 @@ __device__ __forceinline__ void add_rows(const TokArgs& a, const Places& p, uint
     const int k = next_slot(m);
     const int64_t at = __builtin_amdgcn_readlane(p.at, k);
     w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k));
-    r[i] = load8(static_cast<const T*>(a.yp) + at * a.ldp + i0, a.d - i0);
+    r[i] = load8(static_cast<const T*>(a.yp) + at * a.ldp, i0, a.d);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float v[VEC];
-    unpack(r[i], v);
+    unpack(r[i], v, a.d - i0);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc[j] = __builtin_fmaf(w[i], v[j], acc[j]);
   }
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void token_combine_kernel(TokArgs a) {
   const Places p = places_of(a, t, threadIdx.x & 63);
   for (int i0 = lane * VEC; i0 < a.d; i0 += LANES * VEC) {
     float acc[VEC] = {};
-    if (a.base) unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), acc);
+    if (a.base) unpack(load8(static_cast<const T*>(a.base) + t * a.ldt, i0, a.d), acc, a.d - i0);
     uint64_t m = p.mask;
     int left = __popcll(m);
     for (; left >= 8; left -= 8) add_rows<T, 8>(a, p, m, i0, acc);
@@ -103,15 +103,15 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     k[i] = next_slot(m);
-    at[i] = __builtin_amdgcn_readlane(p.at, k[i]) * a.ldp + i0;
+    at[i] = __builtin_amdgcn_readlane(p.at, k[i]) * a.ldp;
     w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k[i]));
-    if (a.dw) r[i] = load8(static_cast<const T*>(a.yp) + at[i], a.d - i0);
+    if (a.dw) r[i] = load8(static_cast<const T*>(a.yp) + at[i], i0, a.d);
   }
   if (a.dw) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[VEC], dot = 0.0f;
-      unpack(r[i], v);
+      unpack(r[i], v, a.d - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) dot = __builtin_fmaf(v[j], g[j], dot);
       dot = wave_sum(dot);
@@ -124,7 +124,7 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
       float o[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) o[j] = w[i] * g[j];
-      store8(static_cast<T*>(a.y) + at[i], o, a.d - i0, a.stream);
+      store8(static_cast<T*>(a.y) + at[i] + i0, o, a.d - i0, a.stream);
     }
   }
 }
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
     for (int s0 = 0; s0 < a.d; s0 += LANES * VEC) {
       const int i0 = s0 + lane * VEC;
       float g[VEC];
-      unpack(load8(static_cast<const T*>(a.base) + t * a.ldt + i0, a.d - i0), g);
+      unpack(load8(static_cast<const T*>(a.base) + t * a.ldt, i0, a.d), g, a.d - i0);
       uint64_t m = p.mask;
       int left = __popcll(m);
       for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, g, sums);

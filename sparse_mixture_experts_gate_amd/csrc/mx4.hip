@@ -98,12 +98,13 @@ template <class T, int ROWS, bool SWIGLU>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
   __shared__ uint32_t words[4][ROWS];
   constexpr int PER = ROWS / 4;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Block b(a);
   const int64_t mat = b.mat, r0 = b.rows * ROWS;
   const int i0 = b.span * kSpan + lane * VEC;
   const T* src = static_cast<const T*>(a.src) + mat * a.mat;
   typename RawOf<T>::type raw[PER], raw2[SWIGLU ? PER : 1];
+  int d[PER];  // lengths of the rows, 0 for none
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int64_t r = r0 + wave * PER + i;
@@ -112,19 +113,19 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
       from = a.perm[r];
       if (from >= a.n_src) from = -1;
     }
-    const int cnt = from >= 0 ? a.k - i0 : 0;
-    const T* p = src + (from >= 0 ? from : 0) * a.ld + i0;
-    raw[i] = load8(p, cnt);
-    if constexpr (SWIGLU) raw2[i] = load8(p + a.k, cnt);
+    d[i] = __builtin_amdgcn_readfirstlane(from >= 0 ? a.k : 0);
+    const T* p = src + (from >= 0 ? from : 0) * a.ld;
+    raw[i] = load8(p, i0, d[i]);
+    if constexpr (SWIGLU) raw2[i] = load8(p + a.k, i0, d[i]);
   }
   uint8_t* codes = a.codes + (mat * a.rows + r0) * a.kb * 16;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     float v[VEC];
-    unpack(raw[i], v);
+    unpack(raw[i], v, d[i] - i0);
     if constexpr (SWIGLU) {
       float up[VEC];
-      unpack(raw2[i], up);
+      unpack(raw2[i], up, d[i] - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] = silu_f32(v[j]) * up[j];
     }

@@ -422,7 +422,9 @@ __global__ __launch_bounds__(C::NT, kMinWaves<C>) void mx4_gemm_kernel(MArgs a) 
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::NST * C::STAGE];
   __shared__ GroupTables gt;
   build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, (a.n + C::BN - 1) / C::BN);
-  const int total = gt.total, nb = gridDim.x;
+  // the grid is sized for the most tiles there can be: fewer are spread over all XCDs
+  const int total = gt.total, nb = min(static_cast<int>(gridDim.x), (total + 7) / 8 * 8);
+  if (static_cast<int>(blockIdx.x) >= nb) return;
   const int first = xcd_logical_block(blockIdx.x, nb);
   if (first >= total) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -7,10 +7,10 @@
 // from memory for every pass instead.
 //
 // The backward of rows past 8192 values holds two rows, the weight and two
-// column sums at 32 values a lane each, which 256 registers do not take: up to
-// 296 bytes a lane go to scratch memory (fp32 with dresidual; 36 without, bf16
-// with it 56). 2048 x 16384: bf16 48 us, with dresidual 74; fp32 104 and 191,
-// 0.4 to 0.9 of a large copy's rate.
+// column sums at 32 values a lane each, which fill 256 registers or do not fit them:
+// 180 bytes a lane go to scratch memory with fp32 rows and dresidual, 20 without.
+// 2048 x 16384: bf16 53 us, with dresidual 65; fp32 101 and 158, 0.7 to 0.85 of a
+// large copy's rate.
 #include "device_common.h"
 #include "internal.h"
 #include "row_io.h"
@@ -40,7 +40,7 @@ struct FwdArgs {
 // Mean first, then the squares of what is left, both from registers: merging
 // per-lane moments in one pass is as stable but took ten times the vector
 // operations, and those then bound the kernel. Bound by memory: 8192 x 7168
-// bf16 with a residual takes 95 us, 470 MB at 4.9 TB/s, a large copy's rate.
+// bf16 with a residual takes 83 us, 470 MB at 5.7 TB/s, past a large copy's rate.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdArgs a) {
   __shared__ float slot[2][NW];
@@ -54,16 +54,16 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdAr
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i0 = (c * LANES + lane) * VEC;
-    rx[c] = load8(x + i0, a.d - i0);
-    if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr + i0, a.d - i0);
+    rx[c] = load8(x, i0, a.d);
+    if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr, i0, a.d);
   }
   float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    unpack(rx[c], v[c]);
+    unpack(rx[c], v[c], a.d - (c * LANES + lane) * VEC);
     if constexpr (RES) {
       float r[VEC];
-      unpack(rr[c], r);
+      unpack(rr[c], r, a.d - (c * LANES + lane) * VEC);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[c][j] += r[j];
     }
@@ -100,8 +100,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_fwd_kernel(FwdAr
     const int cnt = a.d - i0;
     if (cnt <= 0) continue;
     float w[VEC], b[VEC], o[VEC];
-    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
-    load_vec(a.b ? a.b + i0 : nullptr, b, cnt, 0.0f);
+    load_vec(a.w, w, i0, a.d, 1.0f);
+    load_vec(a.b, b, i0, a.d, 0.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) o[j] = v[c][j] * rstd * w[j] + b[j];
     store8(y + i0, o, cnt, a.stream);
@@ -117,10 +117,10 @@ __global__ __launch_bounds__(512) void norm_fwd_long_kernel(FwdArgs a) {
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
   auto get = [&](int i0, float (&v)[VEC]) {
-    unpack(load8(x + i0, a.d - i0), v);
+    unpack(load8(x, i0, a.d), v, a.d - i0);
     if (r) {
       float u[VEC];
-      unpack(load8(r + i0, a.d - i0), u);
+      unpack(load8(r, i0, a.d), u, a.d - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] += u[j];
     }
@@ -149,8 +149,8 @@ __global__ __launch_bounds__(512) void norm_fwd_long_kernel(FwdArgs a) {
     get(i0, v);
     const int cnt = a.d - i0;
     if (r) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v, cnt, a.stream);
-    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
-    load_vec(a.b ? a.b + i0 : nullptr, b, cnt, 0.0f);
+    load_vec(a.w, w, i0, a.d, 1.0f);
+    load_vec(a.b, b, i0, a.d, 0.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) o[j] = (v[j] - mean) * rstd * w[j] + b[j];
     store8(static_cast<T*>(a.y) + row * a.ldy + i0, o, cnt, a.stream);
@@ -195,11 +195,14 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* slot) {
 // each block then writes one partial sum per column. The next row is loaded
 // while the current one is reduced. With NW == 1 the block's four waves add
 // their column sums through LDS, in wave order.
-// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 90 us, 470 MB
-// at 5.2 TB/s.
+// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 89 us, 470 MB
+// at 5.3 TB/s.
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNormArgs a) {
   constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
+  // Four chunks leave no registers for the next row's dresidual: the row's own is loaded
+  // behind its other loads (2048 x 16384 bf16: 65 us before, 61 so; fp32 191 and 154).
+  constexpr bool LATE = RES && CH == 4;
   __shared__ float2 slot[2][NW];
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t first = int64_t(blockIdx.x) * GROUPS + (NW == 1 ? threadIdx.x >> 6 : 0);
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i0 = (c * LANES + lane) * VEC;
-    load_vec(a.w ? a.w + i0 : nullptr, w[c], a.d - i0, 1.0f);
+    load_vec(a.w, w[c], i0, a.d, 1.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) aw[c][j] = ab[c][j] = 0.0f;
   }
@@ -220,9 +223,10 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i0 = (c * LANES + lane) * VEC;
-      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx + i0, a.d - i0);
-      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, a.d - i0);
-      if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0);
+      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx, i0, a.d);
+      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy, i0, a.d);
+      if constexpr (RES && !LATE)
+        rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, i0, a.d);
     }
   };
   if (first < a.n) fetch(first);
@@ -235,10 +239,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
     const float m = mu, r = rs;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      unpack(rx[c], z[c]);
-      unpack(rg[c], g[c]);
-      if constexpr (RES) kr[c] = rr[c];
       const int cnt = a.d - (c * LANES + lane) * VEC;
+      unpack(rx[c], z[c], cnt);
+      unpack(rg[c], g[c], cnt);
+      if constexpr (LATE)
+        kr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, (c * LANES + lane) * VEC, a.d);
+      else if constexpr (RES)
+        kr[c] = rr[c];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         z[c][j] = j < cnt ? (z[c][j] - m) * r : 0.0f;
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
       for (int j = 0; j < VEC; ++j) o[j] = r * (g[c][j] - c1 - z[c][j] * c2);
       if constexpr (RES) {
         float e[VEC];
-        unpack(kr[c], e);
+        unpack(kr[c], e, a.d - i0);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += e[j];
       }
@@ -310,9 +317,9 @@ __global__ __launch_bounds__(512) void norm_bwd_long_kernel(BwdNormArgs a) {
   auto get = [&](int i0, float (&z)[VEC], float (&g)[VEC]) {
     float w[VEC];
     const int cnt = a.d - i0;
-    unpack(load8(x + i0, cnt), z);
-    unpack(load8(dy + i0, cnt), g);
-    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
+    unpack(load8(x, i0, a.d), z, a.d - i0);
+    unpack(load8(dy, i0, a.d), g, a.d - i0);
+    load_vec(a.w, w, i0, a.d, 1.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       z[j] = j < cnt ? (z[j] - m) * r : 0.0f;
@@ -338,7 +345,7 @@ __global__ __launch_bounds__(512) void norm_bwd_long_kernel(BwdNormArgs a) {
     for (int j = 0; j < VEC; ++j) o[j] = r * (g[j] - c1 - z[j] * c2);
     if (a.dr) {
       float e[VEC];
-      unpack(load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0), e);
+      unpack(load8(static_cast<const T*>(a.dr) + row * a.ldr, i0, a.d), e, a.d - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) o[j] += e[j];
     }
@@ -356,8 +363,8 @@ __global__ __launch_bounds__(64) void norm_cols_kernel(BwdNormArgs a) {
   float aw[VEC] = {}, ab[VEC] = {};
   for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
     float z[VEC], g[VEC];
-    unpack(load8(static_cast<const T*>(a.x) + row * a.ldx + i0, cnt), z);
-    unpack(load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, cnt), g);
+    unpack(load8(static_cast<const T*>(a.x) + row * a.ldx, i0, a.d), z, a.d - i0);
+    unpack(load8(static_cast<const T*>(a.dy) + row * a.ldy, i0, a.d), g, a.d - i0);
     const float m = a.mean[row], r = a.rstd[row];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -502,7 +509,7 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
 
 // Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
 // More blocks hide more latency but write and add more partial rows (8192 x 7168
-// bf16 with dresidual: 90 us with 256 blocks of 8 waves, 98 with 512; 8192 x 4096:
+// bf16 with dresidual: 89 us with 256 blocks of 8 waves, 98 with 512; 8192 x 4096:
 // 53 us with 256 of 4 waves, 56 with 512, 63 with 1024; 8192 x 2048: 36, 29, 33).
 int norm_backward_parts(int64_t n, int d) {
   if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);

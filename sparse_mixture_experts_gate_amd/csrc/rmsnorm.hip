@@ -96,21 +96,21 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_fwd_kernel(RmsFwd
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i0 = (c * LANES + lane) * VEC;
-    rx[c] = load8(x + i0, a.d - i0);
-    if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr + i0, a.d - i0);
+    rx[c] = load8(x, i0, a.d);
+    if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.r) + row * a.ldr, i0, a.d);
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i0 = (c * LANES + lane) * VEC;
-    load_vec(a.w ? a.w + i0 : nullptr, w[c], a.d - i0, 1.0f);
+    load_vec(a.w, w[c], i0, a.d, 1.0f);
   }
   float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    unpack(rx[c], v[c]);
+    unpack(rx[c], v[c], a.d - (c * LANES + lane) * VEC);
     if constexpr (RES) {
       float r[VEC];
-      unpack(rr[c], r);
+      unpack(rr[c], r, a.d - (c * LANES + lane) * VEC);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[c][j] += r[j];
     }
@@ -148,10 +148,10 @@ __global__ __launch_bounds__(512) void rms_fwd_long_kernel(RmsFwdArgs a) {
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
   auto get = [&](int i0, float (&v)[VEC]) {
-    unpack(load8(x + i0, a.d - i0), v);
+    unpack(load8(x, i0, a.d), v, a.d - i0);
     if (r) {
       float u[VEC];
-      unpack(load8(r + i0, a.d - i0), u);
+      unpack(load8(r, i0, a.d), u, a.d - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[j] += u[j];
     }
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(512) void rms_fwd_long_kernel(RmsFwdArgs a) {
     float v[VEC], w[VEC], o[VEC];
     const int cnt = a.d - i0;
     get(i0, v);
-    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
+    load_vec(a.w, w, i0, a.d, 1.0f);
     if (r && cnt > 0) store8(static_cast<T*>(a.sum) + row * a.lds + i0, v, cnt, a.stream);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) o[j] = v[j] * rstd * w[j];
@@ -207,6 +207,10 @@ struct RmsBwdArgs {
 template <class T, int NW, int CH, bool RES>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwdArgs a) {
   constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
+  // Four chunks of fp32 rows leave no registers for the next row's dresidual: the row's
+  // own is loaded behind its other loads (2048 x 16384: 145 us before, 118 so; bf16, which
+  // has them, 48 and 53).
+  constexpr bool LATE = RES && CH == 4 && sizeof(T) == 4;
   __shared__ float slot[2][NW];
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t first = int64_t(blockIdx.x) * GROUPS + (NW == 1 ? threadIdx.x >> 6 : 0);
@@ -215,7 +219,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwd
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i0 = (c * LANES + lane) * VEC;
-    load_vec(a.w ? a.w + i0 : nullptr, w[c], a.d - i0, 1.0f);
+    load_vec(a.w, w[c], i0, a.d, 1.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) aw[c][j] = 0.0f;
   }
@@ -226,9 +230,10 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwd
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i0 = (c * LANES + lane) * VEC;
-      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx + i0, a.d - i0);
-      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, a.d - i0);
-      if constexpr (RES) rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0);
+      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx, i0, a.d);
+      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy, i0, a.d);
+      if constexpr (RES && !LATE)
+        rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, i0, a.d);
     }
   };
   if (first < a.n) fetch(first);
@@ -241,10 +246,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwd
     const float r = rs;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      unpack(rx[c], z[c]);
-      unpack(rg[c], g[c]);
-      if constexpr (RES) kr[c] = rr[c];
       const int cnt = a.d - (c * LANES + lane) * VEC;
+      unpack(rx[c], z[c], cnt);
+      unpack(rg[c], g[c], cnt);
+      if constexpr (LATE)
+        kr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, (c * LANES + lane) * VEC, a.d);
+      else if constexpr (RES)
+        kr[c] = rr[c];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         z[c][j] = j < cnt ? z[c][j] * r : 0.0f;
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwd
       for (int j = 0; j < VEC; ++j) o[j] = r * (g[c][j] - z[c][j] * c2);
       if constexpr (RES) {
         float e[VEC];
-        unpack(kr[c], e);
+        unpack(kr[c], e, a.d - i0);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += e[j];
       }
@@ -306,9 +314,9 @@ __global__ __launch_bounds__(512) void rms_bwd_long_kernel(RmsBwdArgs a) {
   auto get = [&](int i0, float (&z)[VEC], float (&g)[VEC]) {
     float w[VEC];
     const int cnt = a.d - i0;
-    unpack(load8(x + i0, cnt), z);
-    unpack(load8(dy + i0, cnt), g);
-    load_vec(a.w ? a.w + i0 : nullptr, w, cnt, 1.0f);
+    unpack(load8(x, i0, a.d), z, a.d - i0);
+    unpack(load8(dy, i0, a.d), g, a.d - i0);
+    load_vec(a.w, w, i0, a.d, 1.0f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       z[j] = j < cnt ? z[j] * r : 0.0f;
@@ -330,7 +338,7 @@ __global__ __launch_bounds__(512) void rms_bwd_long_kernel(RmsBwdArgs a) {
     for (int j = 0; j < VEC; ++j) o[j] = r * (g[j] - z[j] * c2);
     if (a.dr) {
       float e[VEC];
-      unpack(load8(static_cast<const T*>(a.dr) + row * a.ldr + i0, a.d - i0), e);
+      unpack(load8(static_cast<const T*>(a.dr) + row * a.ldr, i0, a.d), e, a.d - i0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) o[j] += e[j];
     }
@@ -348,8 +356,8 @@ __global__ __launch_bounds__(64) void rms_cols_kernel(RmsBwdArgs a) {
   float aw[VEC] = {};
   for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
     float z[VEC], g[VEC];
-    unpack(load8(static_cast<const T*>(a.x) + row * a.ldx + i0, cnt), z);
-    unpack(load8(static_cast<const T*>(a.dy) + row * a.ldy + i0, cnt), g);
+    unpack(load8(static_cast<const T*>(a.x) + row * a.ldx, i0, a.d), z, a.d - i0);
+    unpack(load8(static_cast<const T*>(a.dy) + row * a.ldy, i0, a.d), g, a.d - i0);
     const float r = a.rstd[row];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) aw[j] += g[j] * (z[j] * r);

@@ -27,28 +27,63 @@ struct RawOf<float> {
   using type = Raw32;
 };
 
-// Eight values at p, of which the first `cnt` exist (the rest read as zero).
-// Rows may start at any element, so the 16-byte accesses go through memcpy,
-// which the compiler emits as one unaligned access.
-template <class T>
-__device__ __forceinline__ typename RawOf<T>::type load8(const T* p, int cnt) {
-  typename RawOf<T>::type r;
-  if (cnt >= VEC) {
-    __builtin_memcpy(&r, p, sizeof(r));
+// The eight values i0 .. i0 + 7 (i0 a multiple of 8) of a row of d values, for unpack.
+// Rows may start at any element, so the 16-byte accesses go through memcpy, which the
+// compiler emits as one unaligned access.
+// bf16: where the row ends among them, they are the row's last eight, which unpack
+// shifts into place: one access like the others, not waited for before that. Value by
+// value, the halves of words met here and each load of a row's end cost a wait of its
+// own (RMS norm of 8192 x 2815 forward 38 us, 33 so; backward 77 and 40; return of 8192
+// rows 17 and 12). A lane uses its own values of them only, so another lane may be storing
+// the others. Lanes past the row load nothing; unpack gives them zeros.
+__device__ __forceinline__ Raw16 load8(const uint16_t* row, int i0, int d) {
+  Raw16 r;
+  if (d >= VEC) {
+    if (i0 < d) __builtin_memcpy(&r, row + min(i0, d - VEC), sizeof(r));
   } else {
-    T tmp[VEC];
+    uint16_t tmp[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) tmp[j] = j < cnt ? p[j] : T(0);
+    for (int j = 0; j < VEC; ++j) tmp[j] = i0 == 0 && j >= VEC - d ? row[j - (VEC - d)] : 0;
     __builtin_memcpy(&r, tmp, sizeof(r));
   }
   return r;
 }
-__device__ __forceinline__ void unpack(const Raw16& r, float (&v)[VEC]) {
+// fp32: value by value at the end, zeros past it (shifts cost the registers that the
+// backward's occupancy needs: 8192 x 2815 75 us, 78 with them).
+__device__ __forceinline__ Raw32 load8(const float* row, int i0, int d) {
+  Raw32 r;
+  const float* p = row + i0;
+  const int cnt = d - i0;
+  if (cnt >= VEC) {
+    __builtin_memcpy(&r, p, sizeof(r));
+  } else {
+    float tmp[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) tmp[j] = j < cnt ? p[j] : 0.0f;
+    __builtin_memcpy(&r, tmp, sizeof(r));
+  }
+  return r;
+}
+// load8's values in order, with cnt = d - i0: zeros past the row's end.
+__device__ __forceinline__ void unpack(Raw16 r, float (&v)[VEC], int cnt) {
+  if (cnt < VEC) {  // the first VEC - cnt are not this lane's
+    const int by = VEC - cnt;
+    if (by & 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[j] = (r.w[j] >> 16) | (j < 3 ? r.w[j + 1] << 16 : 0u);
+    }
+#pragma unroll
+    for (int s = 1; s < 4; s *= 2)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[j] = by & (2 * s) ? (j + s < 4 ? +r.w[j + s] : 0u) : +r.w[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = cnt > 0 ? +r.w[j] : 0u;
+  }
 #pragma unroll
   for (int j = 0; j < VEC; ++j)
     v[j] = __uint_as_float((j & 1) ? (r.w[j >> 1] & 0xFFFF0000u) : (r.w[j >> 1] << 16));
 }
-__device__ __forceinline__ void unpack(const Raw32& r, float (&v)[VEC]) {
+__device__ __forceinline__ void unpack(const Raw32& r, float (&v)[VEC], int) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(r.w[j]);
 }
@@ -60,16 +95,26 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_any2_t __attribute__((aligned(2)));
+
+// The first cnt (1 .. 7) of eight bf16 values: four, two and one of them.
+__device__ __forceinline__ void store_end(uint16_t* p, u32x4_any_t r, int cnt) {
+  if (cnt & 4) *reinterpret_cast<u32x2_any2_t*>(p) = u32x2_any2_t{r[0], r[1]};
+  const uint32_t lo = cnt & 4 ? +r[2] : +r[0], hi = cnt & 4 ? +r[3] : +r[1];
+  if (cnt & 2) *reinterpret_cast<u32_any2_t*>(p + (cnt & 4)) = lo;
+  if (cnt & 1) p[cnt & 6] = static_cast<uint16_t>(cnt & 2 ? hi : lo);
+}
 
 // The first `cnt` of eight values. `stream`: past the caches, for outputs larger
 // than the L2s together, which no reader would find there. The empty statements keep
 // the compiler from merging the two stores into one without the hint.
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int cnt,
                                        bool stream = false) {
-  if (cnt >= VEC) {
-    u32x4_any_t r;
+  u32x4_any_t r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < 4; ++j) r[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+  if (cnt >= VEC) {
     if (stream) {
       asm volatile("");
       __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any_t*>(p));
@@ -77,10 +122,8 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[VEC], int c
     } else {
       *reinterpret_cast<u32x4_any_t*>(p) = r;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (j < cnt) p[j] = static_cast<uint16_t>(bf16_pair(v[j], 0.0f));
+  } else if (cnt > 0) {
+    store_end(p, r, cnt);
   }
 }
 // fp32 values leave in two stores per lane, 16 bytes of every 32 each, which the
@@ -97,13 +140,32 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[VEC], int cnt,
       if (j < cnt) p[j] = v[j];
   }
 }
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC], int cnt, float none) {
-  if (p) {
-    unpack(load8(p, cnt), v);
-  } else {
+// A weight's values, `none` without one, zeros past its end; its last eight shifted into
+// place as bf16 rows' are (layer norm of 8192 x 2816 bf16 31 us value by value, 28 so).
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC], int i0, int d,
+                                         float none) {
+  if (!p) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = none;
+    return;
   }
+  const int cnt = d - i0;
+  if (d < VEC) {
+    unpack(load8(p, i0, d), v, cnt);
+    return;
+  }
+  Raw32 r;
+  if (cnt > 0) __builtin_memcpy(&r, p + min(i0, d - VEC), sizeof(r));
+  if (cnt < VEC) {
+    const int by = VEC - cnt;
+#pragma unroll
+    for (int s = 1; s < VEC; s *= 2)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) r.w[j] = by & s ? (j + s < VEC ? +r.w[j + s] : 0u) : +r.w[j];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r.w[j] = cnt > 0 ? +r.w[j] : 0u;
+  }
+  unpack(r, v, cnt);
 }
 
 // Sum over the wave by DPP adds (rows of 16 lanes, then across rows; lane 63
@@ -137,8 +199,8 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
 }
 
 // bf16 row outputs of this many bytes or more are stored past the caches: eight L2s
-// of 4 MB (layer norm of 8192 x 7168 with a residual 98 -> 95 us, its backward 92 ->
-// 89, 4096 x 4096 19 -> 17; fp32 rows of 8192 x 7168, in both stores, 137 -> 155).
+// of 4 MB (layer norm of 8192 x 7168 with a residual 98 us without, 95 so, its backward 92
+// and 89, both with weights loaded value by value; fp32 rows of 8192 x 7168, in both stores, 137 -> 155).
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
 // The same for rows moved between tokens and experts, whose reader comes next and
 // finds smaller outputs in the 256 MB that the L2s share: E4M3 rows of 8192 tokens to 8
