@@ -92,10 +92,10 @@ __global__ __launch_bounds__(256) void token_combine_kernel(TokArgs a) {
 }
 
 // The gradients of the next N slots for the chunk of dy that a lane holds, all loads
-// first; lane 0 of each wave adds the wave's part of <dy, row> to the slot's.
+// first; lane k of each wave adds the wave's part of <dy, row> to slot k's `sum`.
 template <class T, int N>
 __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uint64_t& m, int i0,
-                                          const float (&g)[VEC], float* part) {
+                                          const float (&g)[VEC], float& sum) {
   typename RawOf<T>::type r[N];
   int64_t at[N];
   float w[N];
@@ -115,7 +115,7 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
 #pragma unroll
       for (int j = 0; j < VEC; ++j) dot = __builtin_fmaf(v[j], g[j], dot);
       dot = wave_sum(dot);
-      if ((threadIdx.x & 63) == 0) part[k[i]] += dot;
+      if (static_cast<int>(threadIdx.x & 63) == k[i]) sum += dot;
     }
   }
   if (a.y && i0 < a.d) {
@@ -130,8 +130,8 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
 }
 
 // A chunk of dy's row stays in a lane's registers for all places; longer rows take
-// several sweeps over them. Partial sums of <dy, row> are kept per wave and slot in
-// LDS and added in wave order.
+// several sweeps over them. A wave's part of slot k's <dy, row> is lane k's; the waves'
+// are added through LDS in wave order.
 template <class T, int LANES>
 __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
   constexpr int GROUPS = 256 / LANES, WAVES = LANES / 64;
@@ -142,19 +142,19 @@ __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
   const bool real = t < a.T;
   if (real) {
     const Places p = places_of(a, t, threadIdx.x & 63);
-    float* sums = part[group][wave];
-    if ((threadIdx.x & 63) < a.K) sums[threadIdx.x & 63] = 0.0f;
+    float sum = 0.0f;
     for (int s0 = 0; s0 < a.d; s0 += LANES * VEC) {
       const int i0 = s0 + lane * VEC;
       float g[VEC];
       unpack(load8(static_cast<const T*>(a.base) + t * a.ldt, i0, a.d), g, a.d - i0);
       uint64_t m = p.mask;
       int left = __popcll(m);
-      for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, g, sums);
-      for (; left >= 4; left -= 4) grad_rows<T, 4>(a, p, m, i0, g, sums);
-      for (; left >= 2; left -= 2) grad_rows<T, 2>(a, p, m, i0, g, sums);
-      for (; left >= 1; --left) grad_rows<T, 1>(a, p, m, i0, g, sums);
+      for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, g, sum);
+      for (; left >= 4; left -= 4) grad_rows<T, 4>(a, p, m, i0, g, sum);
+      for (; left >= 2; left -= 2) grad_rows<T, 2>(a, p, m, i0, g, sum);
+      for (; left >= 1; --left) grad_rows<T, 1>(a, p, m, i0, g, sum);
     }
+    part[group][wave][threadIdx.x & 63] = sum;
   }
   if (!a.dw) return;
   __syncthreads();

@@ -2,8 +2,8 @@
 // in dsmoe_tokens.h).
 //
 // Memory-bound: a lane holds 8 adjacent values (one word of codes), four lanes a
-// block, 16 lanes four blocks, whose scale bytes make one word. A workgroup takes
-// ROWS rows of 512 values at a time, so that the scale words of a column of blocks,
+// block, 16 lanes four blocks, whose scale bytes make one word. LANES lanes take a row,
+// or 512 values of one; a workgroup takes PER rows for each, so that the scale words of a column of blocks,
 // which lie row by row, leave as one run of ROWS words and not one by one from
 // several XCDs. bf16 rows of 8192 x 7168: 28 us, 148 MB at 5.3 TB/s; 32 matrices of 4096
 // x 7168: 407 us, 2.4 GB at 5.8, and back 363 us at 6.5.
@@ -15,10 +15,13 @@ namespace dsmoe {
 
 namespace {
 
-constexpr int kSpan = 512;  // values of a row that one wave takes
-// Blocks of 16 rows from which on these are taken; fewer leave CUs idle, and 8 rows
-// make twice as many (3 x 613 x 1407 values the same). 8192 x 7168 bf16: 28 us with 16
-// rows, 29 with 8, 30 with 32.
+// Lanes of a row: 16 up to 128 values, 32 up to 256, else a wave (63 matrices of 1408 x
+// 128 bf16 values: 18 us and back 13 by a wave a row, 7.2 and 7.1 by 16 lanes; 18 of 3343
+// x 256 14 and 11, 8.9 and 8.6 by 32).
+int lanes_of(int k) { return k <= 128 ? 16 : k <= 256 ? 32 : 64; }
+// Blocks with PER = 4 from which on these are taken; fewer leave CUs idle, and PER = 2
+// makes twice as many (3 x 613 x 1407 values the same). 8192 x 7168 bf16: 28 us with 4,
+// 29 with 2, 30 with 8.
 constexpr int64_t kWide = 1024;
 
 struct QArgs {
@@ -92,28 +95,34 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&v)[VEC], uint32_t& b
   return w;
 }
 
-// Block (matrix, rows of ROWS, span of 512 values), four waves of ROWS / 4 rows
-// each.
-template <class T, int ROWS, bool SWIGLU>
+// Rows of a workgroup: four waves, each of 64 / LANES groups of lanes.
+template <int LANES, int PER>
+constexpr int kRows = 4 * (64 / LANES) * PER;
+
+// Block (matrix, rows, span of 8 LANES values).
+template <class T, int LANES, int PER, bool SWIGLU>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
-  __shared__ uint32_t words[4][ROWS];
-  constexpr int PER = ROWS / 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int ROWS = kRows<LANES, PER>, GROUPS = 64 / LANES;
+  __shared__ uint32_t words[LANES / 16][ROWS];
+  const int lane = threadIdx.x & (LANES - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = wave * PER * GROUPS + (threadIdx.x & 63) / LANES;  // and every GROUPS rows
   const Block b(a);
   const int64_t mat = b.mat, r0 = b.rows * ROWS;
-  const int i0 = b.span * kSpan + lane * VEC;
+  const int i0 = (b.span * LANES + lane) * VEC;
   const T* src = static_cast<const T*>(a.src) + mat * a.mat;
   typename RawOf<T>::type raw[PER], raw2[SWIGLU ? PER : 1];
   int d[PER];  // lengths of the rows, 0 for none
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int64_t r = r0 + wave * PER + i;
+    const int64_t r = r0 + first + i * GROUPS;
     int64_t from = r < a.rows ? r : -1;
     if (a.perm && from >= 0) {
       from = a.perm[r];
       if (from >= a.n_src) from = -1;
     }
-    d[i] = __builtin_amdgcn_readfirstlane(from >= 0 ? a.k : 0);
+    d[i] = from >= 0 ? a.k : 0;
+    if constexpr (GROUPS == 1) d[i] = __builtin_amdgcn_readfirstlane(d[i]);
     const T* p = src + (from >= 0 ? from : 0) * a.ld;
     raw[i] = load8(p, i0, d[i]);
     if constexpr (SWIGLU) raw2[i] = load8(p + a.k, i0, d[i]);
@@ -131,7 +140,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
     }
     uint32_t byte;
     const uint32_t w = mx4_codes(v, byte);
-    const int row = wave * PER + i;
+    const int row = first + i * GROUPS;
     if (r0 + row < a.rows && i0 < a.kb * 32) {
       uint32_t* to = reinterpret_cast<uint32_t*>(codes + int64_t(row) * a.kb * 16 + i0 / 2);
       if (a.stream) {  // (the empty statements keep the two stores apart)
@@ -149,9 +158,9 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(QArgs a) {
     if ((lane & 15) == 0) words[lane >> 4][row] = s;
   }
   __syncthreads();
-  if (threadIdx.x < 4 * ROWS) {
+  if (threadIdx.x < LANES / 16 * ROWS) {
     const int g = threadIdx.x / ROWS, row = threadIdx.x % ROWS;
-    const int64_t kg = b.span * 4 + g;
+    const int64_t kg = b.span * (LANES / 16) + g;
     if (kg < a.kg && r0 + row < a.rows)
       reinterpret_cast<uint32_t*>(a.scales)[(mat * a.kg + kg) * a.rows + r0 + row] = words[g][row];
   }
@@ -169,29 +178,30 @@ __device__ __forceinline__ void mx4_values(uint32_t w, uint32_t byte, float (&v)
   for (int j = 0; j < VEC; ++j) v[j] = p[j >> 1][j & 1] * s;
 }
 
-constexpr int kDeqRows = 8;
-template <class T>
+constexpr int kDeqPer = 2;
+template <class T, int LANES>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(QArgs a) {
-  constexpr int PER = kDeqRows / 4;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int PER = kDeqPer, GROUPS = 64 / LANES;
+  const int lane = threadIdx.x & (LANES - 1), wave = threadIdx.x >> 6;
   const Block b(a);
-  const int64_t mat = b.mat, r0 = b.rows * kDeqRows + wave * PER;
-  const int i0 = b.span * kSpan + lane * VEC;
+  const int64_t mat = b.mat, r0 = b.rows * kRows<LANES, PER> + wave * PER * GROUPS +
+                                  (threadIdx.x & 63) / LANES;
+  const int i0 = (b.span * LANES + lane) * VEC;
   if (i0 >= a.k) return;
   const int64_t kg = i0 / 128, col = i0 / 2;
   uint32_t w[PER], sc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int64_t r = min(r0 + i, a.rows - 1);
+    const int64_t r = min(r0 + i * GROUPS, a.rows - 1);
     w[i] = *reinterpret_cast<const uint32_t*>(a.codes + (mat * a.rows + r) * a.kb * 16 + col);
     sc[i] = reinterpret_cast<const uint32_t*>(a.scales)[(mat * a.kg + kg) * a.rows + r];
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (r0 + i >= a.rows) return;
+    if (r0 + i * GROUPS >= a.rows) return;
     float v[VEC];
     mx4_values(w[i], (sc[i] >> (8 * ((i0 >> 5) & 3))) & 255u, v);
-    store8(static_cast<T*>(a.dst) + mat * a.mat + (r0 + i) * a.ld + i0, v, a.k - i0,
+    store8(static_cast<T*>(a.dst) + mat * a.mat + (r0 + i * GROUPS) * a.ld + i0, v, a.k - i0,
            a.stream);
   }
 }
@@ -210,7 +220,7 @@ QArgs q_args(const Mx4Args& p) {
   a.k = p.k;
   a.kb = (p.k + 31) / 32;
   a.kg = (a.kb + 3) / 4;
-  a.spans = (p.k + kSpan - 1) / kSpan;
+  a.spans = (p.k + lanes_of(p.k) * VEC - 1) / (lanes_of(p.k) * VEC);
   // (32 matrices of 4096 x 7168: codes 425 -> 407 us, values in bf16 400 -> 365)
   const int64_t out = p.dst ? int64_t(p.k) * (p.bf16 ? 2 : 4) : a.kb * 16;
   a.stream = p.mats * p.rows * out >= kFarBytes;
@@ -230,16 +240,46 @@ void in_launches(QArgs a, int64_t mats, int per, Go&& go) {
   }
 }
 
+template <class T, int LANES, int PER, bool SWIGLU>
+void quantize_by(const QArgs& a, int64_t mats, hipStream_t s) {
+  in_launches(a, mats, kRows<LANES, PER>, [&](const QArgs& b, dim3 grid) {
+    hipLaunchKernelGGL((mx4_quantize_kernel<T, LANES, PER, SWIGLU>), grid, dim3(256), 0, s, b);
+  });
+}
+template <class T, int LANES, bool SWIGLU>
+void quantize_with(const QArgs& a, int64_t mats, hipStream_t s) {
+  constexpr int rows = kRows<LANES, 4>;
+  if (mats * ((a.rows + rows - 1) / rows) * a.spans >= kWide)
+    quantize_by<T, LANES, 4, SWIGLU>(a, mats, s);
+  else
+    quantize_by<T, LANES, 2, SWIGLU>(a, mats, s);
+}
 template <class T, bool SWIGLU>
 void quantize(const QArgs& a, int64_t mats, hipStream_t s) {
-  if (mats * ((a.rows + 15) / 16) * a.spans >= kWide)
-    in_launches(a, mats, 16, [&](const QArgs& b, dim3 grid) {
-      hipLaunchKernelGGL((mx4_quantize_kernel<T, 16, SWIGLU>), grid, dim3(256), 0, s, b);
-    });
+  const int lanes = lanes_of(a.k);
+  if (lanes == 16)
+    quantize_with<T, 16, SWIGLU>(a, mats, s);
+  else if (lanes == 32)
+    quantize_with<T, 32, SWIGLU>(a, mats, s);
   else
-    in_launches(a, mats, 8, [&](const QArgs& b, dim3 grid) {
-      hipLaunchKernelGGL((mx4_quantize_kernel<T, 8, SWIGLU>), grid, dim3(256), 0, s, b);
-    });
+    quantize_with<T, 64, SWIGLU>(a, mats, s);
+}
+
+template <class T, int LANES>
+void dequantize_with(const QArgs& a, int64_t mats, hipStream_t s) {
+  in_launches(a, mats, kRows<LANES, kDeqPer>, [&](const QArgs& b, dim3 grid) {
+    hipLaunchKernelGGL((mx4_dequantize_kernel<T, LANES>), grid, dim3(256), 0, s, b);
+  });
+}
+template <class T>
+void dequantize(const QArgs& a, int64_t mats, hipStream_t s) {
+  const int lanes = lanes_of(a.k);
+  if (lanes == 16)
+    dequantize_with<T, 16>(a, mats, s);
+  else if (lanes == 32)
+    dequantize_with<T, 32>(a, mats, s);
+  else
+    dequantize_with<T, 64>(a, mats, s);
 }
 
 }  // namespace
@@ -256,12 +296,8 @@ hipError_t launch_mx4_quantize(const Mx4Args& p, hipStream_t s) {
 
 hipError_t launch_mx4_dequantize(const Mx4Args& p, hipStream_t s) {
   if (p.mats == 0 || p.rows == 0) return hipSuccess;
-  in_launches(q_args(p), p.mats, kDeqRows, [&](const QArgs& b, dim3 grid) {
-    if (p.bf16)
-      hipLaunchKernelGGL(mx4_dequantize_kernel<uint16_t>, grid, dim3(256), 0, s, b);
-    else
-      hipLaunchKernelGGL(mx4_dequantize_kernel<float>, grid, dim3(256), 0, s, b);
-  });
+  const QArgs a = q_args(p);
+  p.bf16 ? dequantize<uint16_t>(a, p.mats, s) : dequantize<float>(a, p.mats, s);
   return hipGetLastError();
 }
 
