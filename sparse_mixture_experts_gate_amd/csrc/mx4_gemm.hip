@@ -40,12 +40,12 @@ constexpr int kChunks = 8;          // blocks of a row per k-step, 16 bytes each
 constexpr int kRow = kChunks * 16;  // bytes of a row of a stage
 constexpr int kSubs = kChunks / 2;  // matrix instructions along a k-step
 
-// BM x BN tile in waves of WM x WN, NST LDS stages in the load ring.
-template <int BM_, int BN_, int WM_, int WN_, int NST_, bool B_NT_ = false>
+// BM x BN tile in waves of WM x WN (ALIKE waves on each), NST LDS stages in the load ring.
+template <int BM_, int BN_, int WM_, int WN_, int NST_, bool B_NT_ = false, int ALIKE = 1>
 struct MxTile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
   static constexpr bool B_NT = B_NT_;  // weights streamed past L2
-  static constexpr int WAVES_N = BN / WN, NWAVES = BM / WM * WAVES_N, NT = NWAVES * 64;
+  static constexpr int WAVES_N = BN / WN, NWAVES = BM / WM * WAVES_N * ALIKE, NT = NWAVES * 64;
   static constexpr int MI = WM / 32, NJ = WN / 32;
   static constexpr int RPP = NT / kChunks;  // rows covered by one pass of 16-byte loads
   static constexpr int A_LOADS = BM / RPP, B_LOADS = BN / RPP;
@@ -413,6 +413,55 @@ __device__ __forceinline__ void mx4_ring(uint8_t* lds, int first, int nb, int to
   vm_wait<0>();
 }
 
+// The k-loop of few tiles: 32 columns of weights a tile, so that four times as many CUs
+// stream them. The four waves load a quarter each, all multiply the whole tile, each on
+// its own matrix core and in the order of the other tiles (a row's sums are the same bits
+// in every tile), and wave g ends with columns 8 g .. of each 32. One barrier per k-step:
+// behind it the step's blocks are there and the stage before it is free. Latency-bound: a
+// row of 7168 by 4096 x 7168 11.8 us (a launch and its 16 MB 5.6), of which the 112 matrix
+// instructions one after the other are most: with the next step's blocks read ahead the
+// same, split over the waves 8.9, which would make a row's sums depend on the tile.
+template <class C, class NextOps, class Epilogue>
+__device__ __forceinline__ void mx4_thin_ring(uint8_t* lds, int first, int nb, int total,
+                                              NextOps&& next_ops, Epilogue&& epilogue) {
+  static_assert(C::NWAVES == 4 && C::MI == 1 && C::NJ == 1, "one tile, a quarter a wave");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  MLoader<C, std::remove_reference_t<NextOps>> ld(next_ops, lds_addr(lds), first, nb, total, wave);
+  auto load_step = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < C::NL; ++i) ld.load(st, i);
+    ld.advance();
+  };
+#pragma unroll
+  for (int j = 0; j < C::NST - 1; ++j) load_step(j);
+  int st = 0;
+  for (int tc = first; tc < total; tc += nb) {
+    f32x16_t acc = {};
+    const int nkc = epilogue.k_steps();
+    for (int kc = 0; kc < nkc; ++kc) {
+      vm_wait<C::NL*(C::NST - 2)>();
+      lds_barrier();
+      load_step(st == 0 ? C::NST - 1 : st - 1);
+      const uint8_t* s = lds + st * C::STAGE;
+      const int sa = word_of<C>(s, false, 0, lane), sb = word_of<C>(s, true, 0, lane);
+      i32x4_t a[kSubs], b[kSubs];
+#pragma unroll
+      for (int kk = 0; kk < kSubs; ++kk) {
+        a[kk] = block_of<C>(s, false, 0, kk, lane);
+        b[kk] = block_of<C>(s, true, 0, kk, lane);
+      }
+      acc = mma4<0>(a[0], b[0], acc, sa, sb);
+      acc = mma4<1>(a[1], b[1], acc, sa, sb);
+      acc = mma4<2>(a[2], b[2], acc, sa, sb);
+      acc = mma4<3>(a[3], b[3], acc, sa, sb);
+      st = st == C::NST - 1 ? 0 : st + 1;
+    }
+    epilogue(tc, wave, lane, acc);
+  }
+  vm_wait<0>();
+}
+
 // waves per SIMD the register budget is sized for
 template <class C>
 constexpr int kMinWaves = C::NWAVES >= 8 ? 2 : 1;
@@ -441,12 +490,58 @@ __global__ __launch_bounds__(C::NT, kMinWaves<C>) void mx4_gemm_kernel(MArgs a) 
   mx4_ring<C>(lds, first, nb, total, next_ops, ep);
 }
 
+template <class C>
+__global__ __launch_bounds__(C::NT) void mx4_thin_kernel(MArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::NST * C::STAGE];
+  __shared__ GroupTables gt;
+  build_group_tables(gt, a.offsets, a.G, a.rows, C::BM, (a.n + C::BN - 1) / C::BN);
+  const int total = gt.total, nb = min(static_cast<int>(gridDim.x), (total + 7) / 8 * 8);
+  if (static_cast<int>(blockIdx.x) >= nb) return;
+  const int first = xcd_logical_block(blockIdx.x, nb);
+  if (first >= total) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  auto next_ops = [&](int tile, MOps<C>& op) { tile_ops<C>(a, tile_of<C>(a, gt, tile), wave, op); };
+  struct Epilogue {
+    const MArgs& a;
+    const GroupTables& t;
+    __device__ int k_steps() const { return (a.kb + kChunks - 1) / kChunks; }
+    // columns 8 g + 4 h .. + 3 of row l % 32
+    __device__ void operator()(int tile, int g, int lane, const f32x16_t& acc) const {
+      const MTile c = tile_of<C>(a, t, tile);
+      const int r = c.m * C::BM + (lane & 31), col = c.n * C::BN + 8 * g + 4 * (lane >> 5);
+      if (r >= c.rows || col >= a.n) return;
+      const int64_t at = (c.row0 + r) * a.ldy + col;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = g & 1 ? +acc[4 + j] : +acc[j], hi = g & 1 ? +acc[12 + j] : +acc[8 + j];
+        v[j] = g & 2 ? hi : lo;
+      }
+      if (a.out_f32) {
+        put4<false>(static_cast<float*>(a.y) + at, a.vec, a.n - col, v);
+        return;
+      }
+      uint16_t* p = static_cast<uint16_t*>(a.y) + at;
+      const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      if (a.vec && a.n - col >= 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < a.n - col) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  } ep{a, gt};
+  mx4_thin_ring<C>(lds, first, nb, total, next_ops, ep);
+}
+
 // ---- choice of the kernel -------------------------------------------------------
 
 using TileBig = MxTile<256, 256, 128, 64, 2>;      // 8 waves
 using TileWide = MxTile<128, 256, 64, 64, 3>;      // 8 waves
 using TileFlat = MxTile<64, 256, 32, 64, 3>;       // 8 waves
 using TileLow = MxTile<32, 128, 32, 32, 6, true>;  // 4 waves, weights streamed past L2
+using TileThin = MxTile<32, 32, 32, 32, 4, true, 4>;  // the same, 4 waves alike
 
 template <class C>
 int64_t tile_bound(const MArgs& a) {
@@ -454,10 +549,9 @@ int64_t tile_bound(const MArgs& a) {
   return (a.rows / C::BM + (a.rows < a.G ? a.rows : a.G)) * tn;
 }
 
-template <class C>
+template <auto K, class C>
 void launch(const MArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx4_gemm_kernel<C>), dim3(grid_of<mx4_gemm_kernel<C>>(C::NT, tile_bound<C>(a))),
-                     dim3(C::NT), 0, s, a);
+  hipLaunchKernelGGL(K, dim3(grid_of<K>(C::NT, tile_bound<C>(a))), dim3(C::NT), 0, s, a);
 }
 
 // Time model of a tile (microseconds), fitted to measured products, per k-step: `one`
@@ -473,10 +567,11 @@ constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.76, 1.22, 7.0},
                                {64, 256, 0.7, 0.95, 0.36, 1.8},
                                {32, 128, 0.34, 0.38, 0.21, 1.1}};
 
-// The rule: the tile with the least modelled time. Row counts per group live on the
-// device, so the expected number of row tiles stands in for them: at least one per
-// group with rows, else rows / BM and half a tile per group; with more than one group
-// half a round more than the tiles fill. Measured (us, 256 / 128 / 64 / 32 rows):
+// The rule: 32 x 32 tiles while they are no more than the CUs, else the tile with the
+// least modelled time. Row counts per group live on the device, so the expected number
+// of row tiles stands in for them: at least one per group with rows, else rows / BM and
+// half a tile per group; with more than one group half a round more than the tiles fill.
+// Measured (us, 256 / 128 / 64 / 32 rows):
 //   x [16, 4096], 1 x 4096                    25 / 15 / 13 / 10
 //   x [512, 2048], 8 x 1408                   17 / 12 / 10 / 8
 //   x [1024, 7168], 1 x 4096                  47 / 30 / 26 / 48
@@ -489,18 +584,29 @@ constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.76, 1.22, 7.0},
 //   x [24576, 2048], 64 x 2816               119 / 122 / 158 / 271
 //   x [128, 7168], 128 of 256 groups x 4096   32 rows: 276 (weights through the caches
 //                                            325), 64: 328
+// 32 x 32 against 32 x 128:
+//   x [1, 7168], 1 x 4096, 128 tiles         11.8 / 13.4
+//   x [16, 7168], 2 x 4096, 256 tiles        12.5 / 15.4
+//   x [64, 2048], 32 x 256, 256 tiles         6.9 / 7.8
+//   x [6, 2048], 6 x 1408, 264 tiles          7.5 / 7.8
+//   x [128, 7168], 1 x 4096, 512 tiles       14.8 / 15.0
+//   x [8, 2048], 8 x 2816, 704 tiles          9.5 / 8.8
 // and where it is wrong, the tile it takes first:
 //   x [2048, 7168], 32 x 4096                 128 rows: 124, 64: 109
 int choose(const MArgs& a) {
   const double touched = static_cast<double>(a.rows < a.G ? a.rows : a.G);
+  auto row_tiles = [&](int bm) {
+    const double mt = a.G == 1 ? std::ceil(a.rows / static_cast<double>(bm))
+                               : a.rows / static_cast<double>(bm) + 0.5 * touched;
+    return mt > touched ? mt : touched;
+  };
+  if ((a.n + TileThin::BN - 1) / TileThin::BN * row_tiles(TileThin::BM) <= 256) return 4;
   const double nk = (a.kb + kChunks - 1) / kChunks;
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < 4; ++i) {
     const TileCost& t = kCosts[i];
-    const double mt = a.G == 1 ? std::ceil(a.rows / static_cast<double>(t.bm))
-                               : a.rows / static_cast<double>(t.bm) + 0.5 * touched;
-    const double share = (a.n + t.bn - 1) / t.bn * (mt > touched ? mt : touched) / 256;
+    const double share = (a.n + t.bn - 1) / t.bn * row_tiles(t.bm) / 256;
     const double rounds = a.G == 1 ? std::ceil(share) : share > 0.5 ? share + 0.5 : 1.0;
     const double step = share <= 0.5 ? t.idle : a.G == 1 ? t.one : t.many;
     const double us = rounds * (nk * step + t.fixed);
@@ -533,13 +639,15 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& p, hipStream_t s) {
   a.vec = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
   const int c = choose(a);
   if (c == 0)
-    launch<TileBig>(a, s);
+    launch<mx4_gemm_kernel<TileBig>, TileBig>(a, s);
   else if (c == 1)
-    launch<TileWide>(a, s);
+    launch<mx4_gemm_kernel<TileWide>, TileWide>(a, s);
   else if (c == 2)
-    launch<TileFlat>(a, s);
+    launch<mx4_gemm_kernel<TileFlat>, TileFlat>(a, s);
+  else if (c == 3)
+    launch<mx4_gemm_kernel<TileLow>, TileLow>(a, s);
   else
-    launch<TileLow>(a, s);
+    launch<mx4_thin_kernel<TileThin>, TileThin>(a, s);
   return hipGetLastError();
 }
 

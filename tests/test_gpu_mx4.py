@@ -301,3 +301,29 @@ def test_products_at_the_ends_of_the_range(a, b):
     y = host(lin.forward(torch.full((5, 32), 2.0 ** a, device=DEV), off, out_dtype=torch.float32))
     with np.errstate(over="ignore"):
         assert (y == np.float32(2.0 ** (a + b + 5))).all()
+
+
+@pytest.mark.parametrize("rows,G,n,k", [
+    (8, 8, 2816, 300), (64, 32, 1030, 257), (33, 4, 2817, 96), (100, 7, 2000, 1000), (40, 1, 5000, 70)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_products_of_few_rows_in_many_tiles(rows, G, n, k, out):
+    """Past one 32 x 32 tile for each CU: 32 x 128 tiles."""
+    _check_product(rows, G, n, k, out=out, seed=11)
+
+
+@pytest.mark.parametrize("n", [4096, 4100, 9000])
+def test_rows_outside_the_groups_of_few_rows(n):
+    """Both tiles of 32 rows: rows and columns around the outputs are left as they were."""
+    import sparse_mixture_experts_gate_amd as M
+    rows, G, k = 40, 2, 520
+    x, lin = _rand(1, rows, k), M.MX4Linear.from_weight(_rand(2, G, n, k))
+    off = torch.tensor([3, 20, 37], dtype=torch.int32, device=DEV)
+    codes, scales = M.mx4_quantize(x)
+    for out, dt in ((M.MOE_DT_F32, torch.float32), (M.MOE_DT_BF16, torch.bfloat16)):
+        wide = torch.full((rows, n + 5), 7.0, device=DEV, dtype=dt)
+        desc = M.MoeMx4GemmDesc(rows=rows, n_groups=G, n=n, k=k, out_dtype=out, ld_y=n + 5)
+        M.moe_mx4_gemm(desc, codes, scales, lin.codes, lin.scales, off, wide[:, 2:2 + n])
+        want = lin.forward(x, off, out_dtype=dt)
+        assert torch.equal(wide[3:37, 2:2 + n], want[3:37])
+        wide[3:37, 2:2 + n] = 7.0
+        assert bool((wide == 7).all())
