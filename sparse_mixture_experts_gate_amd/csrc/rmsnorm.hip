@@ -191,11 +191,48 @@ struct RmsBwdArgs {
   const float* rstd;
   const void* dr;
   void* dx;
-  float* part;  // [gridDim.x][d] partial dweight; NULL: not wanted
+  float* part;  // [blocks][d] partial dweight; NULL: not wanted, or
+  float* dw;    // dweight from blocks of this launch behind the rows' own
+  int blocks;   // of rows
   int64_t n, ldx, ldr, ldy, lds;
   int d;
   bool stream;  // row outputs past the caches
 };
+
+// dweight of 32 columns: the block's half-waves take rows of dy and x each, eight of both
+// in flight, and their sums are added in order. For few rows, beside the blocks that write
+// dx; it reads dy itself, which dx must not overwrite.
+template <class T, int HALVES>
+__device__ void dweight_columns(const RmsBwdArgs& a, int block) {
+  __shared__ float red[HALVES][32];
+  const int half = threadIdx.x >> 5, lane = threadIdx.x & 31, col = block * 32 + lane;
+  const int n = static_cast<int>(a.n);
+  float s = 0.0f;
+  if (col < a.d) {
+    const T* x = static_cast<const T*>(a.x) + col;
+    const T* dy = static_cast<const T*>(a.dy) + col;
+    constexpr int N = 8;
+    for (int r0 = half; r0 < n; r0 += N * HALVES) {
+      float v[N], g[N], rs[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = min(r0 + i * HALVES, n - 1);
+        v[i] = one_value(x[row * a.ldx]);
+        g[i] = one_value(dy[row * a.ldy]);
+        rs[i] = a.rstd[row];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (r0 + i * HALVES < n) s += g[i] * (v[i] * rs[i]);
+    }
+  }
+  red[half][lane] = s;
+  __syncthreads();
+  if (half || col >= a.d) return;
+#pragma unroll
+  for (int h = 1; h < HALVES; ++h) s += red[h][lane];
+  a.dw[col] = s;
+}
 
 // A row group (NW waves) takes rows slot, slot + slots, ... and keeps the column
 // sums of dy z for its columns in registers over all of them; each block then
@@ -213,8 +250,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_bwd_kernel(RmsBwd
   constexpr bool LATE = RES && CH == 4 && sizeof(T) == 4;
   __shared__ float slot[2][NW];
   const int lane = threadIdx.x & (LANES - 1);
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    dweight_columns<T, (NW == 1 ? 4 : NW) * 2>(a, blockIdx.x - a.blocks);
+    return;
+  }
   const int64_t first = int64_t(blockIdx.x) * GROUPS + (NW == 1 ? threadIdx.x >> 6 : 0);
-  const int64_t stride = int64_t(gridDim.x) * GROUPS;
+  const int64_t stride = int64_t(a.blocks) * GROUPS;
   float aw[CH][VEC], w[CH][VEC];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -479,9 +520,10 @@ void bwd_dispatch(const RmsBwdArgs& a, int parts, hipStream_t s) {
     return;
   }
   const RowShape r = row_shape(a.d);
+  const int grid = parts + (a.dw ? (a.d + 31) / 32 : 0);
 #define RMS_CASE(NW, CH)                                                          \
   if (r.nw == NW && r.ch == CH) {                                                 \
-    hipLaunchKernelGGL((rms_bwd_kernel<T, NW, CH, RES>), dim3(parts),             \
+    hipLaunchKernelGGL((rms_bwd_kernel<T, NW, CH, RES>), dim3(grid),              \
                        dim3(NW == 1 ? 256 : NW * 64), 0, s, a);                   \
     return;                                                                       \
   }
@@ -508,6 +550,10 @@ int rmsnorm_backward_parts(int64_t n, int d) {
 }
 
 namespace {
+// Rows up to which dweight comes from the same launch. With dresidual, one launch / two (us,
+// replayed graphs): bf16 128 x 1407 3.7 / 7.0, 256 x 7168 5.5 / 11.5, 512 x 512 5.9 / 6.5, 512
+// x 7168 10.9 / 13.6, 1003 x 1407 13.0 / 9.8; fp32 512 x 7168 17.5 / 17.0.
+constexpr int64_t kOneLaunch = 512;
 bool streamed(const RmsArgs& p) { return p.n * p.d * (p.bf16 ? 2 : 4) >= kStreamBytes; }
 }  // namespace
 
@@ -524,15 +570,16 @@ hipError_t launch_rmsnorm_forward(const RmsArgs& p, hipStream_t s) {
 
 hipError_t launch_rmsnorm_backward(const RmsArgs& p, float* dw, float* part, hipStream_t s) {
   const int parts = rmsnorm_backward_parts(p.n, p.d);
+  const bool one = dw && p.n > 0 && p.n <= kOneLaunch && p.d <= kMaxRow && p.s != p.y;
   if (p.n > 0) {
-    const RmsBwdArgs a{p.y, p.x, p.w, p.rstd, p.r, p.s, dw ? part : nullptr,
-                       p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, streamed(p)};
+    const RmsBwdArgs a{p.y, p.x, p.w, p.rstd, p.r, p.s, dw && !one ? part : nullptr,
+                       one ? dw : nullptr, parts, p.n, p.ldx, p.ldr, p.ldy, p.lds, p.d, streamed(p)};
     if (p.bf16)
       p.r ? bwd_dispatch<uint16_t, true>(a, parts, s) : bwd_dispatch<uint16_t, false>(a, parts, s);
     else
       p.r ? bwd_dispatch<float, true>(a, parts, s) : bwd_dispatch<float, false>(a, parts, s);
   }
-  if (dw)
+  if (dw && !one)
     hipLaunchKernelGGL(rms_sum_parts_kernel, dim3((p.d + 31) / 32), dim3(1024), 0, s, part,
                        p.n > 0 ? parts : 0, p.d, dw);
   return hipGetLastError();

@@ -87,6 +87,10 @@ __device__ __forceinline__ void unpack(const Raw32& r, float (&v)[VEC], int) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(r.w[j]);
 }
+__device__ __forceinline__ float one_value(uint16_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ float one_value(float v) { return v; }
 // Two fp32 -> bf16 to nearest even (one instruction; NaN stays NaN).
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));

@@ -198,3 +198,27 @@ def test_more_rows_than_a_launch_counts():
     d = M.RMSNorm(None, 0.0).backward(x, x, o["rstd"])
     # a row of one value: its norm does not move but for a few u of 3 * 1/3
     assert bool((d["dx"].abs() <= 16 * U).all())
+
+
+@pytest.mark.parametrize("n", [511, 512, 513])
+@pytest.mark.parametrize("d", [31, 700, 1500, 2300, 4500, 9000])
+def test_both_ways_to_dweight(n, d):
+    """From the rows' own launch and from partial rows; dresidual's place for dx."""
+    import sparse_mixture_experts_gate_amd as M
+    for dt in ("bf16", "f32"):
+        x, dy, dr = (_rand(s, n, d).to(DT[dt]) for s in (1, 2, 3))
+        op = M.RMSNorm(_rand(4, d, scale=0.2, shift=1.0))
+        f = op.forward(x)
+        o = op.backward(dy, x, f["rstd"], dr)
+        _check_backward(o, dy, x, f["rstd"], op.weight, dr, dt)
+        again = op.backward(dy, x, f["rstd"], dr)
+        assert torch.equal(again["dweight"], o["dweight"])
+        desc = op._desc(x)
+        for place in (dr.clone(), dy.clone()):
+            a, b = (place, dy) if torch.equal(place, dr) else (dr, place)
+            dw = torch.empty(d, device="cuda:0")
+            ws = torch.empty(M.moe_rmsnorm_backward_workspace_size(desc), dtype=torch.uint8,
+                             device="cuda:0")
+            M.moe_rmsnorm_backward(desc, b, x, op.weight, f["rstd"], a, place, dw, ws)
+            assert torch.equal(place, o["dx"])
+            _check_backward({"dx": place, "dweight": dw}, dy, x, f["rstd"], op.weight, dr, dt)
