@@ -75,7 +75,7 @@ struct MArgs {
   int G, n;
   int kb;   // blocks of a row
   int kg;   // words of scales of a row
-  int out_f32, vec;
+  int out_f32;
 };
 
 // Swizzled position of a row's chunk: 16 lanes that one 128-bit LDS access serves
@@ -240,22 +240,22 @@ __device__ __forceinline__ f32x16_t mma4(i32x4_t a, i32x4_t b, f32x16_t c, int s
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(B, A, c, kFp4, kFp4, KK, sb, KK, sa);
 }
 
-// Stores eight adjacent values of a row, of which `cnt` exist; all of them, in whole
-// 16-byte accesses, where FULL.
+// Stores eight (bf16) or four adjacent values of a row, of which `cnt` > 0 exist; all of
+// them where FULL. Rows start at any element, which 16-byte stores take (13151 x 256 rows,
+// 39 groups of 953: 56 us in two-byte stores, 22 so).
 template <bool FULL>
-__device__ __forceinline__ void put8(uint16_t* p, bool vec, int cnt, const uint32_t (&w)[4]) {
-  if (FULL || (vec && cnt >= 8)) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-  }
+__device__ __forceinline__ void put8(uint16_t* p, int cnt, const uint32_t (&w)[4]) {
+  const u32x4_any_t r = {w[0], w[1], w[2], w[3]};
+  if (FULL || cnt >= 8)
+    *reinterpret_cast<u32x4_any_t*>(p) = r;
+  else
+    store_end(p, r, cnt);
 }
 template <bool FULL>
-__device__ __forceinline__ void put4(float* p, bool vec, int cnt, const float (&v)[4]) {
-  if (FULL || (vec && cnt >= 4)) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void put4(float* p, int cnt, const float (&v)[4]) {
+  typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+  if (FULL || cnt >= 4) {
+    *reinterpret_cast<f32x4_any_t*>(p) = f32x4_any_t{v[0], v[1], v[2], v[3]};
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -284,7 +284,7 @@ __device__ __forceinline__ void store_part(const MArgs& a, const MTile& c, int w
           const int col = col0 + 8 * g + 4 * h;
           const float v[4] = {x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
           if (FULL || (r < c.rows && col < a.n))
-            put4<FULL>(static_cast<float*>(a.y) + row + col, a.vec, a.n - col, v);
+            put4<FULL>(static_cast<float*>(a.y) + row + col, a.n - col, v);
         }
       } else {
 #pragma unroll
@@ -300,7 +300,7 @@ __device__ __forceinline__ void store_part(const MArgs& a, const MTile& c, int w
           }
           const int col = col0 + 16 * q + 8 * h;
           if (FULL || (r < c.rows && col < a.n))
-            put8<FULL>(static_cast<uint16_t*>(a.y) + row + col, a.vec, a.n - col, w);
+            put8<FULL>(static_cast<uint16_t*>(a.y) + row + col, a.n - col, w);
         }
       }
     }
@@ -311,7 +311,7 @@ __device__ __forceinline__ void store_part(const MArgs& a, const MTile& c, int w
 template <class C>
 __device__ __forceinline__ void store_tile(const MArgs& a, const MTile& c, int wm, int wn, int lane,
                                            const f32x16_t (&acc)[C::MI][C::NJ]) {
-  if (a.vec && c.m * C::BM + (wm + 1) * C::WM <= c.rows && c.n * C::BN + (wn + 1) * C::WN <= a.n)
+  if (c.m * C::BM + (wm + 1) * C::WM <= c.rows && c.n * C::BN + (wn + 1) * C::WN <= a.n)
     store_part<C, true>(a, c, wm, wn, lane, acc);
   else
     store_part<C, false>(a, c, wm, wn, lane, acc);
@@ -518,18 +518,15 @@ __global__ __launch_bounds__(C::NT) void mx4_thin_kernel(MArgs a) {
         v[j] = g & 2 ? hi : lo;
       }
       if (a.out_f32) {
-        put4<false>(static_cast<float*>(a.y) + at, a.vec, a.n - col, v);
+        put4<false>(static_cast<float*>(a.y) + at, a.n - col, v);
         return;
       }
       uint16_t* p = static_cast<uint16_t*>(a.y) + at;
-      const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-      if (a.vec && a.n - col >= 4) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < a.n - col) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-      }
+      const u32x4_any_t w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), 0, 0};
+      if (a.n - col >= 4)
+        *reinterpret_cast<u32x2_any2_t*>(p) = u32x2_any2_t{w[0], w[1]};
+      else
+        store_end(p, w, a.n - col);
     }
   } ep{a, gt};
   mx4_thin_ring<C>(lds, first, nb, total, next_ops, ep);
@@ -636,7 +633,6 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& p, hipStream_t s) {
   a.kb = (p.k + 31) / 32;
   a.kg = (a.kb + 3) / 4;
   a.out_f32 = p.out_f32;
-  a.vec = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
   const int c = choose(a);
   if (c == 0)
     launch<mx4_gemm_kernel<TileBig>, TileBig>(a, s);
