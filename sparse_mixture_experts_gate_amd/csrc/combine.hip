@@ -4,8 +4,8 @@
 // Memory-bound: a group of LANES lanes owns a token, 8 adjacent values per lane
 // and chunk; its places and weights are wave-uniform, and the rows of up to eight
 // places are in flight together. 8192 x 8 rows of 7168 bf16 values: 207 us, 1.06 GB at
-// 5.1 TB/s; the gradients 403 us, 2.0 GB at 5.0; 64 x 8 rows of 4096: 4.8 and 8.5 us
-// (gradients with one place's row at a time 9.9, with four 9.1; large ones the same).
+// 5.1 TB/s; the gradients 403 us, 2.0 GB at 5.0. Few tokens: latency; gradients of 64 x 8
+// rows of 4096 by 256 lanes a token 8.7 us, with one place's row at a time 9.9.
 #include "device_common.h"
 #include "internal.h"
 #include "row_io.h"
@@ -72,10 +72,15 @@ __device__ __forceinline__ void add_rows(const TokArgs& a, const Places& p, uint
   }
 }
 
+// Threads of a workgroup whose groups of LANES lanes own a token each.
+template <int LANES>
+constexpr int kThreads = LANES < 256 ? 256 : LANES;
+
 template <class T, int LANES>
-__global__ __launch_bounds__(256) void token_combine_kernel(TokArgs a) {
+__global__ __launch_bounds__(kThreads<LANES>) void token_combine_kernel(TokArgs a) {
+  constexpr int GROUPS = kThreads<LANES> / LANES;
   const int lane = threadIdx.x & (LANES - 1);
-  const int64_t t = a.t0 + int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t t = a.t0 + int64_t(blockIdx.x) * GROUPS + threadIdx.x / LANES;
   if (t >= a.T) return;  // whole waves
   const Places p = places_of(a, t, threadIdx.x & 63);
   for (int i0 = lane * VEC; i0 < a.d; i0 += LANES * VEC) {
@@ -133,8 +138,8 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
 // several sweeps over them. A wave's part of slot k's <dy, row> is lane k's; the waves'
 // are added through LDS in wave order.
 template <class T, int LANES>
-__global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
-  constexpr int GROUPS = 256 / LANES, WAVES = LANES / 64;
+__global__ __launch_bounds__(kThreads<LANES>) void token_combine_bwd_kernel(TokArgs a) {
+  constexpr int GROUPS = kThreads<LANES> / LANES, WAVES = LANES / 64;
   __shared__ float part[GROUPS][WAVES][kMaxK];
   const int lane = threadIdx.x & (LANES - 1), group = threadIdx.x / LANES;
   const int wave = lane >> 6;
@@ -159,10 +164,35 @@ __global__ __launch_bounds__(256) void token_combine_bwd_kernel(TokArgs a) {
   if (!a.dw) return;
   __syncthreads();
   if (real && lane < a.K) {
-    float s = part[group][0][lane];
+    // 1024 lanes are four sweeps of 256 side by side: added as those are one after the
+    // other, dweight is the same bits however many tokens there are
+    constexpr int FIRST = WAVES < 4 ? WAVES : 4;
+    float s = 0.0f;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += part[group][w][lane];
+    for (int w = 0; w < FIRST; ++w) {
+      float q = part[group][w][lane];
+#pragma unroll
+      for (int j = w + 4; j < WAVES; j += 4) q += part[group][j][lane];
+      s = w ? s + q : q;
+    }
     a.dw[t * a.K + lane] = s;
+  }
+}
+
+template <class T, int LANES>
+void launch_with(TokArgs a, bool backward, hipStream_t s) {
+  constexpr int GROUPS = kThreads<LANES> / LANES;
+  // (work items of a launch are counted in 32 bits)
+  const int64_t T_ = a.T, per = kMaxBlocks * 256 / kThreads<LANES> * GROUPS;
+  for (int64_t t = 0; t < T_; t += per) {
+    const int64_t n = T_ - t < per ? T_ - t : per;
+    a.t0 = t;
+    a.T = t + n;
+    const dim3 grid(static_cast<unsigned>((n + GROUPS - 1) / GROUPS)), threads(kThreads<LANES>);
+    if (backward)
+      hipLaunchKernelGGL((token_combine_bwd_kernel<T, LANES>), grid, threads, 0, s, a);
+    else
+      hipLaunchKernelGGL((token_combine_kernel<T, LANES>), grid, threads, 0, s, a);
   }
 }
 
@@ -171,28 +201,18 @@ void launch(const CombineArgs& p, bool backward, hipStream_t s) {
   TokArgs a{p.yp, p.inv, p.w, p.base, p.y, p.dw, 0, p.T, p.rows, p.ldt, p.ldp, p.K, p.d, false};
   a.stream = (backward ? p.rows : p.T) * p.d * int64_t(sizeof(T)) >= kFarBytes;
   // a wave takes rows that its lanes hold in one chunk each: 4096 tokens of 8 places,
-  // rows of 256 bf16 values 5.0 us and 10.3 backward (a block per token 6.1 and 19.1), of
-  // 512 6.6 and 13.0 (7.5, 17.4), of 1024 13.9 and 24.4 (13.9, 24.9); 64 tokens of 1024
-  // 4.7 and 8.0 (3.6, 5.6)
-  const bool narrow = p.d <= 512;
-  const int64_t per = kMaxBlocks * (narrow ? 4 : 1);
-  for (int64_t t = 0; t < p.T; t += per) {
-    const int64_t n = p.T - t < per ? p.T - t : per;
-    a.t0 = t;
-    a.T = t + n;
-    const dim3 grid(static_cast<unsigned>(narrow ? (n + 3) / 4 : n));
-    if (!backward) {
-      if (narrow)
-        hipLaunchKernelGGL((token_combine_kernel<T, 64>), grid, dim3(256), 0, s, a);
-      else
-        hipLaunchKernelGGL((token_combine_kernel<T, 256>), grid, dim3(256), 0, s, a);
-    } else {
-      if (narrow)
-        hipLaunchKernelGGL((token_combine_bwd_kernel<T, 64>), grid, dim3(256), 0, s, a);
-      else
-        hipLaunchKernelGGL((token_combine_bwd_kernel<T, 256>), grid, dim3(256), 0, s, a);
-    }
-  }
+  // rows of 256 bf16 values 5.0 us and 10.3 backward (a block of 256 per token 6.1 and 19.1),
+  // of 512 6.6 and 13.0 (7.5, 17.4), of 1024 13.9 and 24.4 (13.9, 24.9); 64 tokens of 1024
+  // 4.7 and 8.0 (3.6, 5.6).
+  // Longer rows that 1024 lanes hold, of no more tokens than CUs, take those: 64 tokens of 4096 4.2 and 7.1
+  // (256 lanes 4.9 and 8.7), of 7168 5.3 and 7.9 (7.3, 14.4), 256 of 7168 6.2 and 12.1 (8.5,
+  // 18.5), 512 of 4096 6.8 and 17.0 (7.2, 15.8); 64 of 2048 3.7 and 6.8 (3.8, 5.7).
+  if (p.d <= 512)
+    launch_with<T, 64>(a, backward, s);
+  else if (p.d > 2048 && p.d <= 8192 && p.T <= 256)
+    launch_with<T, 1024>(a, backward, s);
+  else
+    launch_with<T, 256>(a, backward, s);
 }
 
 }  // namespace

@@ -250,3 +250,29 @@ def test_both_sides_of_one_launch(T, K):
         n = int(off[-1])
         assert torch.equal(o["rows"][:n], x[torch.from_numpy(perm[:n].astype(np.int64)).to(DEV)])
         _check_return(T, K, d, "f32", idx, 40, None, True, False)
+
+
+@pytest.mark.parametrize("T,d", [(256, 2056), (257, 2056), (260, 7168), (300, 4099), (20, 2049)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_long_rows_by_few_and_by_more_tokens(T, d, dt):
+    """A token's row by 1024 lanes and by 256."""
+    _check_return(T, 5, d, dt, _idx(T, T, 5, 30, 0.3), 30, None, True, True)
+
+
+@pytest.mark.parametrize("d", [100, 513, 2056, 4099, 7168, 8192, 8200])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_token_s_gradients_do_not_depend_on_the_others(d, dt):
+    import sparse_mixture_experts_gate_amd as M
+    T, K = 300, 4
+    inv = torch.randperm(T * K, device=DEV).int().reshape(T, K)
+    rows, dy = _rows(1, T * K, d, dt), _rows(2, T, d, dt)
+    w = torch.rand(T, K, device=DEV)
+    many = M.TokenDispatch.combine_grad(dy, rows, inv, w)
+    y = M.TokenDispatch.combine(rows, inv, w)
+    for n in (1, 7, 256):
+        some = inv[:n].reshape(-1).long()
+        own = torch.arange(n * K, device=DEV).int().reshape(n, K)
+        few = M.TokenDispatch.combine_grad(dy[:n], rows[some], own, w[:n].contiguous())
+        assert torch.equal(few["dweight"], many["dweight"][:n])
+        assert torch.equal(few["drows"], many["drows"][some])
+        assert torch.equal(M.TokenDispatch.combine(rows[some], own, w[:n].contiguous()), y[:n])
