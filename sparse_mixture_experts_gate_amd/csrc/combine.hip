@@ -204,9 +204,10 @@ void launch(const CombineArgs& p, bool backward, hipStream_t s) {
   // rows of 256 bf16 values 5.0 us and 10.3 backward (a block of 256 per token 6.1 and 19.1),
   // of 512 6.6 and 13.0 (7.5, 17.4), of 1024 13.9 and 24.4 (13.9, 24.9); 64 tokens of 1024
   // 4.7 and 8.0 (3.6, 5.6).
-  // Longer rows that 1024 lanes hold, of no more tokens than CUs, take those: 64 tokens of 4096 4.2 and 7.1
-  // (256 lanes 4.9 and 8.7), of 7168 5.3 and 7.9 (7.3, 14.4), 256 of 7168 6.2 and 12.1 (8.5,
-  // 18.5), 512 of 4096 6.8 and 17.0 (7.2, 15.8); 64 of 2048 3.7 and 6.8 (3.8, 5.7).
+  // Longer rows that 1024 lanes hold, of no more tokens than CUs, take those: 64 tokens of
+  // 4096 4.2 and 7.1 (256 lanes 4.9 and 8.7), of 7168 5.3 and 7.9 (7.3, 14.4), 256 of 7168
+  // 6.2 and 12.1 (8.5, 18.5), 512 of 4096 6.8 and 17.0 (7.2, 15.8); 64 of 2048 3.7 and 6.8
+  // (3.8, 5.7).
   if (p.d <= 512)
     launch_with<T, 64>(a, backward, s);
   else if (p.d > 2048 && p.d <= 8192 && p.T <= 256)

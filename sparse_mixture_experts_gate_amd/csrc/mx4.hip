@@ -3,10 +3,10 @@
 //
 // Memory-bound: a lane holds 8 adjacent values (one word of codes), four lanes a
 // block, 16 lanes four blocks, whose scale bytes make one word. LANES lanes take a row,
-// or 512 values of one; a workgroup takes PER rows for each, so that the scale words of a column of blocks,
-// which lie row by row, leave as one run of ROWS words and not one by one from
-// several XCDs. bf16 rows of 8192 x 7168: 28 us, 148 MB at 5.3 TB/s; 32 matrices of 4096
-// x 7168: 407 us, 2.4 GB at 5.8, and back 363 us at 6.5.
+// or 512 values of one; a workgroup takes PER rows for each, so that the scale words of a
+// column of blocks, which lie row by row, leave as one run of words and not one by one
+// from several XCDs. bf16 rows of 8192 x 7168: 28 us, 148 MB at 5.3 TB/s; 32 matrices of
+// 4096 x 7168: 407 us, 2.4 GB at 5.8, and back 363 us at 6.5.
 #include "device_common.h"
 #include "internal.h"
 #include "row_io.h"
