@@ -50,10 +50,27 @@ __device__ __forceinline__ int next_slot(uint64_t& m) {
   return k;
 }
 
+// A token row's chunk that is loaded before those of its places and put in order behind
+// their loads (in front of them, its wait would stand before theirs: a return of 4096 x 8
+// rows of 7168, one in eight here, 32.9 us, 31.8 so).
+template <class T>
+struct Early {
+  typename RawOf<T>::type raw;
+  bool waits = false;
+  __device__ __forceinline__ void load(const void* row, int64_t at, int i0, int d) {
+    raw = load8(static_cast<const T*>(row) + at, i0, d);
+    waits = true;
+  }
+  __device__ __forceinline__ void get(float (&v)[VEC], int cnt) {
+    if (waits) unpack(raw, v, cnt);
+    waits = false;
+  }
+};
+
 // acc += w row over the next N slots, all loads first.
 template <class T, int N>
 __device__ __forceinline__ void add_rows(const TokArgs& a, const Places& p, uint64_t& m, int i0,
-                                         float (&acc)[VEC]) {
+                                         Early<T>& base, float (&acc)[VEC]) {
   typename RawOf<T>::type r[N];
   float w[N];
 #pragma unroll
@@ -63,6 +80,7 @@ __device__ __forceinline__ void add_rows(const TokArgs& a, const Places& p, uint
     w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k));
     r[i] = load8(static_cast<const T*>(a.yp) + at * a.ldp, i0, a.d);
   }
+  base.get(acc, a.d - i0);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float v[VEC];
@@ -85,13 +103,15 @@ __global__ __launch_bounds__(kThreads<LANES>) void token_combine_kernel(TokArgs 
   const Places p = places_of(a, t, threadIdx.x & 63);
   for (int i0 = lane * VEC; i0 < a.d; i0 += LANES * VEC) {
     float acc[VEC] = {};
-    if (a.base) unpack(load8(static_cast<const T*>(a.base) + t * a.ldt, i0, a.d), acc, a.d - i0);
+    Early<T> base;
+    if (a.base) base.load(a.base, t * a.ldt, i0, a.d);
     uint64_t m = p.mask;
     int left = __popcll(m);
-    for (; left >= 8; left -= 8) add_rows<T, 8>(a, p, m, i0, acc);
-    if (left & 4) add_rows<T, 4>(a, p, m, i0, acc);
-    if (left & 2) add_rows<T, 2>(a, p, m, i0, acc);
-    if (left & 1) add_rows<T, 1>(a, p, m, i0, acc);
+    for (; left >= 8; left -= 8) add_rows<T, 8>(a, p, m, i0, base, acc);
+    if (left & 4) add_rows<T, 4>(a, p, m, i0, base, acc);
+    if (left & 2) add_rows<T, 2>(a, p, m, i0, base, acc);
+    if (left & 1) add_rows<T, 1>(a, p, m, i0, base, acc);
+    base.get(acc, a.d - i0);
     store8(static_cast<T*>(a.y) + t * a.ldt + i0, acc, a.d - i0, a.stream);
   }
 }
@@ -100,7 +120,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void token_combine_kernel(TokArgs 
 // first; lane k of each wave adds the wave's part of <dy, row> to slot k's `sum`.
 template <class T, int N>
 __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uint64_t& m, int i0,
-                                          const float (&g)[VEC], float& sum) {
+                                          Early<T>& dy, float (&g)[VEC], float& sum) {
   typename RawOf<T>::type r[N];
   int64_t at[N];
   float w[N];
@@ -112,6 +132,7 @@ __device__ __forceinline__ void grad_rows(const TokArgs& a, const Places& p, uin
     w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p.w), k[i]));
     if (a.dw) r[i] = load8(static_cast<const T*>(a.yp) + at[i], i0, a.d);
   }
+  dy.get(g, a.d - i0);
   if (a.dw) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -151,13 +172,14 @@ __global__ __launch_bounds__(kThreads<LANES>) void token_combine_bwd_kernel(TokA
     for (int s0 = 0; s0 < a.d; s0 += LANES * VEC) {
       const int i0 = s0 + lane * VEC;
       float g[VEC];
-      unpack(load8(static_cast<const T*>(a.base) + t * a.ldt, i0, a.d), g, a.d - i0);
+      Early<T> dy;
+      dy.load(a.base, t * a.ldt, i0, a.d);
       uint64_t m = p.mask;
       int left = __popcll(m);
-      for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, g, sum);
-      for (; left >= 4; left -= 4) grad_rows<T, 4>(a, p, m, i0, g, sum);
-      for (; left >= 2; left -= 2) grad_rows<T, 2>(a, p, m, i0, g, sum);
-      for (; left >= 1; --left) grad_rows<T, 1>(a, p, m, i0, g, sum);
+      for (; left >= 8; left -= 8) grad_rows<T, 8>(a, p, m, i0, dy, g, sum);
+      for (; left >= 4; left -= 4) grad_rows<T, 4>(a, p, m, i0, dy, g, sum);
+      for (; left >= 2; left -= 2) grad_rows<T, 2>(a, p, m, i0, dy, g, sum);
+      for (; left >= 1; --left) grad_rows<T, 1>(a, p, m, i0, dy, g, sum);
     }
     part[group][wave][threadIdx.x & 63] = sum;
   }
