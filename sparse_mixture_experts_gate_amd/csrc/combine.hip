@@ -101,7 +101,13 @@ __global__ __launch_bounds__(kThreads<LANES>) void token_combine_kernel(TokArgs 
   const int64_t t = a.t0 + int64_t(blockIdx.x) * GROUPS + threadIdx.x / LANES;
   if (t >= a.T) return;  // whole waves
   const Places p = places_of(a, t, threadIdx.x & 63);
-  for (int i0 = lane * VEC; i0 < a.d; i0 += LANES * VEC) {
+  // The whole wave sweeps on or ends, since places come out of lanes that may hold no
+  // values: lanes past the row take its last chunk along and store nothing.
+  const int last = (a.d - 1) & ~(VEC - 1);
+  for (int s0 = __builtin_amdgcn_readfirstlane(lane >> 6) * 64 * VEC; s0 < a.d;
+       s0 += LANES * VEC) {
+    const int i0 = min(s0 + static_cast<int>(threadIdx.x & 63) * VEC, last);
+    __builtin_assume(i0 < a.d);
     float acc[VEC] = {};
     Early<T> base;
     if (a.base) base.load(a.base, t * a.ldt, i0, a.d);
@@ -112,7 +118,8 @@ __global__ __launch_bounds__(kThreads<LANES>) void token_combine_kernel(TokArgs 
     if (left & 2) add_rows<T, 2>(a, p, m, i0, base, acc);
     if (left & 1) add_rows<T, 1>(a, p, m, i0, base, acc);
     base.get(acc, a.d - i0);
-    store8(static_cast<T*>(a.y) + t * a.ldt + i0, acc, a.d - i0, a.stream);
+    if (s0 + static_cast<int>(threadIdx.x & 63) * VEC < a.d)
+      store8(static_cast<T*>(a.y) + t * a.ldt + i0, acc, a.d - i0, a.stream);
   }
 }
 

@@ -29,7 +29,8 @@ struct MoveArgs {
   uint8_t* xp;
   uint8_t* xp2;
   int64_t t0, T;  // tokens t0 .. T - 1 of this launch's groups
-  int64_t pairs, rows, row_bytes, row2_bytes, ldt, ldp;
+  int64_t pairs, rows, ldt, ldp;
+  int row_bytes, row2_bytes;  // (below 2^31: d * 4 is)
   int E, K;
   bool stream;
   // the sort's tables (many pairs)
@@ -38,13 +39,15 @@ struct MoveArgs {
 };
 
 // Copies one row to the places that exist, by LANES lanes; lane k of a wave holds slot
-// k's in `at`.
-template <int LANES>
-__device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64_t bytes,
-                                         int64_t ldp, int32_t at, int K, int lane, bool stream) {
+// k's in `at`. The whole wave sweeps on or ends: places come out of lanes that may hold
+// no piece of the row.
+template <int LANES, bool STREAM>
+__device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int bytes, int64_t ldp,
+                                         int32_t at, int K, int lane) {
   constexpr int CH = 4;  // 16-byte pieces of a lane in flight
-  const int64_t whole = bytes / 16;
-  for (int64_t c0 = lane; c0 < whole; c0 += CH * LANES) {
+  const int whole = bytes / 16;
+  int w0 = __builtin_amdgcn_readfirstlane(lane >> 6) * 64;
+  for (int c0 = lane; w0 < whole; w0 += CH * LANES, c0 += CH * LANES) {
     u32x4_any1_t v[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i)
@@ -58,17 +61,14 @@ __device__ __forceinline__ void move_row(const uint8_t* src, uint8_t* dst, int64
       for (int i = 0; i < CH; ++i)
         if (c0 + i * LANES < whole) {
           auto* q = reinterpret_cast<u32x4_any1_t*>(d + (c0 + i * LANES) * 16);
-          if (stream) {  // (the empty statements keep the two stores apart)
-            asm volatile("");
+          if constexpr (STREAM)
             __builtin_nontemporal_store(v[i], q);
-            asm volatile("");
-          } else {
+          else
             *q = v[i];
-          }
         }
     }
   }
-  const int tail = static_cast<int>(bytes - whole * 16);
+  const int tail = bytes - whole * 16;
   if (tail == 0) return;
   const uint8_t v = lane < tail ? src[whole * 16 + lane] : 0;
   for (int k = 0; k < K; ++k) {
@@ -82,10 +82,14 @@ __device__ __forceinline__ void move_token(const MoveArgs& a, int64_t t, const i
                                            int lane) {
   if (!a.x) return;
   const int32_t at = (lane & 63) < a.K ? pos[lane & 63] : -1;
-  move_row<LANES>(a.x + t * a.ldt, a.xp, a.row_bytes, a.ldp, at, a.K, lane, a.stream);
+  const uint8_t* x = a.x + t * a.ldt;
+  if (a.stream)
+    move_row<LANES, true>(x, a.xp, a.row_bytes, a.ldp, at, a.K, lane);
+  else
+    move_row<LANES, false>(x, a.xp, a.row_bytes, a.ldp, at, a.K, lane);
   if (a.x2)
-    move_row<LANES>(a.x2 + t * a.row2_bytes, a.xp2, a.row2_bytes, a.row2_bytes, at, a.K, lane,
-                    false);
+    move_row<LANES, false>(a.x2 + t * a.row2_bytes, a.xp2, a.row2_bytes, a.row2_bytes, at, a.K,
+                           lane);
 }
 
 // Sum over the wave, the same for all lanes.
@@ -379,8 +383,8 @@ hipError_t launch_dispatch(const DispatchArgs& p, void* ws, hipStream_t s) {
   a.T = p.T;
   a.pairs = pairs;
   a.rows = p.rows;
-  a.row_bytes = p.row_bytes;
-  a.row2_bytes = p.row2_bytes;
+  a.row_bytes = static_cast<int>(p.row_bytes);
+  a.row2_bytes = static_cast<int>(p.row2_bytes);
   a.ldt = p.ldt;
   a.ldp = p.ldp;
   a.E = p.E;
