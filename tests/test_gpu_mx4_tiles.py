@@ -76,3 +76,30 @@ def test_tile(rows, G, n, k, tile, out):
             few = one.forward(x[sel[a:b]], torch.tensor([0, b - a], dtype=torch.int32, device=DEV),
                               out_dtype=DT[out])
             assert torch.equal(few, y[sel[a:b]])
+
+
+@pytest.mark.parametrize("rows,n,k,bad,split", [
+    (50, 40, 64, [-9, 10, 5, 2 ** 31 - 1, 3], [0, 10, 10, 50, 50]),
+    (50, 40, 64, [60, -1, 70, 8, 9], [50, 50, 50, 50, 50]),
+    (100, 4100, 300, [7, 30, -5, 90, 20], [7, 30, 30, 90, 90]),
+    (2000, 1000, 520, [-2 ** 31, 900, 300, 2 ** 31 - 1], [0, 900, 900, 2000]),
+    (16000, 1030, 1290, [-9, 9000, 4000, 1 << 20], [0, 9000, 9000, 16000])])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_offsets_out_of_order_are_a_clamped_split(rows, n, k, bad, split, out):
+    """The whole product is that of the clamped ascending split, from the tile of few rows
+    to the largest; nothing around it is written."""
+    import sparse_mixture_experts_gate_amd as M
+    lin = M.MX4Linear.from_weight(_rand(1, len(bad) - 1, n, k, dt="bf16"))
+    codes, scales = M.mx4_quantize(_rand(2, rows, k, dt="bf16"))
+    desc = M.MoeMx4GemmDesc(rows=rows, n_groups=len(bad) - 1, n=n, k=k, ld_y=n + 3,
+                            out_dtype=M.MOE_DT_BF16 if out == "bf16" else M.MOE_DT_F32)
+    got = []
+    for off in (bad, split):
+        wide = torch.full((rows + 600, n + 3), 7.0, dtype=DT[out], device=DEV)
+        M.moe_mx4_gemm(desc, codes, scales, lin.codes, lin.scales,
+                       torch.tensor(off, dtype=torch.int32, device=DEV), wide[300:-300, 1:1 + n])
+        inside = wide[300:-300, 1:1 + n]
+        got.append(inside.clone())
+        inside[split[0]:split[-1]] = 7.0
+        assert bool((wide == 7).all())
+    assert torch.equal(*got)
