@@ -308,12 +308,20 @@ class MX4Linear:
         return cls(*mx4_quantize(weight, stream=stream), weight.shape[2])
 
     @classmethod
-    def from_blocks(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MX4Linear":
-        """From scales in row order, uint8 [groups, n, blocks]."""
+    def from_blocks(cls, codes: torch.Tensor, scales: torch.Tensor,
+                    k: int | None = None) -> "MX4Linear":
+        """From scales in row order, uint8 [groups, n, blocks]; rows of k values (all
+        of the blocks' without it)."""
+        if scales.dim() != 3:
+            raise ValueError(f"scales: expected uint8 [groups, n, blocks], got {list(scales.shape)}")
         G, n, kb = scales.shape
         _matrix(codes, "codes", torch.uint8, G, n, kb * 16)
+        if k is None:
+            k = kb * 32
+        if -(-k // 32) != kb:
+            raise ValueError(f"k: expected {kb * 32 - 31} .. {kb * 32} for {kb} blocks, got {k}")
         words = torch.nn.functional.pad(scales, (0, -kb % 4)).reshape(G, n, -1, 4)
-        return cls(codes, words.transpose(1, 2).contiguous(), kb * 32)
+        return cls(codes, words.transpose(1, 2).contiguous(), k)
 
     def values(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """The weights [groups, n, k] that the codes stand for."""

@@ -1,0 +1,49 @@
+"""Maps from 4-bit weights whose scales come in row order: rows that end inside a block."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.token_ops as B
+
+DEV = "cuda:0"
+
+
+def _blocks(seed, *shape, dev="cpu"):
+    w = np.random.default_rng(seed).standard_normal(shape).astype(np.float32)
+    c, b = B.mx4_encode(w)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    return torch.from_numpy(w), t(B.mx4_pack(c)), t(b)
+
+
+@pytest.mark.parametrize("k,blocks", [(1, 1), (32, 1), (33, 2), (200, 7), (224, 7), (1407, 44)])
+def test_rows_that_end_inside_a_block(k, blocks):
+    import sparse_mixture_experts_gate_amd as M
+    _, codes, scales = _blocks(k, 2, 3, k)
+    lin = M.MX4Linear.from_blocks(codes, scales, k=k)
+    assert lin.k == k and M.MX4Linear.from_blocks(codes, scales).k == 32 * blocks
+    assert lin.scales.shape == (2, -(-blocks // 4), 3, 4)
+    for bad in (0, -1, 32 * blocks - 32, 32 * blocks + 1):
+        with pytest.raises(ValueError):
+            M.MX4Linear.from_blocks(codes, scales, k=bad)
+
+
+def test_scales_that_are_no_blocks():
+    import sparse_mixture_experts_gate_amd as M
+    _, codes, scales = _blocks(1, 2, 3, 64)
+    for bad in (scales[0], scales.int(), scales[:, :2], scales[:, :, :1]):
+        with pytest.raises(ValueError):
+            M.MX4Linear.from_blocks(codes, bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [31, 200, 1407])
+def test_product(k):
+    """A map from blocks takes the activations that the weights were made for."""
+    import sparse_mixture_experts_gate_amd as M
+    w, codes, scales = _blocks(k, 3, 40, k, dev=DEV)
+    x = torch.randn(30, k, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    off = torch.tensor([0, 5, 5, 30], dtype=torch.int32, device=DEV)
+    lin, ref = M.MX4Linear.from_blocks(codes, scales, k=k), M.MX4Linear.from_weight(w.to(DEV))
+    assert torch.equal(lin.codes, ref.codes) and torch.equal(lin.scales, ref.scales)
+    assert torch.equal(lin.values(), ref.values())
+    assert torch.equal(lin.forward(x, off), ref.forward(x, off))
