@@ -308,8 +308,8 @@ class MX4Linear:
         return cls(*mx4_quantize(weight, stream=stream), weight.shape[2])
 
     @classmethod
-    def from_blocks(cls, codes: torch.Tensor, scales: torch.Tensor,
-                    k: int | None = None) -> "MX4Linear":
+    def from_blocks(cls, codes: torch.Tensor, scales: torch.Tensor, k: int | None = None,
+                    stream=None) -> "MX4Linear":
         """From scales in row order, uint8 [groups, n, blocks]; rows of k values (all
         of the blocks' without it)."""
         if scales.dim() != 3:
@@ -320,8 +320,10 @@ class MX4Linear:
             k = kb * 32
         if -(-k // 32) != kb:
             raise ValueError(f"k: expected {kb * 32 - 31} .. {kb * 32} for {kb} blocks, got {k}")
-        words = torch.nn.functional.pad(scales, (0, -kb % 4)).reshape(G, n, -1, 4)
-        return cls(codes, words.transpose(1, 2).contiguous(), k)
+        with _on(stream):
+            words = torch.nn.functional.pad(scales, (0, -kb % 4)).reshape(G, n, -1, 4)
+            words = words.transpose(1, 2).contiguous()
+        return cls(codes, words, k)
 
     def values(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """The weights [groups, n, k] that the codes stand for."""

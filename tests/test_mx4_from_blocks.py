@@ -1,4 +1,5 @@
-"""Maps from 4-bit weights whose scales come in row order: rows that end inside a block."""
+"""Maps from 4-bit weights whose scales come in row order: rows that end inside a block,
+the stream that the scales are put in order on."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +48,21 @@ def test_product(k):
     assert torch.equal(lin.codes, ref.codes) and torch.equal(lin.scales, ref.scales)
     assert torch.equal(lin.values(), ref.values())
     assert torch.equal(lin.forward(x, off), ref.forward(x, off))
+
+
+@pytest.mark.gpu
+def test_scales_still_being_written():
+    """All of it on the stream that writes the scales: none is read before."""
+    import sparse_mixture_experts_gate_amd as M
+    w, codes, scales = _blocks(3, 2, 64, 512, dev=DEV)
+    x, off = torch.randn(20, 512, device=DEV), torch.tensor([0, 7, 20], dtype=torch.int32, device=DEV)
+    want = M.MX4Linear.from_weight(w.to(DEV)).forward(x, off)
+    late = torch.zeros_like(scales)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(scales)
+    y = M.MX4Linear.from_blocks(codes, late, stream=s).forward(x, off, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
