@@ -9,8 +9,8 @@
 // The backward of rows past 8192 values holds two rows, the weight and two
 // column sums at 32 values a lane each, which fill 256 registers or do not fit them:
 // 180 bytes a lane go to scratch memory with fp32 rows and dresidual, 20 without.
-// 2048 x 16384: bf16 53 us, with dresidual 65; fp32 101 and 158, 0.7 to 0.85 of a
-// large copy's rate.
+// 2048 x 16384 (replayed graphs): bf16 44 us, with dresidual 53; fp32 98 and 157, 3.4
+// to 5.0 TB/s where a large copy reaches 4.8.
 #include "device_common.h"
 #include "internal.h"
 #include "row_io.h"
@@ -195,16 +195,29 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* slot) {
 // each block then writes one partial sum per column. The next row is loaded
 // while the current one is reduced. With NW == 1 the block's four waves add
 // their column sums through LDS, in wave order.
-// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 89 us, 470 MB
-// at 5.3 TB/s.
-template <class T, int NW, int CH, bool RES>
+// Bound by memory: 8192 x 7168 bf16 with dresidual, both kernels: 87 us, 470 MB
+// at 5.4 TB/s.
+// WHOLE: no row ends inside a lane's eight values, so nothing is shifted at its end.
+template <class T, int NW, int CH, bool RES, bool WHOLE>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNormArgs a) {
   constexpr int LANES = NW * 64, GROUPS = NW == 1 ? 4 : 1;
   // Four chunks leave no registers for the next row's dresidual: the row's own is loaded
-  // behind its other loads (2048 x 16384 bf16: 65 us before, 61 so; fp32 191 and 154).
+  // behind its other loads (2048 x 16384 bf16: 64 us before, 53 so; fp32 189 and 157).
   constexpr bool LATE = RES && CH == 4;
   __shared__ float2 slot[2][NW];
   const int lane = threadIdx.x & (LANES - 1);
+  auto load = [&](const void* rows, int64_t at, int i0) {
+    if constexpr (WHOLE)
+      return load8_whole(static_cast<const T*>(rows) + at, i0, a.d);
+    else
+      return load8(static_cast<const T*>(rows) + at, i0, a.d);
+  };
+  auto open = [&](const typename RawOf<T>::type& r, float (&v)[VEC], int cnt) {
+    if constexpr (WHOLE)
+      unpack_whole(r, v);
+    else
+      unpack(r, v, cnt);
+  };
   const int64_t first = int64_t(blockIdx.x) * GROUPS + (NW == 1 ? threadIdx.x >> 6 : 0);
   const int64_t stride = int64_t(gridDim.x) * GROUPS;
   float aw[CH][VEC], ab[CH][VEC], w[CH][VEC];
@@ -223,10 +236,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i0 = (c * LANES + lane) * VEC;
-      rx[c] = load8(static_cast<const T*>(a.x) + row * a.ldx, i0, a.d);
-      rg[c] = load8(static_cast<const T*>(a.dy) + row * a.ldy, i0, a.d);
-      if constexpr (RES && !LATE)
-        rr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, i0, a.d);
+      rx[c] = load(a.x, row * a.ldx, i0);
+      rg[c] = load(a.dy, row * a.ldy, i0);
+      if constexpr (RES && !LATE) rr[c] = load(a.dr, row * a.ldr, i0);
     }
   };
   if (first < a.n) fetch(first);
@@ -240,15 +252,15 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int cnt = a.d - (c * LANES + lane) * VEC;
-      unpack(rx[c], z[c], cnt);
-      unpack(rg[c], g[c], cnt);
+      open(rx[c], z[c], cnt);
+      open(rg[c], g[c], cnt);
       if constexpr (LATE)
-        kr[c] = load8(static_cast<const T*>(a.dr) + row * a.ldr, (c * LANES + lane) * VEC, a.d);
+        kr[c] = load(a.dr, row * a.ldr, (c * LANES + lane) * VEC);
       else if constexpr (RES)
         kr[c] = rr[c];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        z[c][j] = j < cnt ? (z[c][j] - m) * r : 0.0f;
+        z[c][j] = (WHOLE ? 0 : j) < cnt ? (z[c][j] - m) * r : 0.0f;
         aw[c][j] += g[c][j] * z[c][j];
         ab[c][j] += g[c][j];
         g[c][j] *= w[c][j];
@@ -270,7 +282,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
       for (int j = 0; j < VEC; ++j) o[j] = r * (g[c][j] - c1 - z[c][j] * c2);
       if constexpr (RES) {
         float e[VEC];
-        unpack(kr[c], e, a.d - i0);
+        open(kr[c], e, a.d - i0);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += e[j];
       }
@@ -490,11 +502,18 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
     return;
   }
   const RowShape r = row_shape(a.d);
-#define NORM_CASE(NW, CH)                                                          \
-  if (r.nw == NW && r.ch == CH) {                                                  \
-    hipLaunchKernelGGL((norm_bwd_kernel<T, NW, CH, RES>), dim3(parts),             \
-                       dim3(NW == 1 ? 256 : NW * 64), 0, s, a);                    \
-    return;                                                                        \
+  // bf16 rows that end inside no lane's eight values take a kernel without the shifts of
+  // row ends, without / with dresidual (us, replayed graphs): 8192 x 512 9.7 / 10.2, with
+  // the shifts 10.1 / 10.9; 8192 x 1024 14.6 / 16.8, 15.2 / 17.1; 8192 x 7168 58 / 87.7,
+  // 60 / 89.5; 2048 x 8200 28 / 32, 36 / 39; 2048 x 16384 44.4 / 53, 45.4 / 58; 64 x 16384
+  // 14.8 / 15.0, 16.3 / 16.9. fp32 rows' ends are loaded value by value.
+  const bool whole = sizeof(T) == 2 && a.d % VEC == 0;
+#define NORM_CASE(NW, CH)                                                                  \
+  if (r.nw == NW && r.ch == CH) {                                                          \
+    hipLaunchKernelGGL(whole ? (norm_bwd_kernel<T, NW, CH, RES, sizeof(T) == 2>)           \
+                             : (norm_bwd_kernel<T, NW, CH, RES, false>),                   \
+                       dim3(parts), dim3(NW == 1 ? 256 : NW * 64), 0, s, a);               \
+    return;                                                                                \
   }
   NORM_CASE(1, 1)
   NORM_CASE(1, 2)
@@ -508,9 +527,11 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
 }  // namespace
 
 // Blocks of the backward, each with a partial row of column sums: 8 waves per CU.
-// More blocks hide more latency but write and add more partial rows (8192 x 7168
-// bf16 with dresidual: 89 us with 256 blocks of 8 waves, 98 with 512; 8192 x 4096:
-// 53 us with 256 of 4 waves, 56 with 512, 63 with 1024; 8192 x 2048: 36, 29, 33).
+// More blocks hide more latency but write and add more partial rows. 8192 bf16 rows,
+// without / with dresidual, of 256, 512 and 1024 blocks (us, replayed graphs): 512 values,
+// where four rows share a block, 11.2 / 11.3, 10.0 / 10.3, 12.2 / 12.0; 2048 30 / 30, 23 /
+// 26, 25 / 29; 2815 46 / 53, 35 / 41, 36 / 49; 4096 41 / 45, 38 / 46, 42 / 54; 7168, blocks
+// of 8 waves, 59 / 87, 63 / 93, 76 / 106.
 int norm_backward_parts(int64_t n, int d) {
   if (d > kMaxRow) return static_cast<int>(n < 1 ? 1 : n < 256 ? n : 256);
   const int nw = row_shape(d).nw;

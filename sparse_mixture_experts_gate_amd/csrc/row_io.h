@@ -64,6 +64,18 @@ __device__ __forceinline__ Raw32 load8(const float* row, int i0, int d) {
   }
   return r;
 }
+// bf16 rows of a multiple of 8 values, which end inside no lane's eight: zeros past the
+// row, and nothing for unpack to shift.
+__device__ __forceinline__ Raw16 load8_whole(const uint16_t* row, int i0, int d) {
+  Raw16 r{};
+  if (i0 < d) __builtin_memcpy(&r, row + i0, sizeof(r));
+  return r;
+}
+__device__ __forceinline__ void unpack_whole(const Raw16& r, float (&v)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    v[j] = __uint_as_float((j & 1) ? (r.w[j >> 1] & 0xFFFF0000u) : (r.w[j >> 1] << 16));
+}
 // load8's values in order, with cnt = d - i0: zeros past the row's end.
 __device__ __forceinline__ void unpack(Raw16 r, float (&v)[VEC], int cnt) {
   if (cnt < VEC) {  // the first VEC - cnt are not this lane's
@@ -79,9 +91,7 @@ __device__ __forceinline__ void unpack(Raw16 r, float (&v)[VEC], int cnt) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.w[j] = cnt > 0 ? +r.w[j] : 0u;
   }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    v[j] = __uint_as_float((j & 1) ? (r.w[j >> 1] & 0xFFFF0000u) : (r.w[j >> 1] << 16));
+  unpack_whole(r, v);
 }
 __device__ __forceinline__ void unpack(const Raw32& r, float (&v)[VEC], int) {
 #pragma unroll
