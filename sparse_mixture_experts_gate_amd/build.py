@@ -38,16 +38,21 @@ SOURCES = ["dsmoe_api.cpp", "router.hip", "permute.hip", "gemm_bf16.hip", "gemm_
            "mx4_gemm.hip"]
 
 
+def flags(src: str) -> list[str]:
+    """hipcc's flags for a source."""
+    out = list(COMMON)
+    if src in NO_CONTRACT:
+        out.append("-ffp-contract=off")
+    if src in MFMA_VGPR:
+        out += ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+    if src.endswith(".cpp"):
+        out += ["-x", "hip"]
+    return out
+
+
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, src + ".o")
-    cmd = [HIPCC, *COMMON]
-    if src in NO_CONTRACT:
-        cmd.append("-ffp-contract=off")
-    if src in MFMA_VGPR:
-        cmd += ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-    if src.endswith(".cpp"):
-        cmd += ["-x", "hip"]
-    cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *flags(src), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

@@ -5,23 +5,20 @@ without that lane.
 
 In the assembly a loop of that kind takes lanes out of exec in front of its back edge
 (s_andn2 exec, exec); one that the whole wave leaves branches on a scalar condition."""
-import concurrent.futures as cf
-import os
 import re
-import subprocess
 
 import pytest
 
-from sparse_mixture_experts_gate_amd import build as B
+from asm_util import assembly, kernels, no_hipcc
 
-pytestmark = pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="no hipcc")
+pytestmark = pytest.mark.skipif(no_hipcc(), reason="no hipcc")
 SOURCES = ["combine.hip", "dispatch.hip"]
 
 
 def _kernels(asm):
     """{name: (instructions of each basic block, successors of each)}."""
     out = {}  # a block while it is read: [lines, labels of its branches, whether the next follows]
-    for name, body in re.findall(r"^(_Z\w+):.*?\n(.*?)^\.Lfunc_end", asm, re.M | re.S):
+    for name, body in kernels(asm).items():
         blocks, at = [[[], [], True]], {}
         for line in (s.split(";")[0].strip() for s in body.splitlines()):
             label = re.match(r"(\.LBB\w+):", line)
@@ -109,15 +106,9 @@ def test_loops_are_told_apart(read, latch, bad):
     assert bool(bad_loops(LOOP.format(read=read, latch=latch))) == bad
 
 
-def test_lanes_are_read_by_whole_waves(tmp_path):
-    def assembly(src):
-        out = str(tmp_path / (src + ".s"))
-        subprocess.run([B.HIPCC, *B.COMMON, "--cuda-device-only", "-S",
-                        os.path.join(B.CSRC, src), "-o", out], check=True, capture_output=True)
-        return open(out).read()
-
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
-        for src, asm in zip(SOURCES, ex.map(assembly, SOURCES)):
-            assert "v_readlane_b32" in asm
-            bad = bad_loops(asm)
-            assert not bad, (src, bad[:4], len(bad))
+@pytest.mark.parametrize("src", SOURCES)
+def test_lanes_are_read_by_whole_waves(src):
+    asm = assembly(src)
+    assert "v_readlane_b32" in asm
+    bad = bad_loops(asm)
+    assert not bad, (bad[:4], len(bad))
