@@ -204,6 +204,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
   // Four chunks leave no registers for the next row's dresidual: the row's own is loaded
   // behind its other loads (2048 x 16384 bf16: 64 us before, 53 so; fp32 189 and 157).
   constexpr bool LATE = RES && CH == 4;
+  // Whether large dx goes past the caches. bf16 without dresidual, past them / through them,
+  // inputs from memory and (replayed graphs) from the caches as far as they fit: 8192 x 4096
+  // 46.4 / 45.1 us and 38.2 / 38.1, 4096 x 16384 91 / 88, 2048 x 16384 53 / 51 and 44.4 / 43.7,
+  // but 8192 x 7168 73 / 71 and 58 / 70. With it: 8192 x 7168 91.7 / 91.9 and 88 / 89, 32768 x
+  // 4096 196 / 200, 2048 x 16384 65 / 64 and 53 / 56.
+  constexpr bool PAST = RES || (NW == 8 && CH == 2);
   __shared__ float2 slot[2][NW];
   const int lane = threadIdx.x & (LANES - 1);
   auto load = [&](const void* rows, int64_t at, int i0) {
@@ -286,7 +292,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void norm_bwd_kernel(BwdNo
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += e[j];
       }
-      store8(dx + i0, o, a.d - i0, a.stream);
+      store8(dx + i0, o, a.d - i0, PAST && a.stream);
     }
   }
   if (!a.part) return;
@@ -505,8 +511,7 @@ void bwd_dispatch(const BwdNormArgs& a, int parts, hipStream_t s) {
   // bf16 rows that end inside no lane's eight values take a kernel without the shifts of
   // row ends, without / with dresidual (us, replayed graphs): 8192 x 512 9.7 / 10.2, with
   // the shifts 10.1 / 10.9; 8192 x 1024 14.6 / 16.8, 15.2 / 17.1; 8192 x 7168 58 / 87.7,
-  // 60 / 89.5; 2048 x 8200 28 / 32, 36 / 39; 2048 x 16384 44.4 / 53, 45.4 / 58; 64 x 16384
-  // 14.8 / 15.0, 16.3 / 16.9. fp32 rows' ends are loaded value by value.
+  // 60 / 89.5; 2048 x 8200 28 / 32, 36 / 39; 64 x 16384 14.8 / 15.0, 16.3 / 16.9. fp32 rows' ends are loaded value by value.
   const bool whole = sizeof(T) == 2 && a.d % VEC == 0;
 #define NORM_CASE(NW, CH)                                                                  \
   if (r.nw == NW && r.ch == CH) {                                                          \

@@ -212,9 +212,10 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
   return v;
 }
 
-// bf16 row outputs of this many bytes or more are stored past the caches: eight L2s
-// of 4 MB (layer norm of 8192 x 7168 with a residual 98 us without, 95 so, its backward 92
-// and 89, both with weights loaded value by value; fp32 rows of 8192 x 7168, in both stores, 137 -> 155).
+// bf16 row outputs of this many bytes or more are stored past the caches: eight L2s of 4
+// MB (layer norm of 8192 x 7168, inputs from memory, 52.4 us through the caches and 51.7
+// past them, with a residual the same; its backward's sides are in norm.hip; fp32 rows of
+// 8192 x 7168, in both stores, 137 -> 155).
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
 // The same for rows moved between tokens and experts, whose reader comes next and
 // finds smaller outputs in the 256 MB that the L2s share: E4M3 rows of 8192 tokens to 8
