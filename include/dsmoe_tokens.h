@@ -155,8 +155,8 @@ moe_status moe_token_combine_backward(const moe_dispatch_desc* desc, const void*
  * byte b that stands for 2^(b - 127). With amax the block's largest magnitude
  *   e = floor(log2(amax)) - 2, at least -127;  b = e + 127;
  *   code = e2m1(v * 2^-e), to nearest even, magnitudes past 6 to 6.
- * amax == 0: b = 0 and zero codes. A NaN or infinity in a block: b = 255 (NaN:
- * every value of the block) and zero codes.
+ * amax == 0: b = 0 and codes of zeros with their signs. A NaN or infinity in a block:
+ * b = 255 (NaN: every value of the block) and codes 0.
  * Layout of n_mats matrices of `rows` rows, KB = ceil(k / 32):
  *   codes   [n_mats, rows, KB * 16] bytes, value 2 i of a row in the low half of
  *           byte i

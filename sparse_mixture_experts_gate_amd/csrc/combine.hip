@@ -3,8 +3,8 @@
 //
 // Memory-bound: a group of LANES lanes owns a token, 8 adjacent values per lane
 // and chunk; its places and weights are wave-uniform, and the rows of up to eight
-// places are in flight together. 8192 x 8 rows of 7168 bf16 values: 207 us, 1.06 GB at
-// 5.1 TB/s; the gradients 403 us, 2.0 GB at 5.0. Few tokens: latency; gradients of 64 x 8
+// places are in flight together. 8192 x 8 rows of 7168 bf16 values: 205 us, 1.06 GB at
+// 5.2 TB/s; the gradients 398 us, 2.0 GB at 5.0. Few tokens: latency; gradients of 64 x 8
 // rows of 4096 by 256 lanes a token 8.7 us, with one place's row at a time 9.9.
 #include "device_common.h"
 #include "internal.h"
@@ -51,8 +51,11 @@ __device__ __forceinline__ int next_slot(uint64_t& m) {
 }
 
 // A token row's chunk that is loaded before those of its places and put in order behind
-// their loads (in front of them, its wait would stand before theirs: a return of 4096 x 8
-// rows of 7168, one in eight here, 32.9 us, 31.8 so).
+// their loads; in front of them, its wait would stand before theirs. With inputs that no
+// cache holds, a return of 4096 x 8 rows of 7168 bf16 values, one in eight here, takes 43.0
+// us that way and 41.8 so, of 4096 x 6 rows of 2048 30.2 and 28.6, of 8192 x 4 rows of 1408,
+// half of them here, 24.5 and 20.4, the gradients of these 31.0 and 29.8; other gradients,
+// fp32 rows and few tokens the same within 2%.
 template <class T>
 struct Early {
   typename RawOf<T>::type raw;

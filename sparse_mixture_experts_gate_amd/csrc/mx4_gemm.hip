@@ -9,17 +9,20 @@
 // its half holds the bytes of its four sub-steps, and one 4-byte LDS read per 32 rows
 // serves a k-step.
 //
-// What bounds it, measured. Large products the power limit: one group of 8192 rows,
-// 4096 x 7168, 119 us, 4.0 PFLOP/s with random codes and a third more with zeros; the
-// matrix instructions alone, operands held in registers, reach 6.4 at 1.5 GHz, and
-// with the loads into LDS switched off the same loop takes 52% of the time. Few rows:
-// the stream of weights (128 rows over 256 experts of 4096 x 7168: 227 us, 6.9 TB/s).
-// Measured equal or slower: waves in step per sub-step as in the 16-bit products'
-// large tiles (123 us; four barriers more a step), k-steps of 128 values in four
-// stages (127), loads of the lines three steps ahead into L2 (131), waves without rows
-// leaving out their matrix instructions (the same), the last round's tiles cut into
-// quarters (the same), operands through registers three steps ahead into two stages
-// (128 rows a tile, Zipf loads over 32 groups: 226 against 199).
+// What bounds it, measured. Large products no unit by itself: one group of 8192 rows,
+// 4096 x 7168, takes 112 to 129 us, 3.7 to 4.3 PFLOP/s, at 1.9 GHz; the matrix
+// instructions are busy for half of the cycles (alone, operands held in registers, they
+// reach 6.4 PFLOP/s at 1.5 GHz), LDS reads for 22% (a CU reads 204 bytes a cycle and more),
+// and zero codes take 87 us where random ones take 112. With the loads into LDS switched
+// off the same loop takes 52% of the time: a k-step's 64 KB of loads and its matrix
+// instructions take turns, as a ring of two stages has no more than one step in flight.
+// Few rows: the stream of weights (128 rows over 256 experts of 4096 x 7168: 227 us, 6.9
+// TB/s). Measured equal or slower on large products: waves in step per sub-step as in the
+// 16-bit products' large tiles (four barriers more a step), k-steps of 128 values in four
+// stages, loads of the lines three steps ahead into L2, waves without rows leaving out
+// their matrix instructions, the last round's tiles cut into quarters, operands through
+// registers three steps ahead into two stages (128 rows a tile, Zipf loads over 32
+// groups: 226 against 199).
 #include "device_common.h"
 #include "gemm16_core.h"
 #include "group_tables.h"
@@ -417,7 +420,7 @@ __device__ __forceinline__ void mx4_ring(uint8_t* lds, int first, int nb, int to
 // its own matrix core and in the order of the other tiles (a row's sums are the same bits
 // in every tile), and wave g ends with columns 8 g .. of each 32. One barrier per k-step:
 // behind it the step's blocks are there and the stage before it is free. Latency-bound: a
-// row of 7168 by 4096 x 7168 11.8 us (a launch and its 16 MB 5.6), of which the 112 matrix
+// row of 7168 by 4096 x 7168 12 to 13 us (a launch and its 16 MB 5.6), of which the 112 matrix
 // instructions one after the other are most: with the next step's blocks read ahead the
 // same, split over the waves 8.9, which would make a row's sums depend on the tile.
 template <class C, class NextOps, class Epilogue>

@@ -25,28 +25,33 @@ constexpr TileCost kCosts[] = {{256, 256, 1.76, 1.76, 1.22, 7.0},
 // least modelled time. Row counts per group live on the device, so the expected number
 // of row tiles stands in for them: at least one per group with rows, else rows / BM and
 // half a tile per group; with more than one group half a round more than the tiles fill.
-// Measured (us, 256 / 128 / 64 / 32 rows):
-//   x [16, 4096], 1 x 4096                    25 / 15 / 13 / 10
-//   x [512, 2048], 8 x 1408                   17 / 12 / 10 / 8
-//   x [1024, 7168], 1 x 4096                  47 / 30 / 26 / 48
-//   x [2048, 4096], 1 x 4096                  35 / 26 / 31 / 58
-//   x [1024, 4096], 16 x 4096                 34 / 39 / 36 / 42
-//   x [2048, 2048], 64 x 2816                 59 / 41 / 37 / 41
-//   x [4096, 7168], 32 x 4096                174 / 125 / 168 / 221
-//   x [8192, 7168], 1 x 4096                 119 / 129 / 173 / 361
-//   x [8192, 7168], 32 x 4096, Zipf loads    195 / 199 / 245 / 424
-//   x [24576, 2048], 64 x 2816               119 / 122 / 158 / 271
-//   x [128, 7168], 128 of 256 groups x 4096   32 rows: 276 (weights through the caches
-//                                            325), 64: 328
-// 32 x 32 against 32 x 128:
-//   x [1, 7168], 1 x 4096, 128 tiles         11.8 / 13.4
-//   x [16, 7168], 2 x 4096, 256 tiles        12.5 / 15.4
-//   x [64, 2048], 32 x 256, 256 tiles         6.9 / 7.8
-//   x [6, 2048], 6 x 1408, 264 tiles          7.5 / 7.8
-//   x [128, 7168], 1 x 4096, 512 tiles       14.8 / 15.0
-//   x [8, 2048], 8 x 2816, 704 tiles          9.5 / 8.8
-// and where it is wrong, the tile it takes first:
-//   x [2048, 7168], 32 x 4096                 128 rows: 124, 64: 109
+// Measured (us, replayed graphs, 256 / 128 / 64 / 32 rows / 32 x 32; *: what the rule takes):
+//   x [1, 7168], 1 x 4096                     41 / 24 / 20 / 14.6 / 13.2*
+//   x [16, 4096], 1 x 4096                    27 / 17 / 14 / 11.4 / 10.3*
+//   x [16, 7168], 2 x 4096                    42 / 24 / 21 / 15.4 / 14.2*
+//   x [64, 2048], 32 x 256                    18 / 12 / 10.8 / 9.9 / 8.5*
+//   x [128, 7168], 1 x 4096                   42 / 26 / 21 / 15.5* / 17.1
+//   x [128, 7168], 256 x 4096                356 / 286 / 286 / 245* / 291
+//   x [128, 7168], 128 of 256 groups x 4096  406 / 324 / 325 / 277* / 331 (32 rows, weights
+//                                            through the caches: 325)
+//   x [1024, 7168], 1 x 4096                  46 / 30 / 27* / 52 / 85
+//   x [2048, 2048], 64 x 2816                 48 / 38 / 37* / 45 / 69
+//   x [2048, 4096], 1 x 4096                  33 / 27* / 30 / 59 / 97
+//   x [1024, 4096], 16 x 4096                 33 / 29* / 34 / 44 / 68
+//   x [2048, 7168], 32 x 4096                118 / 99* / 111 / 154 / 243
+//   x [4096, 7168], 32 x 4096                130 / 132* / 150 / 236 / 421
+//   x [8192, 7168], 32 x 4096                195 / 180* / 242 / 430 / 818
+//   x [8192, 7168], 32 x 4096, Zipf loads    191 / 182* / 242 / 432 / 811
+//   x [8192, 7168], 1 x 4096                 129* / 130 / 167 / 375 / 720
+//   x [24576, 2048], 64 x 2816               129* / 129 / 163 / 296 / 515
+//   x [28240, 843], 5 x 1497                  57* / 61 / 71 / 154 / 246
+// and where it is wrong:
+//   x [6, 2048], 6 x 1408                     18 / 12 / 10.8 / 9.2* / 8.3
+//   x [8, 2048], 8 x 2816                     18 / 12 / 10.9* / 9.8 / 10.5
+//   x [8, 7168], 8 x 4096                     43 / 26 / 23* / 21 / 26
+//   x [512, 2048], 8 x 1408                   18 / 13.5 / 11.9* / 10.1 / 12.9
+//   x [800, 4096], 2 x 4096                   31 / 21* / 18 / 34 / 51
+//   x [2048, 7168], 32 x 4096, Zipf loads    154 / 119* / 108 / 151 / 248
 enum Mx4Tile { kTile256, kTile128, kTile64, kTile32, kTileThin };
 constexpr int kThin = 32;  // rows and columns of kTileThin
 
